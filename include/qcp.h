@@ -20,8 +20,8 @@
  *
  * Conventions shared by every entry point
  *  - Pointers are device pointers (HBM), except where a comment says otherwise.
- *    The caller allocates and frees every buffer; the library allocates nothing,
- *    keeps no pointer after returning and holds no mutable global state.
+ *    The caller allocates and frees every buffer; the library allocates no device
+ *    memory, keeps no pointer after returning and holds no mutable global state.
  *  - `stream` is a hipStream_t (NULL = the legacy default stream).  Every call
  *    enqueues its kernel(s) on `stream` and returns without synchronizing; the
  *    status reports argument validation and launch errors only.
@@ -62,7 +62,8 @@ typedef enum {
     QCP_EINVAL = -1,        /* bad size, G, b, format, dtype, stride, null or overlapping pointer */
     QCP_EALIGN = -2,        /* a pointer or stride is not a multiple of 16 bytes */
     QCP_EUNSUPPORTED = -3,  /* a combination this library does not implement */
-    QCP_EHIP = -4           /* the HIP runtime reported an error at launch */
+    QCP_EHIP = -4,          /* the HIP runtime reported an error at launch */
+    QCP_ENOMEM = -5         /* no host memory for a call's table of tensors (adamw_step) */
 } qcp_status;
 
 typedef enum { QCP_F16 = 1, QCP_BF16 = 2, QCP_F32 = 3 } qcp_dtype;
@@ -195,6 +196,47 @@ int reorder_quantize(const void *x, int xt, int64_t n, int32_t n_nodes, int32_t 
  */
 int fp8_accum_requant(uint8_t *state_codes, float *state_scales, const void *grad, int gt,
                       int64_t n, int32_t G, void *stream);
+
+/*
+ * AdamW over the tensors of an optimizer shard, in place: the step between the
+ * gradient reduce-scatter (whose last reduce leaves fp32 sums, sum_out above)
+ * and the weight all-gather.  For every element, in fp32, with
+ * g = grad * grad_scale, t = step:
+ *   m <- beta1*m + (1-beta1)*g         v <- beta2*v + (1-beta2)*g^2
+ *   p <- p*(1 - lr*weight_decay) - lr/(1-beta1^t) * m / (sqrt(v)/sqrt(1-beta2^t) + eps)
+ *   params    host array of n_tensors pointers to fp32 elements (4-byte aligned)
+ *   grads     host array of pointers to elements of type gt, aligned to them
+ *   copies    null, or a host array of pointers that receive p rounded to the
+ *             16-bit type ct (QCP_F16 or QCP_BF16), 2-byte aligned
+ *   sizes, offsets   host arrays: elements of each tensor, and the place of its
+ *             first element in the moments: a multiple of G, ascending, each
+ *             tensor's ceil(size/G)*G places apart from the next one's
+ *   state     QCP_F32: m and v hold n_state fp32 values; the scales are ignored.
+ *             QCP_E4M3: m and v hold n_state codes of m and of sqrt(v) with
+ *             one fp32 scale per G (value = code * scale).  The scale is 2^k, the
+ *             smallest k >= -126 at which the block's absmax is at most
+ *             448 * 2^k; a block of zeros has scale +0.  A value is rounded to one
+ *             of its two neighbours at random: up in magnitude when its fraction of
+ *             their distance plus u/2^16 reaches 1, where u is 16 bits of a hash of
+ *             (place, step, seed): the low half for m, the high half for sqrt(v).
+ *             A positive sqrt(v) never becomes 0.  All zeros is the state before
+ *             the first step.  Places that pad a tensor's last block stay 0.
+ *   step >= 1; lr, weight_decay >= 0; 0 <= beta1, beta2 < 1; eps > 0
+ *   grad_scale   null (1), or a device pointer to one fp32 factor: the clipping
+ *             or unscaling factor, read when the kernel runs
+ *   seed      of the hash; unused with QCP_F32
+ * The host arrays are read before the call returns.  m, v and the scales are
+ * 16-byte aligned.  At most QCP_ADAMW_MAX_TENSORS tensors; tensors without
+ * elements are skipped.  No two buffers overlap, except that gradients may.
+ * One kernel launch per 64 tensors.  Errors: QCP_EINVAL, QCP_EALIGN, QCP_ENOMEM,
+ * QCP_EHIP.
+ */
+#define QCP_ADAMW_MAX_TENSORS 65536
+int adamw_step(float *const *params, const void *const *grads, void *const *copies,
+               const int64_t *sizes, const int64_t *offsets, int32_t n_tensors, int gt, int ct,
+               int state, void *m, float *m_scales, void *v, float *v_scales, int64_t n_state,
+               int32_t G, int64_t step, double lr, double beta1, double beta2, double eps,
+               double weight_decay, const float *grad_scale, uint64_t seed, void *stream);
 
 /* Payload bytes of n codes at `bits` bits with one fp32 scale per G elements:
  * ceil(n*bits/8) + 4*ceil(n/G); -1 for invalid arguments.  Host only. */

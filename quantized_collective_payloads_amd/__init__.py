@@ -16,6 +16,7 @@ Functions (same names as the C entry points):
                            n_slices, slice_len, G, fmt_in, fmt_out, ...)
                                                        -> (codes, scales[, sums])
     fp8_accum_requant(state_codes, state_scales, grad, G)   (in place)
+    AdamW(params, copies, state, G), adamw_step(optimizer, grads, step, lr, ...)
     payload_bytes(n, bits, G)
 """
 from __future__ import annotations
@@ -27,14 +28,15 @@ import torch
 
 __all__ = ["quantize_blockwise", "dequantize_blockwise", "pack_subbyte", "unpack_subbyte",
            "dequant_reduce_requant", "fp8_accum_requant", "payload_bytes", "code_bytes",
-           "n_blocks", "QcpError", "library", "FORMATS", "DTYPES", "LIB_PATH"]
+           "n_blocks", "AdamW", "adamw_step", "QcpError", "library", "FORMATS", "DTYPES", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqcp.so")
 
 # numbering of include/qcp.h
 DTYPES = {torch.float16: 1, torch.bfloat16: 2, torch.float32: 3}
 FORMATS = {"int2": 2, "int4": 4, "int6": 6, "int8": 8, "e4m3": 0x43}
-_STATUS = {0: "QCP_OK", -1: "QCP_EINVAL", -2: "QCP_EALIGN", -3: "QCP_EUNSUPPORTED", -4: "QCP_EHIP"}
+_STATUS = {0: "QCP_OK", -1: "QCP_EINVAL", -2: "QCP_EALIGN", -3: "QCP_EUNSUPPORTED", -4: "QCP_EHIP",
+           -5: "QCP_ENOMEM"}
 
 _lib = None
 
@@ -54,6 +56,7 @@ def library():
                               "`python -m quantized_collective_payloads_amd.build`")
         lib = ctypes.CDLL(LIB_PATH)
         p, i64, i32, ci = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int
+        f64 = ctypes.c_double
         sig = {
             "quantize_blockwise": [p, ci, i64, i32, ci, p, p, p],
             "dequantize_blockwise": [p, p, ci, i64, i32, p, ci, p],
@@ -64,6 +67,8 @@ def library():
             "reorder_quantize": [p, ci, i64, i32, i32, i32, ci, p, i64, p, i64, p],
             "pack_subbyte_records": [p, ci, i64, i32, i32, p, p],
             "unpack_subbyte_records": [p, i64, i32, i32, p, ci, p],
+            "adamw_step": [p, p, p, p, p, i32, ci, ci, ci, p, p, p, p, i64, i32, i64, f64, f64, f64,
+                           f64, f64, p, ctypes.c_uint64, p],
             "qcp_aquavit_level": [i64, i64, ctypes.c_double, ctypes.c_double,
                                   ctypes.POINTER(i32), ctypes.POINTER(i32)],
         }
@@ -374,3 +379,6 @@ def fp8_accum_requant(state_codes: torch.Tensor, state_scales: torch.Tensor, gra
             _ptr(state_codes), _ptr(state_scales), _ptr(g), _dtype_code(g.dtype), n, G,
             _stream(dev)))
     return state_codes, state_scales
+
+
+from .optimizer import AdamW, adamw_step  # noqa: E402  (they use the helpers above)

@@ -2,9 +2,13 @@
 //
 // Each entry point validates its arguments on the host (pure checks: no HIP
 // call is made for a rejected call or for n == 0), then enqueues one kernel on
-// the caller's stream and maps a launch error to QCP_EHIP.  Nothing is
-// allocated and no state is kept between calls.
+// the caller's stream (adamw_step one per 64 tensors) and maps a launch error to
+// QCP_EHIP.  No device memory is allocated and no state is kept between calls.
+#include <math.h>
 #include <stdint.h>
+
+#include <algorithm>
+#include <new>
 
 #include "qcp.h"
 #include "qcp_launch.h"
@@ -36,6 +40,26 @@ bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
 }
 
 int status_of(hipError_t e) { return e == hipSuccess ? QCP_OK : QCP_EHIP; }
+
+// a range of memory that a call touches
+struct Range {
+    uintptr_t at, end;
+    bool written;
+};
+
+// does any written range meet another one?  The ranges are sorted by where they
+// begin; then a range meets an earlier one exactly if it begins before the
+// furthest end so far (of all ranges, or of the written ones if it is only read).
+bool ranges_clash(Range *r, int64_t n) {
+    std::sort(r, r + n, [](const Range &a, const Range &b) { return a.at < b.at; });
+    uintptr_t all = 0, written = 0;
+    for (int64_t i = 0; i < n; i++) {
+        if (r[i].at < (r[i].written ? all : written)) return true;
+        all = std::max(all, r[i].end);
+        if (r[i].written) written = std::max(written, r[i].end);
+    }
+    return false;
+}
 
 int check_common(int64_t n, int32_t G) {
     if (n < 0 || n > kMaxElems) return QCP_EINVAL;
@@ -187,6 +211,94 @@ int fp8_accum_requant(uint8_t *state_codes, float *state_scales, const void *gra
                                        (hipStream_t)stream));
 }
 
+int adamw_step(float *const *params, const void *const *grads, void *const *copies,
+               const int64_t *sizes, const int64_t *offsets, int32_t n_tensors, int gt, int ct,
+               int state, void *m, float *m_scales, void *v, float *v_scales, int64_t n_state,
+               int32_t G, int64_t step, double lr, double beta1, double beta2, double eps,
+               double weight_decay, const float *grad_scale, uint64_t seed, void *stream) {
+    if (n_tensors < 0 || n_tensors > QCP_ADAMW_MAX_TENSORS || n_state < 0 || !valid_g(G)) return QCP_EINVAL;
+    if (!valid_dtype(gt) || (state != QCP_F32 && state != QCP_E4M3)) return QCP_EINVAL;
+    if (copies && ct != QCP_F16 && ct != QCP_BF16) return QCP_EINVAL;
+    const bool scalars = step >= 1 && isfinite(lr) && lr >= 0 && beta1 >= 0 && beta1 < 1 && beta2 >= 0 &&
+                         beta2 < 1 && isfinite(eps) && (float)eps > 0 && isfinite(weight_decay) &&
+                         weight_decay >= 0;
+    if (!scalars) return QCP_EINVAL;
+    if (n_tensors == 0) return QCP_OK;
+    if (!params || !grads || !sizes || !offsets) return QCP_EINVAL;
+    const bool eight = state == QCP_E4M3;
+    int64_t past = 0;                                       // end of the last tensor's blocks
+    int32_t live = 0;
+    for (int32_t i = 0; i < n_tensors; i++) {
+        const int64_t n = sizes[i];
+        if (n < 0 || n > kMaxElems) return QCP_EINVAL;
+        if (offsets[i] < past || offsets[i] % G != 0) return QCP_EINVAL;
+        if (offsets[i] > n_state || n_blocks(n, G) > (n_state - offsets[i]) / G) return QCP_EINVAL;
+        past = offsets[i] + n_blocks(n, G) * G;
+        if (n == 0) continue;
+        live++;
+        if (!params[i] || !grads[i] || (copies && !copies[i])) return QCP_EINVAL;
+        if ((uintptr_t)params[i] % 4 || (uintptr_t)grads[i] % dtype_bytes(gt)) return QCP_EALIGN;
+        if (copies && (uintptr_t)copies[i] % 2) return QCP_EALIGN;
+    }
+    if (live == 0) return QCP_OK;
+    if (!m || !v || (eight && (!m_scales || !v_scales))) return QCP_EINVAL;
+    if (!aligned16(m) || !aligned16(v)) return QCP_EALIGN;
+    if (eight && (!aligned16(m_scales) || !aligned16(v_scales))) return QCP_EALIGN;
+    if ((uintptr_t)grad_scale % 4) return QCP_EALIGN;
+
+    qcp::AdamwTensor *t = new (std::nothrow) qcp::AdamwTensor[live];
+    Range *r = new (std::nothrow) Range[3 * (int64_t)live + 5];
+    int rc = t && r ? QCP_OK : QCP_ENOMEM;
+    if (rc == QCP_OK) {
+        int64_t k = 0, at = 0;
+        auto range = [&](const void *p, int64_t bytes, bool written) {
+            if (p && bytes > 0) r[k++] = Range{(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, written};
+        };
+        for (int32_t i = 0; i < n_tensors; i++) {
+            const int64_t n = sizes[i];
+            if (n == 0) continue;
+            void *copy = copies ? copies[i] : nullptr;
+            t[at++] = qcp::AdamwTensor{params[i], grads[i], copy, n, offsets[i]};
+            range(params[i], 4 * n, true);
+            range(grads[i], n * dtype_bytes(gt), false);
+            range(copy, 2 * n, true);
+        }
+        range(m, eight ? past : 4 * past, true);
+        range(v, eight ? past : 4 * past, true);
+        if (eight) {
+            range(m_scales, past / G * 4, true);
+            range(v_scales, past / G * 4, true);
+        }
+        range(grad_scale, 4, false);
+        if (ranges_clash(r, k)) rc = QCP_EINVAL;
+    }
+    if (rc == QCP_OK) {
+        uint32_t key = 0;
+        for (uint32_t word : {(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)step, (uint32_t)((uint64_t)step >> 32)})
+            key = qcp::adamw_mix(key + word + 0x9e3779b9u);
+        qcp::AdamwConst c = {};
+        c.m = m;
+        c.v = v;
+        c.m_scales = m_scales;
+        c.v_scales = v_scales;
+        c.grad_scale = grad_scale;
+        c.beta1 = (float)beta1;
+        c.one_beta1 = (float)(1 - beta1);
+        c.beta2 = (float)beta2;
+        c.one_beta2 = (float)(1 - beta2);
+        c.decay = (float)(1 - lr * weight_decay);
+        c.step_size = (float)(lr / (1 - pow(beta1, (double)step)));
+        c.root_scale = (float)(1 / sqrt(1 - pow(beta2, (double)step)));
+        c.eps = (float)eps;
+        c.key = key;
+        c.copy_type = ct;
+        rc = status_of(qcp::launch_adamw(t, live, gt, state, G, c, (hipStream_t)stream));
+    }
+    delete[] t;
+    delete[] r;
+    return rc;
+}
+
 int64_t qcp_payload_bytes(int64_t n, int32_t bits, int32_t G) {
     if (n < 0 || G < 1 || bits < 1 || bits > 32) return -1;
     return (n * bits + 7) / 8 + 4 * ((n + G - 1) / G);
@@ -225,6 +337,7 @@ const char *qcp_strerror(int status) {
     case QCP_EINVAL: return "invalid argument (size, block size, bit width, format, dtype, stride, null or overlapping buffer)";
     case QCP_EALIGN: return "pointer or stride not aligned to 16 bytes";
     case QCP_EUNSUPPORTED: return "unsupported combination";
+    case QCP_ENOMEM: return "out of host memory";
     case QCP_EHIP: return "HIP runtime error at kernel launch";
     default: return "unknown status";
     }

@@ -40,6 +40,39 @@ hipError_t launch_reduce(const uint8_t *codes_in, int64_t slice_stride, const fl
 hipError_t launch_accum(uint8_t *state_codes, float *state_scales, const void *grad, int gt,
                         int64_t n, int G, hipStream_t st);
 
+// AdamW over n tensors (tensors without elements left out); see qcp_adamw.hip
+struct AdamwTensor {
+    float *param;
+    const void *grad;
+    void *copy;            // null: no 16-bit copy
+    int64_t n;
+    int64_t offset;        // first element's place in the moments
+};
+struct AdamwConst {
+    void *m, *v;           // fp32, or E4M3 codes of m and sqrt(v)
+    float *m_scales, *v_scales;
+    const float *grad_scale;
+    float beta1, one_beta1, beta2, one_beta2, decay, step_size, root_scale, eps;
+    uint32_t key;
+    int copy_type;
+};
+template <int CAP> struct AdamwTable {
+    AdamwTensor t[CAP];
+    uint32_t first[CAP];   // first work-group of each tensor; ~0 past the last
+};
+hipError_t launch_adamw(const AdamwTensor *t, int n, int gt, int state, int G, const AdamwConst &c,
+                        hipStream_t st);
+
+// the counter hash of the stochastic rounding: an invertible scramble of 32 bits
+// (two rounds of xor-shift and an odd multiplier, the fractions of sqrt 2 and sqrt 3)
+__host__ __device__ inline uint32_t adamw_mix(uint32_t x) {
+    x ^= x >> 16;
+    x *= 0x6a09e667u;
+    x ^= x >> 15;
+    x *= 0xbb67ae85u;
+    return x ^ (x >> 16);
+}
+
 // workgroups of 4 waves; each kernel derives its wave index from the
 // work-group and work-item ids
 constexpr int kThreads = 256;
