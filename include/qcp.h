@@ -238,6 +238,51 @@ int adamw_step(float *const *params, const void *const *grads, void *const *copi
                int32_t G, int64_t step, double lr, double beta1, double beta2, double eps,
                double weight_decay, const float *grad_scale, uint64_t seed, void *stream);
 
+/*
+ * The MXFP4 payload of a matrix (OCP Microscaling: E2M1 codes, one E8M0 scale per
+ * 32): 4.25 bits per weight, which the matrix cores multiply as it is
+ * (mxfp4_matmul).  A payload of `lines` rows of n values holds each row padded
+ * with zeros to P = qcp_mxfp4_padded(n) values (whole 128s):
+ *   codes    lines x P/2 bytes; value 2i of a row in the low four bits of its
+ *            byte i, value 2i+1 in the high ones; sign, 2 exponent bits, 1 mantissa
+ *            bit: +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}
+ *   scales   lines x P/32 bytes: e stands for 2^(e-127), 255 for NaN
+ * Quantize: E = exponent field of a block's fp32 absmax, e = max(E - 2, 0); a code
+ * is the value nearest to x * 2^(127-e), ties to the even code, 6 beyond, the sign
+ * of zero kept.  A block with an infinity or a NaN has e = 255 and unspecified
+ * codes.
+ *   x          rows x cols elements of type xt (aligned to them), rows ld
+ *              elements apart, ld >= cols
+ *   transpose  0: the payload of x (lines = rows, blocks along its rows);
+ *              1: the payload of x^T (lines = cols, blocks along its columns)
+ * Dequantize: y (rows x cols of type yt, rows ld apart) is code * 2^(e-127) rounded
+ * once to yt.
+ *   codes, scales   16-byte aligned; lines * P <= qcp_max_elements(), n <= 2^31
+ * Errors: QCP_EINVAL, QCP_EALIGN, QCP_EHIP.
+ */
+int mxfp4_quantize(const void *x, int xt, int64_t rows, int64_t cols, int64_t ld, int32_t transpose,
+                   uint8_t *codes, uint8_t *scales, void *stream);
+int mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *y,
+                     int yt, int64_t ld, void *stream);
+
+/*
+ * Product of two MXFP4 payloads: c[m, n] = sum over k of a[m, k] * b[n, k],
+ * accumulated in fp32 and rounded once to type ct (rows ldc elements apart).
+ *   a_codes, a_scales   the payload of A, M rows of K values
+ *   b_codes, b_scales   the payload of B, N rows of K values (a weight stored as
+ *                       [out, in], as the forward pass has it)
+ * K = 0 gives zeros.  A scale of 255 makes its row (or column) of c NaN.  Forward,
+ * y = x W^T: A = x, B = W.  Backward: dx = dy W takes the payloads of dy and of
+ * W^T, dW = dy^T x those of dy^T and x^T (transpose = 1).
+ */
+int mxfp4_matmul(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *b_codes,
+                 const uint8_t *b_scales, int64_t M, int64_t N, int64_t K, void *c, int ct, int64_t ldc,
+                 void *stream);
+
+/* n rounded up to whole 128s, the row length of an MXFP4 payload; -1 if n is
+ * negative or above qcp_max_elements().  Host only. */
+int64_t qcp_mxfp4_padded(int64_t n);
+
 /* Payload bytes of n codes at `bits` bits with one fp32 scale per G elements:
  * ceil(n*bits/8) + 4*ceil(n/G); -1 for invalid arguments.  Host only. */
 int64_t qcp_payload_bytes(int64_t n, int32_t bits, int32_t G);

@@ -17,6 +17,10 @@ Functions (same names as the C entry points):
                                                        -> (codes, scales[, sums])
     fp8_accum_requant(state_codes, state_scales, grad, G)   (in place)
     AdamW(params, copies, state, G), adamw_step(optimizer, grads, step, lr, ...)
+    mxfp4_quantize(x, transpose)                       -> (codes, scales)
+    mxfp4_dequantize(codes, scales, cols, dtype)       -> y
+    mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, dtype) -> A B^T
+    mxfp4_linear(x, weight)                            -> y (differentiable)
     payload_bytes(n, bits, G)
 """
 from __future__ import annotations
@@ -28,7 +32,8 @@ import torch
 
 __all__ = ["quantize_blockwise", "dequantize_blockwise", "pack_subbyte", "unpack_subbyte",
            "dequant_reduce_requant", "fp8_accum_requant", "payload_bytes", "code_bytes",
-           "n_blocks", "AdamW", "adamw_step", "QcpError", "library", "FORMATS", "DTYPES", "LIB_PATH"]
+           "n_blocks", "AdamW", "adamw_step", "mxfp4_quantize", "mxfp4_dequantize",
+           "mxfp4_matmul", "mxfp4_linear", "mxfp4_padded", "QcpError", "library", "FORMATS", "DTYPES", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqcp.so")
 
@@ -69,6 +74,9 @@ def library():
             "unpack_subbyte_records": [p, i64, i32, i32, p, ci, p],
             "adamw_step": [p, p, p, p, p, i32, ci, ci, ci, p, p, p, p, i64, i32, i64, f64, f64, f64,
                            f64, f64, p, ctypes.c_uint64, p],
+            "mxfp4_quantize": [p, ci, i64, i64, i64, i32, p, p, p],
+            "mxfp4_dequantize": [p, p, i64, i64, p, ci, i64, p],
+            "mxfp4_matmul": [p, p, p, p, i64, i64, i64, p, ci, i64, p],
             "qcp_aquavit_level": [i64, i64, ctypes.c_double, ctypes.c_double,
                                   ctypes.POINTER(i32), ctypes.POINTER(i32)],
         }
@@ -80,6 +88,8 @@ def library():
         lib.qcp_aquavit_target.restype = ctypes.c_double
         lib.qcp_payload_bytes.argtypes = [i64, i32, i32]
         lib.qcp_payload_bytes.restype = i64
+        lib.qcp_mxfp4_padded.argtypes = [i64]
+        lib.qcp_mxfp4_padded.restype = i64
         lib.qcp_strerror.argtypes = [ci]
         lib.qcp_strerror.restype = ctypes.c_char_p
         lib.qcp_version.argtypes = []
@@ -381,4 +391,7 @@ def fp8_accum_requant(state_codes: torch.Tensor, state_scales: torch.Tensor, gra
     return state_codes, state_scales
 
 
-from .optimizer import AdamW, adamw_step  # noqa: E402  (they use the helpers above)
+# these modules use the helpers above
+from .mxfp4 import (mxfp4_dequantize, mxfp4_linear, mxfp4_matmul, mxfp4_padded,  # noqa: E402
+                    mxfp4_quantize)
+from .optimizer import AdamW, adamw_step  # noqa: E402

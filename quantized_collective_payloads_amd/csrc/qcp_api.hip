@@ -67,6 +67,26 @@ int check_common(int64_t n, int32_t G) {
     return QCP_OK;
 }
 
+// a matrix of rows x cols elements with ld elements between rows: its bytes from
+// the first element to the last
+int check_matrix(int64_t rows, int64_t cols, int64_t ld, int t, int64_t *bytes) {
+    if (rows < 0 || cols < 0 || rows > kMaxElems || cols > kMaxElems || !valid_dtype(t)) return QCP_EINVAL;
+    if (ld < cols || ld > kMaxElems) return QCP_EINVAL;
+    *bytes = 0;
+    if (rows == 0 || cols == 0) return QCP_OK;
+    if (rows > 1 && ld > 0 && (rows - 1) > (INT64_MAX / 8 - cols) / ld) return QCP_EINVAL;
+    *bytes = ((rows - 1) * ld + cols) * dtype_bytes(t);
+    return QCP_OK;
+}
+
+// a payload of `lines` rows of n values: the padded row length.  Rows of at most
+// 2^31 values keep every position within a row in 32 bits and the column-wise
+// quantize's grid (one work-group per 256 x 64 values) within one launch.
+bool mx_payload(int64_t lines, int64_t n, int64_t *pad) {
+    *pad = (n + 127) / 128 * 128;
+    return *pad == 0 || (n <= (int64_t)1 << 31 && lines <= kMaxElems / *pad);
+}
+
 }  // namespace
 
 extern "C" {
@@ -298,6 +318,60 @@ int adamw_step(float *const *params, const void *const *grads, void *const *copi
     delete[] r;
     return rc;
 }
+
+int mxfp4_quantize(const void *x, int xt, int64_t rows, int64_t cols, int64_t ld, int32_t transpose,
+                   uint8_t *codes, uint8_t *scales, void *stream) {
+    int64_t xb, pad;
+    int rc = check_matrix(rows, cols, ld, xt, &xb);
+    if (rc != QCP_OK) return rc;
+    if (transpose != 0 && transpose != 1) return QCP_EINVAL;
+    if (rows == 0 || cols == 0) return QCP_OK;
+    const int64_t lines = transpose ? cols : rows;
+    if (!mx_payload(lines, transpose ? rows : cols, &pad)) return QCP_EINVAL;
+    if (!x || !codes || !scales) return QCP_EINVAL;
+    if ((uintptr_t)x % dtype_bytes(xt) || !aligned16(codes) || !aligned16(scales)) return QCP_EALIGN;
+    const int64_t cb = lines * pad / 2, sb = lines * pad / 32;
+    if (overlap(x, xb, codes, cb) || overlap(x, xb, scales, sb) || overlap(codes, cb, scales, sb))
+        return QCP_EINVAL;
+    return status_of(qcp::launch_mx_quantize(x, xt, rows, cols, ld, transpose, codes, scales,
+                                             (hipStream_t)stream));
+}
+
+int mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *y,
+                     int yt, int64_t ld, void *stream) {
+    int64_t yb, pad;
+    int rc = check_matrix(rows, cols, ld, yt, &yb);
+    if (rc != QCP_OK) return rc;
+    if (rows == 0 || cols == 0) return QCP_OK;
+    if (!mx_payload(rows, cols, &pad)) return QCP_EINVAL;
+    if (!codes || !scales || !y) return QCP_EINVAL;
+    if (!aligned16(codes) || !aligned16(scales) || (uintptr_t)y % dtype_bytes(yt)) return QCP_EALIGN;
+    if (overlap(y, yb, codes, rows * pad / 2) || overlap(y, yb, scales, rows * pad / 32)) return QCP_EINVAL;
+    return status_of(qcp::launch_mx_dequantize(codes, scales, rows, cols, y, yt, ld, (hipStream_t)stream));
+}
+
+int mxfp4_matmul(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *b_codes,
+                 const uint8_t *b_scales, int64_t M, int64_t N, int64_t K, void *c, int ct, int64_t ldc,
+                 void *stream) {
+    int64_t cb, pad;
+    int rc = check_matrix(M, N, ldc, ct, &cb);
+    if (rc != QCP_OK) return rc;
+    if (K < 0) return QCP_EINVAL;
+    if (M == 0 || N == 0) return QCP_OK;
+    if (!mx_payload(M, K, &pad) || !mx_payload(N, K, &pad)) return QCP_EINVAL;
+    if ((M + 127) / 128 > qcp::kMaxGroups / ((N + 127) / 128)) return QCP_EINVAL;   // tiles of C
+    if (!c || (K > 0 && (!a_codes || !a_scales || !b_codes || !b_scales))) return QCP_EINVAL;
+    if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(b_codes) || !aligned16(b_scales) ||
+        (uintptr_t)c % dtype_bytes(ct))
+        return QCP_EALIGN;
+    if (overlap(c, cb, a_codes, M * pad / 2) || overlap(c, cb, a_scales, M * pad / 32) ||
+        overlap(c, cb, b_codes, N * pad / 2) || overlap(c, cb, b_scales, N * pad / 32))
+        return QCP_EINVAL;
+    return status_of(qcp::launch_mx_matmul(a_codes, a_scales, b_codes, b_scales, M, N, pad / 128, c, ct,
+                                           ldc, (hipStream_t)stream));
+}
+
+int64_t qcp_mxfp4_padded(int64_t n) { return n < 0 || n > kMaxElems ? -1 : (n + 127) / 128 * 128; }
 
 int64_t qcp_payload_bytes(int64_t n, int32_t bits, int32_t G) {
     if (n < 0 || G < 1 || bits < 1 || bits > 32) return -1;

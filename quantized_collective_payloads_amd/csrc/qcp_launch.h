@@ -63,6 +63,17 @@ template <int CAP> struct AdamwTable {
 hipError_t launch_adamw(const AdamwTensor *t, int n, int gt, int state, int G, const AdamwConst &c,
                         hipStream_t st);
 
+// the MXFP4 payload of x (transpose: of x^T), and back; see qcp_mxfp4.hip
+hipError_t launch_mx_quantize(const void *x, int xt, int64_t rows, int64_t cols, int64_t ld,
+                              int transpose, uint8_t *codes, uint8_t *scales, hipStream_t st);
+hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,
+                                int64_t cols, void *y, int yt, int64_t ld, hipStream_t st);
+
+// C[M, N] = A B^T, rows of `granules` times 128 values; see qcp_mxfp4_matmul.hip
+hipError_t launch_mx_matmul(const uint8_t *a, const uint8_t *as, const uint8_t *b, const uint8_t *bs,
+                            int64_t M, int64_t N, int64_t granules, void *c, int ct, int64_t ldc,
+                            hipStream_t st);
+
 // the counter hash of the stochastic rounding: an invertible scramble of 32 bits
 // (two rounds of xor-shift and an odd multiplier, the fractions of sqrt 2 and sqrt 3)
 __host__ __device__ inline uint32_t adamw_mix(uint32_t x) {

@@ -1,0 +1,408 @@
+// qcp_mxfp4.hip -- the MXFP4 payload: quantize along the rows or along the
+// columns of a matrix, and dequantize.
+//
+// A block is 32 values of one payload row.  With E the exponent field of the
+// block's fp32 absmax, the scale byte is e = max(E - 2, 0) (the OCP MX rule: the
+// largest E2M1 value is 6 = 1.5 * 2^2), and a code is x * 2^(127-e) rounded to the
+// nearest of {0, 0.5, 1, 1.5, 2, 3, 4, 6}, ties to the even code, 6 beyond, sign
+// kept.  gfx950's v_cvt_scalef32_pk_fp4_* does exactly that from fp32, bf16 and
+// fp16, two values an instruction, and v_cvt_scalef32_pk_*_fp4 the way back.  A
+// block with an infinity or a NaN has e = 255 and dequantizes to NaN throughout.
+//
+// A payload row holds its values padded with zeros to whole 128s: 64 code bytes
+// and 4 scale bytes per 128, so every row of codes starts on 64 bytes, every row
+// of scales on 4, and the matrix instructions never see a short block.
+//
+// Bound: HBM; 2 + 0.53 bytes per 16-bit value for a few instructions.
+//
+// Along the rows: a lane owns 8 consecutive values (one 16-byte load of 16-bit
+// input, one dword of codes), so a block is 4 lanes and its absmax two DPP steps,
+// on the 16-bit patterns where the input has them.  Output positions are the same
+// whether rows are padded or not: vector i of the padded matrix has its codes at
+// byte 4i.  A matrix that is one run of whole 128s needs no row arithmetic (FLAT).
+//
+// Along the columns: a work-group takes 256 rows x 64 columns.  A lane owns two
+// neighbouring columns of 32 rows, so its two blocks need no other lane: absmax,
+// scale and codes all come from its own registers.  One input row of the tile and
+// one output row are both 128 bytes; the codes pass through LDS to be stored so.
+#include "qcp_device.h"
+#include "qcp_launch.h"
+
+namespace qcp {
+
+namespace {
+
+typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+typedef u32x4_t u32x4_any __attribute__((aligned(2)));     // at an element's alignment
+typedef unsigned int u32_any __attribute__((aligned(2)));
+typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+typedef u32x2_t u32x2_any __attribute__((aligned(4)));
+
+constexpr int kMxPad = 128;       // values of a row's granule
+constexpr int kMxVecs = 4;        // vectors of 8 values per lane
+
+template <int XT> constexpr int words8() { return XT == F32 ? 8 : 4; }   // dwords of 8 values
+
+// 8 values from p, of which `count` exist (the others are zero)
+template <int XT>
+__device__ __forceinline__ void load8(const void *x, int64_t i, int count, uint32_t (&w)[words8<XT>()]) {
+    constexpr int B = dtype_traits<XT>::bytes;
+    const uint8_t *p = (const uint8_t *)x + i * B;
+    if (count >= 8) {
+#pragma unroll
+        for (int k = 0; k < words8<XT>() / 4; k++) {
+            const u32x4_any v = *((const u32x4_any *)p + k);
+            w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < words8<XT>(); k++) {
+            if constexpr (XT == F32) {
+                w[k] = k < count ? *(const uint32_t *)(p + 4 * k) : 0;
+            } else {
+                const uint32_t lo = 2 * k < count ? *(const uint16_t *)(p + 4 * k) : 0;
+                const uint32_t hi = 2 * k + 1 < count ? *(const uint16_t *)(p + 4 * k + 2) : 0;
+                w[k] = lo | (hi << 16);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    const u16x2_t m = __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a), __builtin_bit_cast(u16x2_t, b));
+    return __builtin_bit_cast(uint32_t, m);
+}
+
+// |x| maximum of one or two values' bit patterns: 16-bit types keep two maxima
+template <int XT>
+__device__ __forceinline__ uint32_t absmax_of(uint32_t m, uint32_t w) {
+    if constexpr (XT == F32) return max(m, w & 0x7fffffffu);
+    else return max_u16x2(m, w & 0x7fff7fffu);
+}
+
+// scale byte from the absmax of a block
+template <int XT>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t m) {
+    uint32_t field;
+    if constexpr (XT == F32) {
+        field = m >> 23;
+    } else {
+        m = max(m & 0xffffu, m >> 16);
+        field = XT == BF16 ? m >> 7 : __float_as_uint(f16_lo(m)) >> 23;
+    }
+    return field == 255u ? 255u : field < 2u ? 0u : field - 2u;
+}
+
+// 2^(e-127); 2^-127 is a subnormal
+__device__ __forceinline__ float scale_of(uint32_t e) {
+    return __uint_as_float(e == 0 ? 0x00400000u : e << 23);
+}
+
+// two values -> two codes in byte K of w
+template <int XT, int K>
+__device__ __forceinline__ uint32_t encode2(uint32_t w, uint32_t a, uint32_t b, float s) {
+    if constexpr (XT == F32)
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, __uint_as_float(a), __uint_as_float(b), s, K);
+    else if constexpr (XT == BF16)
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2_t, a), s, K);
+    else
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(w, __builtin_bit_cast(f16x2_t, a), s, K);
+}
+
+template <int XT>
+__device__ __forceinline__ uint32_t encode8(const uint32_t (&w)[words8<XT>()], float s) {
+    uint32_t c = 0;
+    if constexpr (XT == F32) {
+        c = encode2<XT, 0>(c, w[0], w[1], s);
+        c = encode2<XT, 1>(c, w[2], w[3], s);
+        c = encode2<XT, 2>(c, w[4], w[5], s);
+        c = encode2<XT, 3>(c, w[6], w[7], s);
+    } else {
+        c = encode2<XT, 0>(c, w[0], 0, s);
+        c = encode2<XT, 1>(c, w[1], 0, s);
+        c = encode2<XT, 2>(c, w[2], 0, s);
+        c = encode2<XT, 3>(c, w[3], 0, s);
+    }
+    return c;
+}
+
+// where the wave's vectors lie in rows of `width` vectors: the first one's row and
+// column from one division per wave, a lane's from a small one
+struct RowPlace {
+    int64_t row;
+    uint32_t col;     // in vectors
+};
+__device__ __forceinline__ RowPlace place(int64_t row0, uint32_t col0, uint32_t step, uint32_t width) {
+    const uint32_t c = col0 + step, q = c / width;
+    return RowPlace{row0 + q, c - q * width};
+}
+
+template <int XT, bool FLAT>
+__global__ __launch_bounds__(kThreads) void k_mx_quantize(const void *__restrict__ x, int64_t vecs,
+                                                          uint32_t width, int64_t cols, int64_t ld,
+                                                          uint32_t *__restrict__ codes,
+                                                          uint32_t *__restrict__ scales) {
+    const int lane = lane_id();
+    const int64_t v0 = wave_id() * (64 * kMxVecs);
+    if (v0 >= vecs) return;
+    const int64_t row0 = FLAT ? 0 : v0 / width;
+    const uint32_t col0 = FLAT ? 0 : (uint32_t)(v0 - row0 * width);
+    uint32_t w[kMxVecs][words8<XT>()];
+#pragma unroll
+    for (int u = 0; u < kMxVecs; u++) {
+        const int64_t v = v0 + u * 64 + lane;
+        if constexpr (FLAT) {
+            load8<XT>(x, v * 8, v < vecs ? 8 : 0, w[u]);
+        } else {
+            const RowPlace p = place(row0, col0, u * 64 + lane, width);
+            const int64_t left = v < vecs ? cols - (int64_t)p.col * 8 : 0;
+            load8<XT>(x, p.row * ld + (int64_t)p.col * 8, left > 8 ? 8 : left < 0 ? 0 : (int)left, w[u]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kMxVecs; u++) {
+        const int64_t v = v0 + u * 64 + lane;
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < words8<XT>(); k++) m = absmax_of<XT>(m, w[u][k]);
+        m = absmax_of<XT>(m, dpp_u32<0xB1>(m));
+        m = absmax_of<XT>(m, dpp_u32<0x4E>(m));
+        const uint32_t e = scale_byte<XT>(m);
+        const uint32_t c = encode8<XT>(w[u], scale_of(e));
+        // the scale bytes of 4 blocks (16 lanes) in one dword
+        uint32_t d = e << (8 * ((lane >> 2) & 3));
+        d |= dpp_u32<0x141>(d);
+        d |= dpp_u32<0x140>(d);
+        if (v < vecs) {
+            codes[v] = c;
+            if ((lane & 15) == 0) scales[v >> 4] = d;
+        }
+    }
+}
+
+// 8 codes and their scale byte -> 8 values
+template <int YT>
+__device__ __forceinline__ void decode8(uint32_t c, uint32_t e, uint32_t (&w)[words8<YT>()]) {
+    const float s = scale_of(e);
+    static_for<4>([&](auto K) {
+        constexpr int k = K;
+        if constexpr (YT == F32) {
+            const f32x2_t v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, k);
+            w[2 * k] = __float_as_uint(v.x);
+            w[2 * k + 1] = __float_as_uint(v.y);
+        } else if constexpr (YT == BF16) {
+            w[k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, k));
+        } else {
+            w[k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, k));
+        }
+    });
+    constexpr uint32_t nan = YT == F32 ? 0x7fc00000u : YT == BF16 ? 0x7fc07fc0u : 0x7e007e00u;
+#pragma unroll
+    for (int k = 0; k < words8<YT>(); k++) w[k] = e == 255u ? nan : w[k];
+}
+
+template <int YT>
+__device__ __forceinline__ void store8(void *y, int64_t i, int count, const uint32_t (&w)[words8<YT>()]) {
+    constexpr int B = dtype_traits<YT>::bytes;
+    uint8_t *p = (uint8_t *)y + i * B;
+    if (count >= 8) {
+#pragma unroll
+        for (int k = 0; k < words8<YT>() / 4; k++)
+            __builtin_nontemporal_store(u32x4_any{w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]},
+                                        (u32x4_any *)p + k);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            if (j >= count) continue;
+            if constexpr (YT == F32) ((uint32_t *)p)[j] = w[j];
+            else ((uint16_t *)p)[j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+        }
+    }
+}
+
+template <int YT, bool FLAT>
+__global__ __launch_bounds__(kThreads) void k_mx_dequantize(const uint32_t *__restrict__ codes,
+                                                            const uint8_t *__restrict__ scales,
+                                                            int64_t vecs, uint32_t width, int64_t cols,
+                                                            int64_t ld, void *__restrict__ y) {
+    const int lane = lane_id();
+    const int64_t v0 = wave_id() * (64 * kMxVecs);
+    if (v0 >= vecs) return;
+    const int64_t row0 = FLAT ? 0 : v0 / width;
+    const uint32_t col0 = FLAT ? 0 : (uint32_t)(v0 - row0 * width);
+    uint32_t c[kMxVecs], e[kMxVecs];
+#pragma unroll
+    for (int u = 0; u < kMxVecs; u++) {
+        const int64_t v = v0 + u * 64 + lane;
+        c[u] = v < vecs ? codes[v] : 0;
+        e[u] = v < vecs ? scales[v >> 2] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kMxVecs; u++) {
+        const int64_t v = v0 + u * 64 + lane;
+        uint32_t w[words8<YT>()];
+        decode8<YT>(c[u], e[u], w);
+        if constexpr (FLAT) {
+            store8<YT>(y, v * 8, v < vecs ? 8 : 0, w);
+        } else {
+            const RowPlace p = place(row0, col0, u * 64 + lane, width);
+            const int64_t left = v < vecs ? cols - (int64_t)p.col * 8 : 0;
+            store8<YT>(y, p.row * ld + (int64_t)p.col * 8, left > 8 ? 8 : left < 0 ? 0 : (int)left, w);
+        }
+    }
+}
+
+constexpr int kTRows = 256, kTCols = 64;       // tile of the column-wise quantize
+
+template <int XT>
+__global__ __launch_bounds__(kThreads) void k_mx_quantize_t(const void *__restrict__ x, int64_t rows,
+                                                            int64_t cols, int64_t ld, uint32_t col_tiles,
+                                                            int64_t pad_rows, uint8_t *__restrict__ codes,
+                                                            uint8_t *__restrict__ scales) {
+    constexpr int B = dtype_traits<XT>::bytes;
+    constexpr int kLine = 128 + 16;            // bytes per column in LDS: a shift of 4 banks
+    __shared__ __attribute__((aligned(16))) uint8_t lines[kTCols * kLine];
+    __shared__ __attribute__((aligned(8))) uint8_t marks[kTCols * 8];
+    const uint32_t wg = __builtin_amdgcn_workgroup_id_x();
+    const int64_t tr = (int64_t)(wg / col_tiles) * kTRows, tc = (int64_t)(wg % col_tiles) * kTCols;
+    const int tid = (int)__builtin_amdgcn_workitem_id_x();
+    const int block = tid >> 5;                // which 32 rows of the tile
+    const int pair = tid & 31;                 // which two columns
+    const int64_t r0 = tr + block * 32, c0 = tc + pair * 2;
+    const int64_t have = rows - r0;            // rows of this block that exist (may be <= 0)
+    const int two = cols - c0 >= 2 ? 2 : cols - c0 == 1 ? 1 : 0;
+
+    uint32_t a[32], b[XT == F32 ? 32 : 1];     // 16-bit: both columns of a row in a[r]
+    const uint8_t *p = (const uint8_t *)x + (r0 * ld + c0) * B;
+#pragma unroll
+    for (int r = 0; r < 32; r++) {
+        const uint8_t *q = p + (int64_t)r * ld * B;
+        if constexpr (XT == F32) {
+            a[r] = b[r] = 0;
+            if (r < have && two == 2) {
+                const u32x2_any v = *(const u32x2_any *)q;
+                a[r] = v.x;
+                b[r] = v.y;
+            } else if (r < have && two == 1) {
+                a[r] = *(const uint32_t *)q;
+            }
+        } else {
+            a[r] = 0;
+            if (r < have && two == 2) a[r] = *(const u32_any *)q;
+            else if (r < have && two == 1) a[r] = *(const uint16_t *)q;
+        }
+    }
+    uint32_t ma = 0, mb = 0;
+#pragma unroll
+    for (int r = 0; r < 32; r++) {
+        ma = absmax_of<XT>(ma, a[r]);
+        if constexpr (XT == F32) mb = absmax_of<XT>(mb, b[r]);
+    }
+    if constexpr (XT != F32) {
+        mb = ma >> 16;
+        ma &= 0xffffu;
+    }
+    const uint32_t ea = scale_byte<XT>(ma), eb = scale_byte<XT>(mb);
+    const float sa = scale_of(ea), sb = scale_of(eb);
+    uint32_t ca[4], cb[4];
+    static_for<4>([&](auto W) {
+        constexpr int w = W;
+        ca[w] = cb[w] = 0;
+        static_for<4>([&](auto K) {
+            constexpr int k = K, r = 8 * w + 2 * k;
+            if constexpr (XT == F32) {
+                ca[w] = encode2<XT, k>(ca[w], a[r], a[r + 1], sa);
+                cb[w] = encode2<XT, k>(cb[w], b[r], b[r + 1], sb);
+            } else {                           // rows r, r+1 of one column side by side
+                ca[w] = encode2<XT, k>(ca[w], __builtin_amdgcn_perm(a[r + 1], a[r], 0x05040100u), 0, sa);
+                cb[w] = encode2<XT, k>(cb[w], __builtin_amdgcn_perm(a[r + 1], a[r], 0x07060302u), 0, sb);
+            }
+        });
+    });
+    *(uint4 *)(lines + (2 * pair) * kLine + 16 * block) = make_uint4(ca[0], ca[1], ca[2], ca[3]);
+    *(uint4 *)(lines + (2 * pair + 1) * kLine + 16 * block) = make_uint4(cb[0], cb[1], cb[2], cb[3]);
+    marks[(2 * pair) * 8 + block] = (uint8_t)ea;
+    marks[(2 * pair + 1) * 8 + block] = (uint8_t)eb;
+    __syncthreads();
+
+    // 64 output rows of 128 bytes: 8 threads a row; the padded height may end halfway
+    const int64_t wide = pad_rows - tr;        // 128 or at least 256
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        const int line = (tid >> 3) + 32 * k, piece = tid & 7;
+        const int64_t c = tc + line;
+        if (c < cols && 32 * piece < wide)
+            *(uint4 *)(codes + c * (pad_rows / 2) + tr / 2 + 16 * piece) =
+                *(const uint4 *)(lines + line * kLine + 16 * piece);
+    }
+    if (tid < 2 * kTCols) {
+        const int line = tid >> 1, half = tid & 1;
+        const int64_t c = tc + line;
+        if (c < cols && 128 * half < wide)
+            *(uint32_t *)(scales + c * (pad_rows / 32) + tr / 32 + 4 * half) =
+                *(const uint32_t *)(marks + line * 8 + 4 * half);
+    }
+}
+
+template <int XT>
+hipError_t run_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, int transpose,
+                        uint8_t *codes, uint8_t *scales, hipStream_t st) {
+    if (transpose) {
+        const int64_t pad = (rows + kMxPad - 1) / kMxPad * kMxPad;
+        const int64_t ct = (cols + kTCols - 1) / kTCols, rt = (rows + kTRows - 1) / kTRows;
+        hipLaunchKernelGGL((k_mx_quantize_t<XT>), dim3((unsigned)(ct * rt)), dim3(kThreads), 0, st, x, rows,
+                           cols, ld, (uint32_t)ct, pad, codes, scales);
+        return hipGetLastError();
+    }
+    const int64_t pad = (cols + kMxPad - 1) / kMxPad * kMxPad;
+    const bool flat = cols == pad && (ld == cols || rows == 1);
+    const int64_t vecs = rows * pad / 8;
+    const unsigned grid = grid_for_waves((vecs + 64 * kMxVecs - 1) / (64 * kMxVecs));
+    if (flat)
+        hipLaunchKernelGGL((k_mx_quantize<XT, true>), dim3(grid), dim3(kThreads), 0, st, x, vecs, 1u, cols,
+                           ld, (uint32_t *)codes, (uint32_t *)scales);
+    else
+        hipLaunchKernelGGL((k_mx_quantize<XT, false>), dim3(grid), dim3(kThreads), 0, st, x, vecs,
+                           (uint32_t)(pad / 8), cols, ld, (uint32_t *)codes, (uint32_t *)scales);
+    return hipGetLastError();
+}
+
+template <int YT>
+hipError_t run_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols,
+                          void *y, int64_t ld, hipStream_t st) {
+    const int64_t pad = (cols + kMxPad - 1) / kMxPad * kMxPad;
+    const bool flat = cols == pad && (ld == cols || rows == 1);
+    const int64_t vecs = rows * pad / 8;
+    const unsigned grid = grid_for_waves((vecs + 64 * kMxVecs - 1) / (64 * kMxVecs));
+    if (flat)
+        hipLaunchKernelGGL((k_mx_dequantize<YT, true>), dim3(grid), dim3(kThreads), 0, st,
+                           (const uint32_t *)codes, scales, vecs, 1u, cols, ld, y);
+    else
+        hipLaunchKernelGGL((k_mx_dequantize<YT, false>), dim3(grid), dim3(kThreads), 0, st,
+                           (const uint32_t *)codes, scales, vecs, (uint32_t)(pad / 8), cols, ld, y);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mx_quantize(const void *x, int xt, int64_t rows, int64_t cols, int64_t ld,
+                              int transpose, uint8_t *codes, uint8_t *scales, hipStream_t st) {
+    switch (xt) {
+    case F16: return run_quantize<F16>(x, rows, cols, ld, transpose, codes, scales, st);
+    case BF16: return run_quantize<BF16>(x, rows, cols, ld, transpose, codes, scales, st);
+    case F32: return run_quantize<F32>(x, rows, cols, ld, transpose, codes, scales, st);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,
+                                int64_t cols, void *y, int yt, int64_t ld, hipStream_t st) {
+    switch (yt) {
+    case F16: return run_dequantize<F16>(codes, scales, rows, cols, y, ld, st);
+    case BF16: return run_dequantize<BF16>(codes, scales, rows, cols, y, ld, st);
+    case F32: return run_dequantize<F32>(codes, scales, rows, cols, y, ld, st);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace qcp

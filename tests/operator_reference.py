@@ -62,3 +62,43 @@ def stochastic_e4m3(x, scale, half, slack=0.0):
     q = np.abs(x) / np.where(scale == 0, 1.0, scale)
     unit = 2.0 ** (np.maximum(np.frexp(q)[1] - 1, -6) - 3.0)
     return np.copysign(np.maximum(np.floor(q / unit + half / 65536 + slack), 0) * unit, x)
+
+
+# ------------------------------------------------------------------ MXFP4
+
+E2M1 = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
+
+
+def padded(n):
+    return -(-n // 128) * 128
+
+
+def mx_payload(x):
+    """float64 [rows, cols] (values of a 16- or 32-bit type) -> (codes, scales) bytes."""
+    rows, cols = x.shape
+    t = np.zeros((rows, padded(cols)))
+    t[:, :cols] = x
+    b = t.reshape(rows, -1, 32)
+    with np.errstate(invalid="ignore", over="ignore"):
+        big = np.abs(b).max(2)
+        ok = np.isfinite(big)
+        # the exponent field of the absmax in fp32: floor(log2) + 127, 0 for subnormals
+        field = np.where(big >= 2.0 ** -126, np.frexp(np.where(ok, big, 1.0))[1] - 1 + 127, 0)
+        e = np.where(ok, np.maximum(field - 2, 0), 255)
+        a = np.abs(b) / np.where(ok, np.ldexp(1.0, e - 127), 1.0)[:, :, None]
+        below = np.searchsorted(E2M1, a, side="right") - 1
+        below = np.clip(below, 0, 7)
+        above = np.minimum(below + 1, 7)
+        d0, d1 = a - E2M1[below], E2M1[above] - a
+        up = (d1 < d0) | ((d1 == d0) & (below % 2 == 1))
+        code = np.where(up & (above > below), above, below) + np.where(np.signbit(b), 8, 0)
+    code = code.reshape(rows, -1).astype(np.uint8)
+    return code[:, 0::2] | (code[:, 1::2] << 4), e.astype(np.uint8), ok
+
+
+def mx_values(codes, scales):
+    """payload bytes -> float64 [lines, P]."""
+    c = np.stack([codes & 15, codes >> 4], 2).reshape(codes.shape[0], -1).astype(np.int64)
+    v = np.where(c & 8, -1.0, 1.0) * E2M1[c & 7]
+    s = np.where(scales == 255, np.nan, np.ldexp(1.0, scales.astype(np.int64) - 127))
+    return v * np.repeat(s, 32, axis=1)
