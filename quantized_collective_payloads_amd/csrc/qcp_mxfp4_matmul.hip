@@ -111,9 +111,192 @@ __global__ __launch_bounds__(kThreads) void k_mx_matmul(const uint8_t *__restric
     }
 }
 
+// ---------------------------------------------------------------------------
+// 256 x 256 of C per work-group, for shapes whose tiles fill the GPU.
+// ---------------------------------------------------------------------------
+// Bound: the matrix cores.  Four waves, one per SIMD, hold 128 x 128 each in 256
+// accumulators; a granule of 128 is then 32 instructions of 32 cycles on 16 KB of
+// operands per wave, 64 bytes of LDS a cycle for the whole CU, half of what it
+// gives.  A stage is 256 of K: 128 bytes of each of the 512 operand rows, whole
+// cache lines, in one of two 64 KB slots.
+//
+// Copies go from memory to LDS without registers (buffer_load ... lds), so their
+// latency is covered by the matrix instructions of a whole stage: with the
+// fragments of granule 0 in registers a wave issues its products and reads those
+// of granule 1; one barrier, at which every wave has read this stage and holds no
+// outstanding copy of the next; the copies of the stage after that go into the
+// slot just freed; and the products of granule 1 run beside the reads of the next
+// stage's granule 0.
+//
+// LDS holds a row's 8 pieces of 16 bytes in the order piece ^ (row & 7): the copy
+// permutes its source addresses, so both it and the fragment reads (8 rows at the
+// same piece) touch all banks once.  Scales are copied for 4 granules at a time,
+// 16 bytes a row, into two slots of their own.
+//
+// Rows past the end repeat the last row.  Windows in K are pulled back to end
+// with the row: a last odd granule comes as the second one of its window.
+constexpr int kTile = 256;
+constexpr int kSlot = 2 * kTile * 128;                 // codes of A and B, one stage
+constexpr int kMarkSlot = 2 * kTile * 16;              // scales of A and B, 4 granules
+constexpr int kBigLds = 2 * kSlot + 2 * kMarkSlot;     // 144 KB
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+// 64 lanes x 16 bytes from rsrc[voff + soff] to LDS at `lds` + 16 * lane.  The
+// caller waits for it with wait_copies; no register is written.
+__device__ __forceinline__ void copy_to_lds(uint32_t lds, uint32_t voff, i32x4_t rsrc, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+                 : "memory", "m0");
+}
+
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+__device__ __forceinline__ i32x4_t buffer_of(const void *p, uint64_t bytes) {
+    const uint64_t at = (uint64_t)p;
+    const uint32_t n = bytes > 0xfffffffcull ? 0xfffffffcu : (uint32_t)bytes;
+    return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)at),
+                   __builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32)),
+                   __builtin_amdgcn_readfirstlane((int)n), 0x00020000};
+}
+
+struct Fragments {
+    uint4 a[4][2], b[4][2];
+    uint32_t sa[4], sb[4];
+};
+
+__device__ __forceinline__ void products(const Fragments &f, f32x16_t (&acc)[4][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            acc[i][j] = mma<0>(f.b[j][0], f.sb[j], f.a[i][0], f.sa[i], acc[i][j]);
+            acc[i][j] = mma<1>(f.b[j][1], f.sb[j], f.a[i][1], f.sa[i], acc[i][j]);
+        }
+}
+
+template <int CT>
+__global__ __launch_bounds__(kThreads, 1) void k_mx_matmul_big(
+    const uint8_t *__restrict__ a, const uint8_t *__restrict__ as, const uint8_t *__restrict__ b,
+    const uint8_t *__restrict__ bs, int64_t M, int64_t N, uint32_t granules, uint32_t m_tiles,
+    uint32_t n_tiles, void *__restrict__ c, int64_t ldc) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kBigLds];
+    const int tid = (int)__builtin_amdgcn_workitem_id_x();
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = lane_id();
+
+    // work-groups are dealt round-robin to the 8 XCDs: give each XCD a contiguous
+    // run of tiles, and walk it 4 tiles of M by N, so that the 32 tiles an XCD works
+    // on at a time share 4 + 8 operand panels in its L2
+    const uint32_t tiles = m_tiles * n_tiles;
+    uint32_t t = __builtin_amdgcn_workgroup_id_x();
+    const uint32_t per = tiles / 8, extra = tiles % 8, xcd = t % 8, slot8 = t / 8;
+    t = xcd * per + min(xcd, extra) + slot8;
+    const uint32_t band = 4 * n_tiles, first = t / band * 4, height = min(4u, m_tiles - first);
+    const uint32_t in = t - t / band * band;
+    const int64_t m0 = (int64_t)(first + in % height) * kTile, n0 = (int64_t)(in / height) * kTile;
+
+    const uint32_t row_bytes = granules * 64, mark_bytes = granules * 4;
+    const int64_t m_left = M - m0, n_left = N - n0;
+    const i32x4_t ra = buffer_of(a + m0 * row_bytes, (uint64_t)min(m_left, (int64_t)kTile) * row_bytes);
+    const i32x4_t rb = buffer_of(b + n0 * row_bytes, (uint64_t)min(n_left, (int64_t)kTile) * row_bytes);
+    const i32x4_t rsa = buffer_of(as + m0 * mark_bytes, (uint64_t)min(m_left, (int64_t)kTile) * mark_bytes);
+    const i32x4_t rsb = buffer_of(bs + n0 * mark_bytes, (uint64_t)min(n_left, (int64_t)kTile) * mark_bytes);
+    const uint32_t m_last = (uint32_t)min(m_left, (int64_t)kTile) - 1;
+    const uint32_t n_last = (uint32_t)min(n_left, (int64_t)kTile) - 1;
+
+    // copies: wave w brings rows 64w .. 64w+63 of both operands, 8 rows at a time
+    uint32_t va[8], vb[8];
+    const uint32_t piece = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const uint32_t row = wave * 64 + i * 8 + (lane >> 3);
+        va[i] = min(row, m_last) * row_bytes + piece;
+        vb[i] = min(row, n_last) * row_bytes + piece;
+    }
+    const uint32_t vsa = min((uint32_t)(wave * 64 + lane), m_last) * mark_bytes;
+    const uint32_t vsb = min((uint32_t)(wave * 64 + lane), n_last) * mark_bytes;
+    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
+    const uint32_t stages = (granules + 1) / 2;
+
+    auto copy_stage = [&](uint32_t s) {
+        const uint32_t at = base + (s & 1) * kSlot + wave * 64 * 128;
+        const uint32_t k = min(2 * s, granules - 2) * 64;
+#pragma unroll
+        for (int i = 0; i < 8; i++) copy_to_lds(at + i * 1024, va[i], ra, k);
+#pragma unroll
+        for (int i = 0; i < 8; i++) copy_to_lds(at + kTile * 128 + i * 1024, vb[i], rb, k);
+        if ((s & 1) == 0) {
+            const uint32_t mark = base + 2 * kSlot + ((s >> 1) & 1) * kMarkSlot + wave * 64 * 16;
+            const uint32_t ks = min(2 * s, granules - 4) * 4;
+            copy_to_lds(mark, vsa, rsa, ks);
+            copy_to_lds(mark + kTile * 16, vsb, rsb, ks);
+        }
+    };
+
+    // fragments: wave w computes rows 128*(w&1) of A against rows 128*(w>>1) of B
+    const int r = lane & 31, half = lane >> 5, x = lane & 7;
+    const uint32_t arow = (wave & 1) * 128 + r, brow = kTile + (wave >> 1) * 128 + r;
+    auto read = [&](uint32_t g, Fragments &f) {          // granule g
+        const uint32_t s = g / 2, j = g - min(2 * s, granules - 2);
+        const uint8_t *codes = lds + (s & 1) * kSlot;
+        const uint32_t p0 = ((4 * j + 2 * half) ^ x) * 16, p1 = p0 ^ 16;
+        const uint32_t q = g / 4, k = g - min(4 * q, granules - 4);
+        const uint8_t *marks = lds + 2 * kSlot + (q & 1) * kMarkSlot + 4 * k + 2 * half;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            f.a[i][0] = *(const uint4 *)(codes + (arow + 32 * i) * 128 + p0);
+            f.a[i][1] = *(const uint4 *)(codes + (arow + 32 * i) * 128 + p1);
+            f.b[i][0] = *(const uint4 *)(codes + (brow + 32 * i) * 128 + p0);
+            f.b[i][1] = *(const uint4 *)(codes + (brow + 32 * i) * 128 + p1);
+            f.sa[i] = *(const uint16_t *)(marks + (arow + 32 * i) * 16);
+            f.sb[i] = *(const uint16_t *)(marks + (brow + 32 * i) * 16);
+        }
+    };
+
+    f32x16_t acc[4][4] = {};
+    copy_stage(0);
+    if (stages > 1) copy_stage(1);
+    wait_and_meet();
+    Fragments f, h;
+    read(0, f);
+    uint32_t g = 0;
+    for (uint32_t s = 0; s < granules / 2; s++, g += 2) {
+        read(g + 1, h);
+        products(f, acc);
+        wait_and_meet();
+        if (s + 2 < stages) copy_stage(s + 2);
+        if (g + 2 < granules) read(g + 2, f);
+        products(h, acc);
+    }
+    if (granules & 1) products(f, acc);
+
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int64_t m = m0 + (wave & 1) * 128 + 32 * i + r;
+        if (m >= M) continue;
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const int64_t n = n0 + (wave >> 1) * 128 + 32 * j + 8 * q + 4 * half;
+                const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                store4<CT>(c, m * ldc + n, N - n < 4 ? (int)(N - n) : 4, v);
+            }
+    }
+}
+
 template <int CT>
 hipError_t run_matmul(const uint8_t *a, const uint8_t *as, const uint8_t *b, const uint8_t *bs,
                       int64_t M, int64_t N, int64_t granules, void *c, int64_t ldc, hipStream_t st) {
+    if (M > 128 && N > 128 && granules >= 4 && granules < (1 << 18)) {
+        const int64_t bm = (M + kTile - 1) / kTile, bn = (N + kTile - 1) / kTile;
+        hipLaunchKernelGGL((k_mx_matmul_big<CT>), dim3((unsigned)(bm * bn)), dim3(kThreads), 0, st, a, as, b,
+                           bs, M, N, (uint32_t)granules, (uint32_t)bm, (uint32_t)bn, c, ldc);
+        return hipGetLastError();
+    }
     const int64_t mt = (M + 127) / 128, nt = (N + 127) / 128;
     if (mt * nt > kMaxGroups) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_mx_matmul<CT>), dim3((unsigned)(mt * nt)), dim3(kThreads), 0, st, a, as, b, bs, M,
