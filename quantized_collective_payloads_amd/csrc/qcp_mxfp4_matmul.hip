@@ -120,21 +120,26 @@ __global__ __launch_bounds__(kThreads) void k_mx_matmul(const uint8_t *__restric
 // gives.  A stage is 256 of K: 128 bytes of each of the 512 operand rows, whole
 // cache lines, in one of two 64 KB slots.
 //
+// Within a stage the lower half-wave takes the first granule (64 bytes of its row)
+// and the upper one the second, so a lane's four blocks have their scales in one
+// dword and the instruction picks the byte.  A stage is two phases of 128 of K.
+//
 // Copies go from memory to LDS without registers (buffer_load ... lds), so their
 // latency is covered by the matrix instructions of a whole stage: with the
-// fragments of granule 0 in registers a wave issues its products and reads those
-// of granule 1; one barrier, at which every wave has read this stage and holds no
+// fragments of phase 0 in registers a wave issues its products and reads those of
+// phase 1; one barrier, at which every wave has read this stage and holds no
 // outstanding copy of the next; the copies of the stage after that go into the
-// slot just freed; and the products of granule 1 run beside the reads of the next
-// stage's granule 0.
+// slot just freed; and the products of phase 1 run beside the reads of the next
+// stage's phase 0.
 //
-// LDS holds a row's 8 pieces of 16 bytes in the order piece ^ (row & 7): the copy
-// permutes its source addresses, so both it and the fragment reads (8 rows at the
-// same piece) touch all banks once.  Scales are copied for 4 granules at a time,
+// LDS holds a row's 8 pieces of 16 bytes in the order piece ^ (row / 2 % 8): the
+// copy permutes its source addresses, so that a fragment read, 16 rows of 128 bytes
+// at the same piece a cycle, touches each of the 64 banks once.  Scales are copied for 4 granules at a time,
 // 16 bytes a row, into two slots of their own.
 //
 // Rows past the end repeat the last row.  Windows in K are pulled back to end
-// with the row: a last odd granule comes as the second one of its window.
+// with the row: a last odd granule comes as the second one of its window, and is
+// multiplied by itself as in the kernel above.
 constexpr int kTile = 256;
 constexpr int kSlot = 2 * kTile * 128;                 // codes of A and B, one stage
 constexpr int kMarkSlot = 2 * kTile * 16;              // scales of A and B, 4 granules
@@ -165,17 +170,18 @@ __device__ __forceinline__ i32x4_t buffer_of(const void *p, uint64_t bytes) {
 
 struct Fragments {
     uint4 a[4][2], b[4][2];
-    uint32_t sa[4], sb[4];
+};
+struct Scales {
+    uint32_t a[4], b[4];
 };
 
-__device__ __forceinline__ void products(const Fragments &f, f32x16_t (&acc)[4][4]) {
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            acc[i][j] = mma<0>(f.b[j][0], f.sb[j], f.a[i][0], f.sa[i], acc[i][j]);
-            acc[i][j] = mma<1>(f.b[j][1], f.sb[j], f.a[i][1], f.sa[i], acc[i][j]);
-        }
+// the 32 products of phase P, four rows of instructions at a time
+template <int P>
+__device__ __forceinline__ void products(const Fragments &f, const Scales &e, f32x16_t (&acc)[4][4]) {
+    static_for<32>([&](auto S) {
+        constexpr int s = S, t = s / 16, i = s / 4 % 4, n = s % 4;
+        acc[i][n] = mma<2 * P + t>(f.b[n][t], e.b[n], f.a[i][t], e.a[i], acc[i][n]);
+    });
 }
 
 template <int CT>
@@ -209,10 +215,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_mx_matmul_big(
 
     // copies: wave w brings rows 64w .. 64w+63 of both operands, 8 rows at a time
     uint32_t va[8], vb[8];
-    const uint32_t piece = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const uint32_t row = wave * 64 + i * 8 + (lane >> 3);
+        const uint32_t piece = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
         va[i] = min(row, m_last) * row_bytes + piece;
         vb[i] = min(row, n_last) * row_bytes + piece;
     }
@@ -237,41 +243,130 @@ __global__ __launch_bounds__(kThreads, 1) void k_mx_matmul_big(
     };
 
     // fragments: wave w computes rows 128*(w&1) of A against rows 128*(w>>1) of B
-    const int r = lane & 31, half = lane >> 5, x = lane & 7;
+    const int r = lane & 31, half = lane >> 5, x = (lane >> 1) & 7;
     const uint32_t arow = (wave & 1) * 128 + r, brow = kTile + (wave >> 1) * 128 + r;
-    auto read = [&](uint32_t g, Fragments &f) {          // granule g
-        const uint32_t s = g / 2, j = g - min(2 * s, granules - 2);
-        const uint8_t *codes = lds + (s & 1) * kSlot;
-        const uint32_t p0 = ((4 * j + 2 * half) ^ x) * 16, p1 = p0 ^ 16;
-        const uint32_t q = g / 4, k = g - min(4 * q, granules - 4);
-        const uint8_t *marks = lds + 2 * kSlot + (q & 1) * kMarkSlot + 4 * k + 2 * half;
+    // 16-byte pieces p and p + 1 of the fragments' rows
+    auto read = [&](const uint8_t *codes, uint32_t p, Fragments &f) {
+        static_for<4>([&](auto I) {
+            constexpr int i = I;
+#pragma unroll
+            for (int t = 0; t < 2; t++) {
+                f.a[i][t] = *(const uint4 *)(codes + (arow + 32 * i) * 128 + ((p ^ x) ^ t) * 16);
+                f.b[i][t] = *(const uint4 *)(codes + (brow + 32 * i) * 128 + ((p ^ x) ^ t) * 16);
+            }
+        });
+    };
+    // the scales of one granule, at dword k of the group's 4
+    auto read_scales = [&](const uint8_t *marks, uint32_t k, Scales &e) {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            f.a[i][0] = *(const uint4 *)(codes + (arow + 32 * i) * 128 + p0);
-            f.a[i][1] = *(const uint4 *)(codes + (arow + 32 * i) * 128 + p1);
-            f.b[i][0] = *(const uint4 *)(codes + (brow + 32 * i) * 128 + p0);
-            f.b[i][1] = *(const uint4 *)(codes + (brow + 32 * i) * 128 + p1);
-            f.sa[i] = *(const uint16_t *)(marks + (arow + 32 * i) * 16);
-            f.sb[i] = *(const uint16_t *)(marks + (brow + 32 * i) * 16);
+            e.a[i] = *(const uint32_t *)(marks + (arow + 32 * i) * 16 + 4 * k);
+            e.b[i] = *(const uint32_t *)(marks + (brow + 32 * i) * 16 + 4 * k);
         }
     };
+    auto marks_of = [&](uint32_t s) { return lds + 2 * kSlot + ((s >> 1) & 1) * kMarkSlot; };
+    auto window = [&](uint32_t s) { return min(2 * s & ~3u, granules - 4); };   // first granule of s's scales
 
     f32x16_t acc[4][4] = {};
     copy_stage(0);
     if (stages > 1) copy_stage(1);
     wait_and_meet();
     Fragments f, h;
-    read(0, f);
-    uint32_t g = 0;
-    for (uint32_t s = 0; s < granules / 2; s++, g += 2) {
-        read(g + 1, h);
-        products(f, acc);
+    Scales e;
+    read(lds, 4 * half, f);
+    read_scales(marks_of(0), half, e);
+
+    // the 32 products of phase P of a stage, in the order written: after product n
+    // come the n-th read of the next phase's fragments, and with COPY the n-th copy
+    // of the stage at byte k of the rows, so the matrix cores never wait for the rest
+    // to issue.  GROUP: also the scales of the next 4 granules, and the copy of those
+    // after them.
+    uint4 ga[4], gb[4];
+    auto phase = [&](auto P, const Fragments &now, Fragments &then, const uint8_t *codes, auto COPY,
+                     uint32_t to, uint32_t k, auto READ_GROUP, const uint8_t *marks, auto COPY_GROUP,
+                     uint32_t marks_to) {
+        constexpr int ph = P;
+        const uint32_t p0 = ((4 * half + (ph ? 0 : 2)) ^ x) * 16;
+        static_for<32>([&](auto S) {
+            constexpr int s = S, t = s / 16, i = s / 4 % 4, n = s % 4;
+            acc[i][n] = mma<2 * ph + t>(now.b[n][t], e.b[n], now.a[i][t], e.a[i], acc[i][n]);
+            if constexpr (s < 16) {
+                constexpr int u = s / 8, r4 = s % 4;
+                if constexpr (s % 8 < 4) then.b[r4][u] = *(const uint4 *)(codes + (brow + 32 * r4) * 128 + (p0 ^ (16 * u)));
+                else then.a[r4][u] = *(const uint4 *)(codes + (arow + 32 * r4) * 128 + (p0 ^ (16 * u)));
+            } else if constexpr (READ_GROUP && s < 20) {
+                gb[s - 16] = *(const uint4 *)(marks + (brow + 32 * (s - 16)) * 16);
+            } else if constexpr (READ_GROUP && s < 24) {
+                ga[s - 20] = *(const uint4 *)(marks + (arow + 32 * (s - 20)) * 16);
+            }
+            if constexpr (COPY) {
+                if constexpr (s < 8) copy_to_lds(to + s * 1024, va[s], ra, k);
+                else if constexpr (s < 16) copy_to_lds(to + kTile * 128 + (s - 8) * 1024, vb[s - 8], rb, k);
+                else if constexpr (COPY_GROUP && s == 16) copy_to_lds(marks_to, vsa, rsa, k / 16);
+                else if constexpr (COPY_GROUP && s == 17) copy_to_lds(marks_to + kTile * 16, vsb, rsb, k / 16);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    using no = std::integral_constant<int, 0>;
+    using yes = std::integral_constant<int, 1>;
+
+    // two stages at a time while there are two more to copy: every window then lies
+    // where the stage number says
+    uint32_t s = 0;
+    const uint32_t full = granules / 2;
+    if (full >= 4) {
+        const uint32_t codes_to = base + wave * 64 * 128, marks_to = base + 2 * kSlot + wave * 64 * 16;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            ga[i] = *(const uint4 *)(marks_of(0) + (arow + 32 * i) * 16);
+            gb[i] = *(const uint4 *)(marks_of(0) + (brow + 32 * i) * 16);
+        }
+        for (; s + 4 <= full; s += 2) {
+            const uint32_t next = ((s >> 1) & 1) ^ 1;
+            phase(no{}, f, h, lds, no{}, 0, 0, no{}, lds, no{}, 0);
+            wait_and_meet();
+            phase(yes{}, h, f, lds + kSlot, yes{}, codes_to, (s + 2) * 128, no{}, lds, yes{},
+                  marks_to + next * kMarkSlot);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                e.a[i] = half ? ga[i].w : ga[i].z;
+                e.b[i] = half ? gb[i].w : gb[i].z;
+            }
+            phase(no{}, f, h, lds + kSlot, no{}, 0, 0, no{}, lds, no{}, 0);
+            wait_and_meet();
+            phase(yes{}, h, f, lds, yes{}, codes_to + kSlot, (s + 3) * 128, yes{},
+                  lds + 2 * kSlot + next * kMarkSlot, no{}, 0);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                e.a[i] = half ? ga[i].y : ga[i].x;
+                e.b[i] = half ? gb[i].y : gb[i].x;
+            }
+        }
+        // the group's scales may have come from a window that is pulled back
+        read_scales(marks_of(s), 2 * s - window(s) + half, e);
+    }
+    for (; s < full; s++) {
+        read(lds + (s & 1) * kSlot, 4 * half + 2, h);
+        products<0>(f, e, acc);
         wait_and_meet();
         if (s + 2 < stages) copy_stage(s + 2);
-        if (g + 2 < granules) read(g + 2, f);
-        products(h, acc);
+        products<1>(h, e, acc);
+        if (s + 1 < full) {
+            read(lds + ((s + 1) & 1) * kSlot, 4 * half, f);
+            read_scales(marks_of(s + 1), 2 * s + 2 - window(s + 1) + half, e);
+        }
     }
-    if (granules & 1) products(f, acc);
+    if (granules & 1) {                                  // the last granule, alone
+        read(lds + (full & 1) * kSlot, 4 + 2 * half, f);
+        read_scales(marks_of(full), granules - 1 - window(full), e);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            e.a[i] >>= 16 * half;
+            e.b[i] >>= 16 * half;
+        }
+        products<0>(f, e, acc);
+    }
 
 #pragma unroll
     for (int i = 0; i < 4; i++) {
