@@ -18,9 +18,10 @@ namespace {
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 template <int T>
-__device__ __forceinline__ f32x16_t mma(uint4 a, uint32_t sa, uint4 b, uint32_t sb, f32x16_t c) {
+__device__ __forceinline__ f32x16_t mma(u32x4_t a, uint32_t sa, u32x4_t b, uint32_t sb, f32x16_t c) {
     const i32x8_t av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
     const i32x8_t bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, T, (int)sa, T, (int)sb);
@@ -48,8 +49,9 @@ __device__ __forceinline__ void store4(void *c, int64_t at, int count, const flo
     }
 }
 
-// A wave computes 64 x 64 of C from 2 + 2 fragments per granule, read straight
-// from memory; a work-group's 4 waves make 128 x 128.  Rows past the end repeat
+// The plain form, for the K that the kernels below do not take: a wave computes
+// 64 x 64 of C from 2 + 2 fragments per granule, read straight from memory; a
+// work-group's 4 waves make 128 x 128.  Rows past the end repeat
 // the last one and are not stored.
 template <int CT>
 __global__ __launch_bounds__(kThreads) void k_mx_matmul(const uint8_t *__restrict__ a,
@@ -75,14 +77,14 @@ __global__ __launch_bounds__(kThreads) void k_mx_matmul(const uint8_t *__restric
     }
     f32x16_t acc[2][2] = {};
     for (int64_t g = 0; g < granules; g++) {
-        uint4 fa[2][2], fb[2][2];
+        u32x4_t fa[2][2], fb[2][2];
         uint32_t sa[2], sb[2];
 #pragma unroll
         for (int i = 0; i < 2; i++) {
 #pragma unroll
             for (int t = 0; t < 2; t++) {
-                fa[i][t] = *(const uint4 *)(pa[i] + g * 64 + 16 * t);
-                fb[i][t] = *(const uint4 *)(pb[i] + g * 64 + 16 * t);
+                fa[i][t] = *(const u32x4_t *)(pa[i] + g * 64 + 16 * t);
+                fb[i][t] = *(const u32x4_t *)(pb[i] + g * 64 + 16 * t);
             }
             sa[i] = *(const uint32_t *)(qa[i] + g * 4) >> (16 * half);
             sb[i] = *(const uint32_t *)(qb[i] + g * 4) >> (16 * half);
@@ -112,20 +114,23 @@ __global__ __launch_bounds__(kThreads) void k_mx_matmul(const uint8_t *__restric
 }
 
 // ---------------------------------------------------------------------------
-// 256 x 256 of C per work-group, for shapes whose tiles fill the GPU.
+// 64*FM x 64*FN of C per work-group, staged through LDS.
 // ---------------------------------------------------------------------------
-// Bound: the matrix cores.  Four waves, one per SIMD, hold 128 x 128 each in 256
-// accumulators; a granule of 128 is then 32 instructions of 32 cycles on 16 KB of
-// operands per wave, 64 bytes of LDS a cycle for the whole CU, half of what it
-// gives.  A stage is 256 of K: 128 bytes of each of the 512 operand rows, whole
-// cache lines, in one of two 64 KB slots.
+// Bound: the matrix cores, and their power (random codes multiplied in registers
+// alone reach 5.8 PFLOP/s).  Four waves, 2 x 2, hold 32*FM x 32*FN each.  At 4 x 4
+// that is 256 x 256 per work-group and 256 accumulators, one wave per SIMD: a
+// phase is 32 instructions of 32 cycles on 16 KB of operands, a quarter of what LDS
+// gives.  At 2 x 2, 128 x 128, two work-groups share a CU: twice the operand traffic
+// per product, but four times as many tiles, and one's stores run beside the
+// other's products.  A stage is 256 of K: 128 bytes of each operand row, whole cache
+// lines, in one of two slots.
 //
 // Within a stage the lower half-wave takes the first granule (64 bytes of its row)
 // and the upper one the second, so a lane's four blocks have their scales in one
 // dword and the instruction picks the byte.  A stage is two phases of 128 of K.
 //
 // Copies go from memory to LDS without registers (buffer_load ... lds), so their
-// latency is covered by the matrix instructions of a whole stage: with the
+// latency is covered by the matrix instructions of a whole stage or more: with the
 // fragments of phase 0 in registers a wave issues its products and reads those of
 // phase 1; one barrier, at which every wave has read this stage and holds no
 // outstanding copy of the next; the copies of the stage after that go into the
@@ -134,30 +139,29 @@ __global__ __launch_bounds__(kThreads) void k_mx_matmul(const uint8_t *__restric
 //
 // LDS holds a row's 8 pieces of 16 bytes in the order piece ^ (row / 2 % 8): the
 // copy permutes its source addresses, so that a fragment read, 16 rows of 128 bytes
-// at the same piece a cycle, touches each of the 64 banks once.  Scales are copied for 4 granules at a time,
-// 16 bytes a row, into two slots of their own.
+// at the same piece a cycle, touches each of the 64 banks once.  Scales are copied
+// for 4 granules at a time, 16 bytes a row, into slots of their own.
 //
 // Rows past the end repeat the last row.  Windows in K are pulled back to end
 // with the row: a last odd granule comes as the second one of its window, and is
 // multiplied by itself as in the kernel above.
-constexpr int kTile = 256;
-constexpr int kSlot = 2 * kTile * 128;                 // codes of A and B, one stage
-constexpr int kMarkSlot = 2 * kTile * 16;              // scales of A and B, 4 granules
-constexpr int kBigLds = 2 * kSlot + 2 * kMarkSlot;     // 144 KB
-
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
 // 64 lanes x 16 bytes from rsrc[voff + soff] to LDS at `lds` + 16 * lane.  The
-// caller waits for it with wait_copies; no register is written.
+// caller waits for it with wait_and_meet; no vector register is written, and nothing
+// else in these kernels uses m0.
 __device__ __forceinline__ void copy_to_lds(uint32_t lds, uint32_t voff, i32x4_t rsrc, uint32_t soff) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
-                 : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-                 : "memory", "m0");
+                 : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(voff), "s"(rsrc),
+                   "s"(__builtin_amdgcn_readfirstlane((int)soff))
+                 : "memory");
 }
 
+// until at most N of this wave's copies are in flight; then with the other waves
+template <int N>
 __device__ __forceinline__ void wait_and_meet() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ i32x4_t buffer_of(const void *p, uint64_t bytes) {
@@ -168,142 +172,191 @@ __device__ __forceinline__ i32x4_t buffer_of(const void *p, uint64_t bytes) {
                    __builtin_amdgcn_readfirstlane((int)n), 0x00020000};
 }
 
-struct Fragments {
-    uint4 a[4][2], b[4][2];
-};
-struct Scales {
-    uint32_t a[4], b[4];
-};
-
-// the 32 products of phase P, four rows of instructions at a time
-template <int P>
-__device__ __forceinline__ void products(const Fragments &f, const Scales &e, f32x16_t (&acc)[4][4]) {
-    static_for<32>([&](auto S) {
-        constexpr int s = S, t = s / 16, i = s / 4 % 4, n = s % 4;
-        acc[i][n] = mma<2 * P + t>(f.b[n][t], e.b[n], f.a[i][t], e.a[i], acc[i][n]);
-    });
+// 16 bytes and 4 bytes of LDS at a byte address
+__device__ __forceinline__ u32x4_t lds16(uint32_t at) {
+    return *(const __attribute__((address_space(3))) u32x4_t *)at;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t at) {
+    return *(const __attribute__((address_space(3))) uint32_t *)at;
 }
 
-template <int CT>
-__global__ __launch_bounds__(kThreads, 1) void k_mx_matmul_big(
+template <int FM, int FN> struct tgeom {
+    static constexpr int TM = 64 * FM, TN = 64 * FN;       // C per work-group
+    static constexpr int slots = FM * FN == 1 ? 4 : 2;     // stages in LDS
+    static constexpr int rows = TM + TN;
+    static constexpr int slot = rows * 128;                // codes of A and B, one stage
+    static constexpr int mark_slot = rows * 16;            // scales of A and B, 4 granules
+    static constexpr int lds = slots * (slot + mark_slot); // 144 KB at 4 x 4, 72 KB at 2 x 2 and 1 x 1
+    static constexpr int ops = 2 * FM * FN;                // products per phase and wave
+    static constexpr int reads = 2 * (FM + FN);            // fragment pieces per phase
+    static constexpr int copies = rows / 32;               // per stage and wave, 8 rows each
+    static constexpr int waves_per_simd = FM * FN <= 4 ? 2 : 1;
+    static constexpr int ahead = (slots - 2) * copies;     // copies of stages beyond the next
+};
+
+template <int FM, int FN> struct Fragments {
+    u32x4_t a[FM][2], b[FN][2];
+};
+template <int FM, int FN> struct Scales {
+    uint32_t a[FM], b[FN];
+};
+
+template <int FM, int FN, int CT>
+__global__ __launch_bounds__(kThreads, (tgeom<FM, FN>::waves_per_simd)) void k_mx_matmul_tiled(
     const uint8_t *__restrict__ a, const uint8_t *__restrict__ as, const uint8_t *__restrict__ b,
     const uint8_t *__restrict__ bs, int64_t M, int64_t N, uint32_t granules, uint32_t m_tiles,
     uint32_t n_tiles, void *__restrict__ c, int64_t ldc) {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kBigLds];
+    using Gm = tgeom<FM, FN>;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[Gm::lds];
     const int tid = (int)__builtin_amdgcn_workitem_id_x();
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = lane_id();
 
     // work-groups are dealt round-robin to the 8 XCDs: give each XCD a contiguous
-    // run of tiles, and walk it 4 tiles of M by N, so that the 32 tiles an XCD works
-    // on at a time share 4 + 8 operand panels in its L2
+    // run of tiles, and walk it 4 tiles of M by N, so that the tiles an XCD works on
+    // at a time share few operand panels in its L2
     const uint32_t tiles = m_tiles * n_tiles;
     uint32_t t = __builtin_amdgcn_workgroup_id_x();
     const uint32_t per = tiles / 8, extra = tiles % 8, xcd = t % 8, slot8 = t / 8;
     t = xcd * per + min(xcd, extra) + slot8;
     const uint32_t band = 4 * n_tiles, first = t / band * 4, height = min(4u, m_tiles - first);
     const uint32_t in = t - t / band * band;
-    const int64_t m0 = (int64_t)(first + in % height) * kTile, n0 = (int64_t)(in / height) * kTile;
+    const int64_t m0 = (int64_t)(first + in % height) * Gm::TM, n0 = (int64_t)(in / height) * Gm::TN;
 
     const uint32_t row_bytes = granules * 64, mark_bytes = granules * 4;
-    const int64_t m_left = M - m0, n_left = N - n0;
-    const i32x4_t ra = buffer_of(a + m0 * row_bytes, (uint64_t)min(m_left, (int64_t)kTile) * row_bytes);
-    const i32x4_t rb = buffer_of(b + n0 * row_bytes, (uint64_t)min(n_left, (int64_t)kTile) * row_bytes);
-    const i32x4_t rsa = buffer_of(as + m0 * mark_bytes, (uint64_t)min(m_left, (int64_t)kTile) * mark_bytes);
-    const i32x4_t rsb = buffer_of(bs + n0 * mark_bytes, (uint64_t)min(n_left, (int64_t)kTile) * mark_bytes);
-    const uint32_t m_last = (uint32_t)min(m_left, (int64_t)kTile) - 1;
-    const uint32_t n_last = (uint32_t)min(n_left, (int64_t)kTile) - 1;
+    const uint32_t m_rows = (uint32_t)min(M - m0, (int64_t)Gm::TM), n_rows = (uint32_t)min(N - n0, (int64_t)Gm::TN);
+    const i32x4_t ra = buffer_of(a + m0 * row_bytes, (uint64_t)m_rows * row_bytes);
+    const i32x4_t rb = buffer_of(b + n0 * row_bytes, (uint64_t)n_rows * row_bytes);
+    const i32x4_t rsa = buffer_of(as + m0 * mark_bytes, (uint64_t)m_rows * mark_bytes);
+    const i32x4_t rsb = buffer_of(bs + n0 * mark_bytes, (uint64_t)n_rows * mark_bytes);
 
-    // copies: wave w brings rows 64w .. 64w+63 of both operands, 8 rows at a time
-    uint32_t va[8], vb[8];
+    // copies: a wave brings a quarter of each operand's rows, 8 rows at a time
+    uint32_t va[2 * FM], vb[2 * FN];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const uint32_t row = wave * 64 + i * 8 + (lane >> 3);
-        const uint32_t piece = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
-        va[i] = min(row, m_last) * row_bytes + piece;
-        vb[i] = min(row, n_last) * row_bytes + piece;
+    for (int i = 0; i < 2 * FM; i++) {
+        const uint32_t row = wave * 16 * FM + i * 8 + (lane >> 3);
+        va[i] = min(row, m_rows - 1) * row_bytes + ((lane & 7) ^ ((row >> 1) & 7)) * 16;
     }
-    const uint32_t vsa = min((uint32_t)(wave * 64 + lane), m_last) * mark_bytes;
-    const uint32_t vsb = min((uint32_t)(wave * 64 + lane), n_last) * mark_bytes;
+#pragma unroll
+    for (int i = 0; i < 2 * FN; i++) {
+        const uint32_t row = wave * 16 * FN + i * 8 + (lane >> 3);
+        vb[i] = min(row, n_rows - 1) * row_bytes + ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+    }
+    // scales: 64 rows at a time, FM pieces of A, then FN of B, dealt to the waves (the
+    // last piece twice where they do not divide).  No branches: the loop below stays
+    // one basic block, in which the order written is kept
+    constexpr int mark_rounds = (FM + FN + 3) / 4;
+    uint32_t vs[mark_rounds], mark_at[mark_rounds];
+    i32x4_t rs[mark_rounds];
+#pragma unroll
+    for (int k = 0; k < mark_rounds; k++) {
+        const int q = min(wave + 4 * k, FM + FN - 1);
+        const bool of_a = FM >= 4 * k + 4 || (FM > 4 * k && q < FM);
+        mark_at[k] = q * 1024;
+        vs[k] = (of_a ? min((uint32_t)(64 * q + lane), m_rows - 1) : min((uint32_t)(64 * (q - FM) + lane), n_rows - 1)) * mark_bytes;
+        rs[k] = of_a ? rsa : rsb;
+    }
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
     const uint32_t stages = (granules + 1) / 2;
 
-    auto copy_stage = [&](uint32_t s) {
-        const uint32_t at = base + (s & 1) * kSlot + wave * 64 * 128;
-        const uint32_t k = min(2 * s, granules - 2) * 64;
-#pragma unroll
-        for (int i = 0; i < 8; i++) copy_to_lds(at + i * 1024, va[i], ra, k);
-#pragma unroll
-        for (int i = 0; i < 8; i++) copy_to_lds(at + kTile * 128 + i * 1024, vb[i], rb, k);
-        if ((s & 1) == 0) {
-            const uint32_t mark = base + 2 * kSlot + ((s >> 1) & 1) * kMarkSlot + wave * 64 * 16;
-            const uint32_t ks = min(2 * s, granules - 4) * 4;
-            copy_to_lds(mark, vsa, rsa, ks);
-            copy_to_lds(mark + kTile * 16, vsb, rsb, ks);
-        }
+    // the n-th copy of a stage into the slot at `to`, from byte k of the rows
+    auto copy = [&](auto I, uint32_t to, uint32_t k) __attribute__((always_inline)) {
+        constexpr int n = I;
+        if constexpr (n < 2 * FM) copy_to_lds(to + wave * 16 * FM * 128 + n * 1024, va[n], ra, k);
+        else copy_to_lds(to + Gm::TM * 128 + wave * 16 * FN * 128 + (n - 2 * FM) * 1024, vb[n - 2 * FM], rb, k);
     };
-
-    // fragments: wave w computes rows 128*(w&1) of A against rows 128*(w>>1) of B
-    const int r = lane & 31, half = lane >> 5, x = (lane >> 1) & 7;
-    const uint32_t arow = (wave & 1) * 128 + r, brow = kTile + (wave >> 1) * 128 + r;
-    // 16-byte pieces p and p + 1 of the fragments' rows
-    auto read = [&](const uint8_t *codes, uint32_t p, Fragments &f) {
-        static_for<4>([&](auto I) {
-            constexpr int i = I;
-#pragma unroll
-            for (int t = 0; t < 2; t++) {
-                f.a[i][t] = *(const uint4 *)(codes + (arow + 32 * i) * 128 + ((p ^ x) ^ t) * 16);
-                f.b[i][t] = *(const uint4 *)(codes + (brow + 32 * i) * 128 + ((p ^ x) ^ t) * 16);
-            }
+    auto copy_marks = [&](uint32_t to, uint32_t k) __attribute__((always_inline)) {
+        static_for<mark_rounds>([&](auto I) __attribute__((always_inline)) {
+            copy_to_lds(to + mark_at[I], vs[I], rs[I], k);
         });
     };
-    // the scales of one granule, at dword k of the group's 4
-    auto read_scales = [&](const uint8_t *marks, uint32_t k, Scales &e) {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            e.a[i] = *(const uint32_t *)(marks + (arow + 32 * i) * 16 + 4 * k);
-            e.b[i] = *(const uint32_t *)(marks + (brow + 32 * i) * 16 + 4 * k);
-        }
+    constexpr uint32_t kMarks = Gm::slots * Gm::slot;      // where the scales begin
+    auto slot_of = [&](uint32_t s) __attribute__((always_inline)) { return (s & (Gm::slots - 1)) * Gm::slot; };
+    auto mark_slot_of = [&](uint32_t s) __attribute__((always_inline)) {
+        return kMarks + ((s >> 1) & (Gm::slots - 1)) * Gm::mark_slot;
     };
-    auto marks_of = [&](uint32_t s) { return lds + 2 * kSlot + ((s >> 1) & 1) * kMarkSlot; };
-    auto window = [&](uint32_t s) { return min(2 * s & ~3u, granules - 4); };   // first granule of s's scales
+    auto copy_stage = [&](uint32_t s) __attribute__((always_inline)) {
+        const uint32_t k = min(2 * s, granules - 2) * 64;
+        static_for<Gm::copies>([&](auto I) __attribute__((always_inline)) { copy(I, base + slot_of(s), k); });
+        if ((s & 1) == 0) copy_marks(base + mark_slot_of(s), min(2 * s, granules - 4) * 4);
+    };
 
-    f32x16_t acc[4][4] = {};
-    copy_stage(0);
-    if (stages > 1) copy_stage(1);
-    wait_and_meet();
-    Fragments f, h;
-    Scales e;
-    read(lds, 4 * half, f);
-    read_scales(marks_of(0), half, e);
+    // fragments: wave w computes rows 32*FM*(w&1) of A against rows 32*FN*(w>>1) of B
+    const int r = lane & 31, half = lane >> 5, x = (lane >> 1) & 7;
+    const uint32_t arow = (wave & 1) * 32 * FM + r, brow = Gm::TM + (wave >> 1) * 32 * FN + r;
+    // where piece 4 * half of the first fragment lies in slot 0; pieces p and q of a row
+    // differ by the bits of 16 * (p ^ q)
+    const uint32_t a_at = base + arow * 128 + ((4 * half) ^ x) * 16;
+    const uint32_t b_at = base + brow * 128 + ((4 * half) ^ x) * 16;
+    const uint32_t a_marks = base + arow * 16, b_marks = base + brow * 16;   // + mark_slot_of
+    // the n-th of the fragments' pieces at la, lb and those at the piece beside, in the
+    // order the products use them
+    using Frag = Fragments<FM, FN>;
+    using Scale = Scales<FM, FN>;
+    auto read = [&](auto I, uint32_t la, uint32_t lb, Frag &f) __attribute__((always_inline)) {
+        constexpr int n = I, u = n / (FM + FN), q = n % (FM + FN);
+        if constexpr (q < FN) f.b[q][u] = lds16((lb ^ (16 * u)) + q * 4096);
+        else f.a[q - FN][u] = lds16((la ^ (16 * u)) + (q - FN) * 4096);
+    };
+    // pieces p and p ^ 1 beyond 4 * half of the slot of stage s
+    auto read_all = [&](uint32_t s, uint32_t p, Frag &f) __attribute__((always_inline)) {
+        const uint32_t la = (a_at ^ (16 * p)) + slot_of(s), lb = (b_at ^ (16 * p)) + slot_of(s);
+        static_for<Gm::reads>([&](auto I) __attribute__((always_inline)) { read(I, la, lb, f); });
+    };
+    // the scales of one granule, at dword k of the group of stage s
+    auto read_scales = [&](uint32_t s, uint32_t k, Scale &e) __attribute__((always_inline)) {
+        const uint32_t at = mark_slot_of(s) + 4 * k;
+#pragma unroll
+        for (int i = 0; i < FM; i++) e.a[i] = lds4(a_marks + at + i * 512);
+#pragma unroll
+        for (int i = 0; i < FN; i++) e.b[i] = lds4(b_marks + at + i * 512);
+    };
+    const uint32_t upper = half ? ~0u : 0u;                // all bits in the upper half-wave
+    auto pick = [&](uint32_t lo, uint32_t up) __attribute__((always_inline)) { return (lo & ~upper) | (up & upper); };
+    auto window = [&](uint32_t s) __attribute__((always_inline)) { return min((2 * s) & ~3u, granules - 4); };   // first granule of s's scales
 
-    // the 32 products of phase P of a stage, in the order written: after product n
-    // come the n-th read of the next phase's fragments, and with COPY the n-th copy
-    // of the stage at byte k of the rows, so the matrix cores never wait for the rest
-    // to issue.  GROUP: also the scales of the next 4 granules, and the copy of those
-    // after them.
-    uint4 ga[4], gb[4];
-    auto phase = [&](auto P, const Fragments &now, Fragments &then, const uint8_t *codes, auto COPY,
-                     uint32_t to, uint32_t k, auto READ_GROUP, const uint8_t *marks, auto COPY_GROUP,
-                     uint32_t marks_to) {
-        constexpr int ph = P;
-        const uint32_t p0 = ((4 * half + (ph ? 0 : 2)) ^ x) * 16;
-        static_for<32>([&](auto S) {
-            constexpr int s = S, t = s / 16, i = s / 4 % 4, n = s % 4;
-            acc[i][n] = mma<2 * ph + t>(now.b[n][t], e.b[n], now.a[i][t], e.a[i], acc[i][n]);
-            if constexpr (s < 16) {
-                constexpr int u = s / 8, r4 = s % 4;
-                if constexpr (s % 8 < 4) then.b[r4][u] = *(const uint4 *)(codes + (brow + 32 * r4) * 128 + (p0 ^ (16 * u)));
-                else then.a[r4][u] = *(const uint4 *)(codes + (arow + 32 * r4) * 128 + (p0 ^ (16 * u)));
-            } else if constexpr (READ_GROUP && s < 20) {
-                gb[s - 16] = *(const uint4 *)(marks + (brow + 32 * (s - 16)) * 16);
-            } else if constexpr (READ_GROUP && s < 24) {
-                ga[s - 20] = *(const uint4 *)(marks + (arow + 32 * (s - 20)) * 16);
-            }
+    f32x16_t acc[FM][FN] = {};
+    Frag f, h;
+    Scale e;
+    u32x4_t ga[FM], gb[FN];
+    // the n-th product of phase P
+    auto product = [&](auto P, auto I, const Frag &v) __attribute__((always_inline)) {
+        constexpr int ph = P, n = I, u = n / (FM * FN), i = n / FN % FM, j = n % FN;
+        acc[i][j] = mma<2 * ph + u>(v.b[j][u], e.b[j], v.a[i][u], e.a[i], acc[i][j]);
+    };
+    auto products = [&](auto P, const Frag &v) __attribute__((always_inline)) {
+        static_for<Gm::ops>([&](auto I) __attribute__((always_inline)) { product(P, I, v); });
+    };
+    // the products of phase P of a stage, in the order written: between them the
+    // reads of the next phase's fragments, from the slot at `from`, and with COPY the
+    // copies of stage `next`, so the matrix cores never wait for the rest to issue.
+    // GROUP_READ: also the scales of the group at `marks`; GROUP_COPY: the copy of
+    // those of stage `next`.
+    auto phase = [&](auto P, const Frag &now, Frag &then, uint32_t from, auto COPY, uint32_t next,
+                     auto GROUP_READ, uint32_t marks, auto GROUP_COPY) __attribute__((always_inline)) {
+        constexpr int S = Gm::ops;
+        const uint32_t to = base + slot_of(next), k = next * 128;
+        uint32_t la = a_at, lb = b_at;
+        asm volatile("" : "+v"(la), "+v"(lb));   // addresses made here, not kept for every phase
+        la = (la ^ (P ? 0 : 32)) + from;
+        lb = (lb ^ (P ? 0 : 32)) + from;
+        static_for<S>([&](auto I) __attribute__((always_inline)) {
+            constexpr int n = I;
+            product(P, I, now);
+            // reads in the first half of the phase, copies too
+            constexpr int r0 = n * 2 * Gm::reads / S, r1 = (n + 1) * 2 * Gm::reads / S;
+            static_for<r1 - r0>([&](auto Q) __attribute__((always_inline)) {
+                constexpr int q = r0 + Q, g = q - Gm::reads;
+                if constexpr (q < Gm::reads) read(std::integral_constant<int, q>{}, la, lb, then);
+                else if constexpr (GROUP_READ && g < FN) gb[g] = lds16(b_marks + marks + g * 512);
+                else if constexpr (GROUP_READ && g < FN + FM) ga[g - FN] = lds16(a_marks + marks + (g - FN) * 512);
+            });
             if constexpr (COPY) {
-                if constexpr (s < 8) copy_to_lds(to + s * 1024, va[s], ra, k);
-                else if constexpr (s < 16) copy_to_lds(to + kTile * 128 + (s - 8) * 1024, vb[s - 8], rb, k);
-                else if constexpr (COPY_GROUP && s == 16) copy_to_lds(marks_to, vsa, rsa, k / 16);
-                else if constexpr (COPY_GROUP && s == 17) copy_to_lds(marks_to + kTile * 16, vsb, rsb, k / 16);
+                constexpr int c0 = n * 2 * Gm::copies / S, c1 = (n + 1) * 2 * Gm::copies / S;
+                static_for<c1 - c0>([&](auto Q) __attribute__((always_inline)) {
+                    constexpr int q = c0 + Q;
+                    if constexpr (q < Gm::copies) copy(std::integral_constant<int, q>{}, to, k);
+                });
+                if constexpr (GROUP_COPY && n == S / 2) copy_marks(base + mark_slot_of(next), k / 16);
             }
             __builtin_amdgcn_sched_barrier(0);
         });
@@ -311,87 +364,218 @@ __global__ __launch_bounds__(kThreads, 1) void k_mx_matmul_big(
     using no = std::integral_constant<int, 0>;
     using yes = std::integral_constant<int, 1>;
 
-    // two stages at a time while there are two more to copy: every window then lies
-    // where the stage number says
+    static_for<Gm::slots>([&](auto Q) __attribute__((always_inline)) {
+        if ((uint32_t)Q < stages) copy_stage((uint32_t)Q);
+    });
+    wait_and_meet<0>();
+    read_all(0, 0, f);
+    read_scales(0, half, e);
+
+    // two stages at a time while there are enough more to copy: every window then lies
+    // where the stage number says, and `ahead` copies follow those waited for
     uint32_t s = 0;
     const uint32_t full = granules / 2;
-    if (full >= 4) {
-        const uint32_t codes_to = base + wave * 64 * 128, marks_to = base + 2 * kSlot + wave * 64 * 16;
+    if (full >= 2 + Gm::slots) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            ga[i] = *(const uint4 *)(marks_of(0) + (arow + 32 * i) * 16);
-            gb[i] = *(const uint4 *)(marks_of(0) + (brow + 32 * i) * 16);
-        }
-        for (; s + 4 <= full; s += 2) {
-            const uint32_t next = ((s >> 1) & 1) ^ 1;
-            phase(no{}, f, h, lds, no{}, 0, 0, no{}, lds, no{}, 0);
-            wait_and_meet();
-            phase(yes{}, h, f, lds + kSlot, yes{}, codes_to, (s + 2) * 128, no{}, lds, yes{},
-                  marks_to + next * kMarkSlot);
+        for (int i = 0; i < FM; i++) ga[i] = lds16(a_marks + kMarks + i * 512);
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                e.a[i] = half ? ga[i].w : ga[i].z;
-                e.b[i] = half ? gb[i].w : gb[i].z;
-            }
-            phase(no{}, f, h, lds + kSlot, no{}, 0, 0, no{}, lds, no{}, 0);
-            wait_and_meet();
-            phase(yes{}, h, f, lds, yes{}, codes_to + kSlot, (s + 3) * 128, yes{},
-                  lds + 2 * kSlot + next * kMarkSlot, no{}, 0);
+        for (int i = 0; i < FN; i++) gb[i] = lds16(b_marks + kMarks + i * 512);
+        for (; s + 2 + Gm::slots <= full; s += 2) {
+            const uint32_t s0 = slot_of(s), s1 = slot_of(s + 1), s2 = slot_of(s + 2);
+            phase(no{}, f, h, s0, no{}, 0, no{}, 0, no{});
+            wait_and_meet<Gm::ahead>();
+            phase(yes{}, h, f, s1, yes{}, s + Gm::slots, no{}, 0, yes{});
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                e.a[i] = half ? ga[i].y : ga[i].x;
-                e.b[i] = half ? gb[i].y : gb[i].x;
-            }
+            for (int i = 0; i < FM; i++) e.a[i] = pick(ga[i].z, ga[i].w);
+#pragma unroll
+            for (int i = 0; i < FN; i++) e.b[i] = pick(gb[i].z, gb[i].w);
+            phase(no{}, f, h, s1, no{}, 0, no{}, 0, no{});
+            wait_and_meet<Gm::ahead>();
+            phase(yes{}, h, f, s2, yes{}, s + 1 + Gm::slots, yes{}, mark_slot_of(s + 2), no{});
+#pragma unroll
+            for (int i = 0; i < FM; i++) e.a[i] = pick(ga[i].x, ga[i].y);
+#pragma unroll
+            for (int i = 0; i < FN; i++) e.b[i] = pick(gb[i].x, gb[i].y);
         }
         // the group's scales may have come from a window that is pulled back
-        read_scales(marks_of(s), 2 * s - window(s) + half, e);
+        read_scales(s, 2 * s - window(s) + half, e);
     }
     for (; s < full; s++) {
-        read(lds + (s & 1) * kSlot, 4 * half + 2, h);
-        products<0>(f, e, acc);
-        wait_and_meet();
-        if (s + 2 < stages) copy_stage(s + 2);
-        products<1>(h, e, acc);
+        read_all(s, 2, h);
+        products(no{}, f);
+        wait_and_meet<0>();
+        if (s + Gm::slots < stages) copy_stage(s + Gm::slots);
+        products(yes{}, h);
         if (s + 1 < full) {
-            read(lds + ((s + 1) & 1) * kSlot, 4 * half, f);
-            read_scales(marks_of(s + 1), 2 * s + 2 - window(s + 1) + half, e);
+            read_all(s + 1, 0, f);
+            read_scales(s + 1, 2 * s + 2 - window(s + 1) + half, e);
         }
     }
-    if (granules & 1) {                                  // the last granule, alone
-        read(lds + (full & 1) * kSlot, 4 + 2 * half, f);
-        read_scales(marks_of(full), granules - 1 - window(full), e);
+    if (granules & 1) {                                  // the last granule, alone: pieces 4 + 2 * half
+        read_all(full, 4 ^ (6 * half), f);
+        read_scales(full, granules - 1 - window(full), e);
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            e.a[i] >>= 16 * half;
-            e.b[i] >>= 16 * half;
-        }
-        products<0>(f, e, acc);
+        for (int i = 0; i < FM; i++) e.a[i] >>= 16 * half;
+#pragma unroll
+        for (int i = 0; i < FN; i++) e.b[i] >>= 16 * half;
+        products(no{}, f);
     }
 
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int64_t m = m0 + (wave & 1) * 128 + 32 * i + r;
+    for (int i = 0; i < FM; i++) {
+        const int64_t m = m0 + (wave & 1) * 32 * FM + 32 * i + r;
         if (m >= M) continue;
 #pragma unroll
-        for (int j = 0; j < 4; j++)
+        for (int j = 0; j < FN; j++)
 #pragma unroll
             for (int q = 0; q < 4; q++) {
-                const int64_t n = n0 + (wave >> 1) * 128 + 32 * j + 8 * q + 4 * half;
+                const int64_t n = n0 + (wave >> 1) * 32 * FN + 32 * j + 8 * q + 4 * half;
                 const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
                 store4<CT>(c, m * ldc + n, N - n < 4 ? (int)(N - n) : 4, v);
             }
     }
 }
 
+template <int FM, int FN, int CT>
+hipError_t run_tiled(const uint8_t *a, const uint8_t *as, const uint8_t *b, const uint8_t *bs, int64_t M,
+                     int64_t N, int64_t granules, void *c, int64_t ldc, hipStream_t st) {
+    using Gm = tgeom<FM, FN>;
+    const int64_t mt = (M + Gm::TM - 1) / Gm::TM, nt = (N + Gm::TN - 1) / Gm::TN;
+    hipLaunchKernelGGL((k_mx_matmul_tiled<FM, FN, CT>), dim3((unsigned)(mt * nt)), dim3(kThreads), 0, st, a,
+                       as, b, bs, M, N, (uint32_t)granules, (uint32_t)mt, (uint32_t)nt, c, ldc);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Few rows of A (a token, a small batch): 16*FA rows against 16*FB rows of B.
+// ---------------------------------------------------------------------------
+// Bound: reading B once.  v_mfma_scale_f32_16x16x128_f8f6f4 takes 16 rows, so N/16
+// work-groups; the WV waves of one deal out K in steps of 512 and add their sums in
+// LDS in a fixed order, so a few rows still fill the GPU, without a second launch.  Of a step's 4 granules
+// a quarter-wave takes one: a lane reads 64 consecutive bytes of its row and one
+// dword of scales, a row of the fragment 256.  Operands go straight to registers, a
+// whole step's loads at a time.
+template <int T>
+__device__ __forceinline__ f32x4_t mma16(u32x4_t a, uint32_t sa, u32x4_t b, uint32_t sb, f32x4_t c) {
+    const i32x8_t av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+    const i32x8_t bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, T, (int)sa, T, (int)sb);
+}
+
+template <int F> struct StepOf {
+    u32x4_t v[F][4];
+    uint32_t s[F];
+};
+
+template <int FA, int FB, int WV, int CT>
+__global__ __launch_bounds__(64 * WV) void k_mx_matmul_rows(
+    const uint8_t *__restrict__ a, const uint8_t *__restrict__ as, const uint8_t *__restrict__ b,
+    const uint8_t *__restrict__ bs, int64_t M, int64_t N, int64_t granules, void *__restrict__ c, int64_t ldc) {
+    __shared__ f32x4_t sums[WV][FA * FB][64];
+    const int wave = __builtin_amdgcn_readfirstlane((int)(__builtin_amdgcn_workitem_id_x() >> 6)), lane = lane_id();
+    const int row = lane & 15, quarter = lane >> 4;
+    const int64_t n0 = (int64_t)__builtin_amdgcn_workgroup_id_x() * (16 * FB), m0 = group_y() * (16 * FA);
+    const uint8_t *pa[FA], *qa[FA], *pb[FB], *qb[FB];
+#pragma unroll
+    for (int i = 0; i < FA; i++) {
+        const int64_t m = min(m0 + 16 * i + row, M - 1) * granules + quarter;
+        pa[i] = a + m * 64;
+        qa[i] = as + m * 4;
+    }
+#pragma unroll
+    for (int i = 0; i < FB; i++) {
+        const int64_t n = min(n0 + 16 * i + row, N - 1) * granules + quarter;
+        pb[i] = b + n * 64;
+        qb[i] = bs + n * 4;
+    }
+    auto load = [&](int64_t g, auto &f, const uint8_t *const *p, const uint8_t *const *q, auto F) __attribute__((always_inline)) {
+        static_for<F>([&](auto I) __attribute__((always_inline)) {
+            constexpr int i = I;
+            if (g + quarter < granules) {
+#pragma unroll
+                for (int t = 0; t < 4; t++) f.v[i][t] = *(const u32x4_t *)(p[i] + g * 64 + 16 * t);
+                f.s[i] = *(const uint32_t *)(q[i] + g * 4);
+            } else {
+#pragma unroll
+                for (int t = 0; t < 4; t++) f.v[i][t] = u32x4_t{0, 0, 0, 0};
+                f.s[i] = 0;
+            }
+        });
+    };
+    f32x4_t acc[FA][FB] = {};
+    for (int64_t g = 4 * wave; g < granules; g += 4 * WV) {
+        StepOf<FA> fa;
+        StepOf<FB> fb;
+        load(g, fb, pb, qb, std::integral_constant<int, FB>{});
+        load(g, fa, pa, qa, std::integral_constant<int, FA>{});
+        static_for<4>([&](auto T) __attribute__((always_inline)) {
+            constexpr int t = T;
+#pragma unroll
+            for (int i = 0; i < FA; i++)
+#pragma unroll
+                for (int j = 0; j < FB; j++) acc[i][j] = mma16<t>(fb.v[j][t], fb.s[j], fa.v[i][t], fa.s[i], acc[i][j]);
+        });
+    }
+#pragma unroll
+    for (int i = 0; i < FA; i++)
+#pragma unroll
+        for (int j = 0; j < FB; j++) sums[wave][i * FB + j][lane] = acc[i][j];
+    __syncthreads();
+    // a lane's 4 sums are consecutive n of one m
+    for (int k = wave; k < FA * FB; k += WV) {
+        f32x4_t v = sums[0][k][lane];
+#pragma unroll
+        for (int w = 1; w < WV; w++) v += sums[w][k][lane];
+        const int64_t m = m0 + 16 * (k / FB) + row, n = n0 + 16 * (k % FB) + 4 * quarter;
+        const float r[4] = {v.x, v.y, v.z, v.w};
+        if (m < M && n < N) store4<CT>(c, m * ldc + n, N - n < 4 ? (int)(N - n) : 4, r);
+    }
+}
+
+template <int FA, int FB, int CT>
+hipError_t run_rows(const uint8_t *a, const uint8_t *as, const uint8_t *b, const uint8_t *bs, int64_t M,
+                    int64_t N, int64_t granules, void *c, int64_t ldc, hipStream_t st) {
+    const dim3 grid((unsigned)((N + 16 * FB - 1) / (16 * FB)), (unsigned)((M + 16 * FA - 1) / (16 * FA)));
+    const int64_t groups = (int64_t)grid.x * grid.y, steps = (granules + 3) / 4;
+    // enough waves to cover the latency of memory, each with a step at least
+    const int wv = groups * 4 >= 4096 || steps <= 4 ? 4 : groups * 8 >= 2048 || steps <= 8 ? 8 : 16;
+    if (wv == 4)
+        hipLaunchKernelGGL((k_mx_matmul_rows<FA, FB, 4, CT>), grid, dim3(256), 0, st, a, as, b, bs, M, N, granules, c, ldc);
+    else if (wv == 8)
+        hipLaunchKernelGGL((k_mx_matmul_rows<FA, FB, 8, CT>), grid, dim3(512), 0, st, a, as, b, bs, M, N, granules, c, ldc);
+    else
+        hipLaunchKernelGGL((k_mx_matmul_rows<FA, FB, 16, CT>), grid, dim3(1024), 0, st, a, as, b, bs, M, N, granules, c, ldc);
+    return hipGetLastError();
+}
+
 template <int CT>
 hipError_t run_matmul(const uint8_t *a, const uint8_t *as, const uint8_t *b, const uint8_t *bs,
                       int64_t M, int64_t N, int64_t granules, void *c, int64_t ldc, hipStream_t st) {
-    if (M > 128 && N > 128 && granules >= 4 && granules < (1 << 18)) {
-        const int64_t bm = (M + kTile - 1) / kTile, bn = (N + kTile - 1) / kTile;
-        hipLaunchKernelGGL((k_mx_matmul_big<CT>), dim3((unsigned)(bm * bn)), dim3(kThreads), 0, st, a, as, b,
-                           bs, M, N, (uint32_t)granules, (uint32_t)bm, (uint32_t)bn, c, ldc);
-        return hipGetLastError();
+    const auto tiles = [&](int64_t m, int64_t n) { return ((M + m - 1) / m) * ((N + n - 1) / n); };
+    // Few rows: one pass over B by as many work-groups as it has 16 rows; also for more
+    // rows of A where 64 x 64 tiles would leave most of the GPU idle and K is short
+    // (64 x 4096, K = 4096: 8.5 us warm and 10.0 cold against 7.4 and 12.1; 77 x 1001,
+    // K = 1111: 4.6 and 4.6 against 4.7 and 5.6; but 200 x 520, K = 8192: 13.4 and 14.2
+    // against 10.4 and 14.1).  32 x 28672, K = 8192 is 1792 work-groups of rows and 448
+    // tiles: 50 us and 58 against 21 and 53.
+    const int64_t small = tiles(64, 64), middle = tiles(128, 128), large = tiles(256, 256);
+    const bool staged = granules >= 4 && granules < (1 << 18) && small <= kMaxGroups;
+    const bool rows = (N + 15) / 16 <= kMaxGroups;
+    if (rows && M <= 16) return run_rows<1, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
+    if (rows && M <= 32 && (small < 128 || !staged)) return run_rows<2, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
+    if (rows && small <= 64 && granules <= 32) return run_rows<4, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
+    if (staged) {
+        // 64 x 64 while they fit the GPU twice over (512 x 4096, K = 4096: 12.6 us
+        // against 13.2 with 128 x 128); then whichever of 128 x 128, of which the GPU
+        // holds 512, and 256 x 256, 256 at a time, has the shorter rounds: a full round
+        // of the former takes 0.63 of the latter's (8192 x 8192, K = 28672: 1177 us
+        // against 917; 2048 x 4096, K = 14336, 512 tiles against 128: 80 us against 93)
+        if (small <= 512) return run_tiled<1, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
+        if (63 * ((middle + 511) / 512) < 100 * ((large + 255) / 256))
+            return run_tiled<2, 2, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
+        return run_tiled<4, 4, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
     }
+    // K below 4 granules, or too long for 32-bit offsets within a tile
     const int64_t mt = (M + 127) / 128, nt = (N + 127) / 128;
     if (mt * nt > kMaxGroups) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_mx_matmul<CT>), dim3((unsigned)(mt * nt)), dim3(kThreads), 0, st, a, as, b, bs, M,
