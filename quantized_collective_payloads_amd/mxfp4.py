@@ -3,12 +3,18 @@ a linear layer whose three products run on it (mxfp4_* of include/qcp.h).
 
 A payload of `lines` rows of n values is a pair (codes, scales): uint8
 [lines, P/2] and uint8 [lines, P/32] with P = n rounded up to whole 128s.
+
+The kernels for small sizes take a few microseconds, so each function first asks
+what every valid call answers with yes, in as few questions as it can, and goes
+through the checks that name the fault only where the answer is no.
 """
 from __future__ import annotations
 
 import torch
 
-from . import (DTYPES, _check, _dev, _dtype_code, _ELEMS, _need, _ptr, _stream, _U8, library)
+from . import (DTYPES, _dev, _dtype_code, _ELEMS, _enqueue, _need, _U8, library)
+
+_u8 = torch.uint8
 
 
 def mxfp4_padded(n: int) -> int:
@@ -17,6 +23,10 @@ def mxfp4_padded(n: int) -> int:
     if p < 0:
         raise ValueError(f"row length {n} is negative or too large")
     return p
+
+
+def _pad(n: int) -> int:
+    return (n + 127) // 128 * 128
 
 
 def _matrix(x, what: str):
@@ -30,7 +40,15 @@ def _matrix(x, what: str):
 
 
 def _payload(codes, scales, what: str):
-    """(lines, padded row length) of a payload after checking its two tensors."""
+    """(lines, padded row length, GPU) of a payload after checking its two tensors;
+    the GPU is -1 for CPU tensors."""
+    try:
+        (lines, cb), shape, index = codes.shape, scales.shape, codes.get_device()
+        if (codes.dtype is _u8 and scales.dtype is _u8 and cb % 64 == 0 and shape == (lines, cb // 16)
+                and index == scales.get_device() and codes.is_contiguous() and scales.is_contiguous()):
+            return lines, 2 * cb, index
+    except (AttributeError, ValueError):
+        pass
     for t, name, unit in ((codes, "codes", 64), (scales, "scales", 4)):
         _need(t, f"{what}{name}", _U8, 0)
         if t.dim() != 2:
@@ -40,7 +58,28 @@ def _payload(codes, scales, what: str):
     if scales.shape != (codes.shape[0], codes.shape[1] // 16):
         raise ValueError(f"{what}scales: shape {tuple(scales.shape)} for codes of {tuple(codes.shape)}, "
                          f"expected {(codes.shape[0], codes.shape[1] // 16)}")
-    return codes.shape[0], 2 * codes.shape[1]
+    _dev(codes, scales)
+    raise ValueError(f"{what}codes: not a payload")
+
+
+def _result(out, rows: int, cols: int, dtype, like):
+    """The output tensor: the caller's after its checks, or a new one."""
+    if out is None:
+        if dtype not in DTYPES:
+            _dtype_code(dtype)
+        return torch.empty((rows, cols), dtype=dtype, device=like.device)
+    _matrix(out, "out")
+    _need(out, "out", _ELEMS, 0)
+    if tuple(out.shape) != (rows, cols):
+        raise ValueError(f"out: shape {tuple(out.shape)}, expected {(rows, cols)}")
+    return out
+
+
+def _same_gpu(index: int, *ts):
+    """All on GPU `index`; else the fault's name."""
+    if index < 0 or any(t.get_device() != index for t in ts):
+        _dev(*ts)
+        raise ValueError("qcp: tensors on different devices")
 
 
 def mxfp4_quantize(x: torch.Tensor, transpose: bool = False, codes=None, scales=None):
@@ -48,78 +87,94 @@ def mxfp4_quantize(x: torch.Tensor, transpose: bool = False, codes=None, scales=
     `transpose` of x.t().  Rows may lie any distance apart, and a transposed view
     is read where it is; other strides are copied first.  Caller-supplied `codes`
     and `scales` must be contiguous uint8 of the payload's shape."""
-    _matrix(x, "x")
-    if x.numel() and x.stride(1) != 1 and x.shape[1] != 1:
-        if x.stride(0) == 1 or x.shape[0] == 1:
-            x, transpose = x.t(), not transpose
-        else:
-            x = x.contiguous()
+    if type(x) is not torch.Tensor or x.dim() != 2 or x.dtype not in DTYPES:
+        _matrix(x, "x")
     rows, cols = x.shape
-    ld = x.stride(0) if rows > 1 else cols
-    if rows > 1 and ld < cols:                       # rows that overlap (an expanded tensor)
-        x = x.contiguous()
-        ld = cols
+    ld = cols
+    if not x.is_contiguous():
+        if x.numel() and x.stride(1) != 1 and cols != 1:
+            if x.stride(0) == 1 or rows == 1:
+                x, transpose = x.t(), not transpose
+                rows, cols = cols, rows
+            else:
+                x = x.contiguous()
+        ld = x.stride(0) if rows > 1 else cols
+        if ld < cols:                                # rows that overlap (an expanded tensor)
+            x, ld = x.contiguous(), cols
     lines, n = (cols, rows) if transpose else (rows, cols)
-    P = mxfp4_padded(n)
+    P = _pad(n)
+    index = x.get_device()
     for t, what, shape in ((codes, "codes", (lines, P // 2)), (scales, "scales", (lines, P // 32))):
         if t is not None:
             _need(t, what, _U8, 0)
             if tuple(t.shape) != shape:
                 raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
-    dev = _dev(x, codes, scales)
+            _same_gpu(index, x, t)
+    if index < 0:
+        _dev(x)
     if codes is None:
-        codes = torch.empty((lines, P // 2), dtype=torch.uint8, device=dev)
+        codes = torch.empty((lines, P // 2), dtype=_u8, device=x.device)
     if scales is None:
-        scales = torch.empty((lines, P // 32), dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        _check("mxfp4_quantize", library().mxfp4_quantize(
-            _ptr(x), DTYPES[x.dtype], rows, cols, ld, int(bool(transpose)), _ptr(codes), _ptr(scales),
-            _stream(dev)))
+        scales = torch.empty((lines, P // 32), dtype=_u8, device=x.device)
+    _enqueue("mxfp4_quantize", index, x.data_ptr(), DTYPES[x.dtype], rows, cols, ld, 1 if transpose else 0,
+             codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int, dtype=torch.bfloat16, out=None):
     """The [lines, cols] values that a payload stands for, rounded once to `dtype`."""
-    lines, P = _payload(codes, scales, "")
-    if mxfp4_padded(cols) != P:
+    lines, P, index = _payload(codes, scales, "")
+    if cols < 0 or _pad(cols) != P:
         raise ValueError(f"codes: rows of {P} values for {cols} columns, expected {mxfp4_padded(cols)}")
-    if out is not None:
-        _matrix(out, "out")
-        _need(out, "out", _ELEMS, 0)
-        if tuple(out.shape) != (lines, cols):
-            raise ValueError(f"out: shape {tuple(out.shape)}, expected {(lines, cols)}")
-    dev = _dev(codes, scales, out)
-    if out is None:
-        _dtype_code(dtype)
-        out = torch.empty((lines, cols), dtype=dtype, device=dev)
-    with torch.cuda.device(dev):
-        _check("mxfp4_dequantize", library().mxfp4_dequantize(
-            _ptr(codes), _ptr(scales), lines, cols, _ptr(out), DTYPES[out.dtype], cols, _stream(dev)))
-    return out
+    if index < 0 or out is not None:
+        _same_gpu(index, codes, *(() if out is None else (_result(out, lines, cols, dtype, codes),)))
+    y = _result(out, lines, cols, dtype, codes)
+    _enqueue("mxfp4_dequantize", index, codes.data_ptr(), scales.data_ptr(), lines, cols, y.data_ptr(),
+             DTYPES[y.dtype], cols)
+    return y
 
 
 def mxfp4_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor,
                  b_scales: torch.Tensor, dtype=torch.bfloat16, out=None):
     """A B^T for the payloads of A [M, K] and B [N, K]: [M, N] in `dtype`,
     accumulated in fp32 and rounded once."""
-    M, K = _payload(a_codes, a_scales, "a_")
-    N, Kb = _payload(b_codes, b_scales, "b_")
+    M, K, index = _payload(a_codes, a_scales, "a_")
+    N, Kb, other = _payload(b_codes, b_scales, "b_")
     if K != Kb:
         raise ValueError(f"b_codes: rows of {Kb} values, a_codes of {K}")
-    if out is not None:
-        _matrix(out, "out")
-        _need(out, "out", _ELEMS, 0)
-        if tuple(out.shape) != (M, N):
-            raise ValueError(f"out: shape {tuple(out.shape)}, expected {(M, N)}")
-    dev = _dev(a_codes, a_scales, b_codes, b_scales, out)
-    if out is None:
-        _dtype_code(dtype)
-        out = torch.empty((M, N), dtype=dtype, device=dev)
-    with torch.cuda.device(dev):
-        _check("mxfp4_matmul", library().mxfp4_matmul(
-            _ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales), M, N, K, _ptr(out),
-            DTYPES[out.dtype], N, _stream(dev)))
-    return out
+    if index < 0 or index != other or out is not None:
+        _same_gpu(index, a_codes, b_codes, *(() if out is None else (_result(out, M, N, dtype, a_codes),)))
+    c = _result(out, M, N, dtype, a_codes)
+    _enqueue("mxfp4_matmul", index, a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(),
+             b_scales.data_ptr(), M, N, K, c.data_ptr(), DTYPES[c.dtype], N)
+    return c
+
+
+class _Work:
+    """Payloads of one call in one allocation; only their addresses are needed."""
+
+    def __init__(self, like, *shapes):
+        at, self.places = 0, []
+        for lines, n in shapes:
+            P = _pad(n)
+            self.places.append((at, at + lines * P // 2))
+            at += lines * P // 2 + (lines * P // 32 + 15) // 16 * 16
+        self.buffer = torch.empty(at, dtype=_u8, device=like.device)
+        self.base = self.buffer.data_ptr()
+
+    def __getitem__(self, k):
+        codes, scales = self.places[k]
+        return self.base + codes, self.base + scales
+
+
+def _quantize_to(index, x, rows, cols, ld, transpose, place):
+    _enqueue("mxfp4_quantize", index, x.data_ptr(), DTYPES[x.dtype], rows, cols, ld, transpose, *place)
+
+
+def _product(index, a, b, M, N, K, dtype, like):
+    c = torch.empty((M, N), dtype=dtype, device=like.device)
+    _enqueue("mxfp4_matmul", index, *a, *b, M, N, K, c.data_ptr(), DTYPES[dtype], N)
+    return c
 
 
 class _Linear(torch.autograd.Function):
@@ -130,21 +185,36 @@ class _Linear(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w):
-        y = mxfp4_matmul(*mxfp4_quantize(x), *mxfp4_quantize(w), dtype=x.dtype)
-        kept = mxfp4_quantize(x, transpose=True) if ctx.needs_input_grad[1] else (None, None)
-        ctx.save_for_backward(w if ctx.needs_input_grad[0] else None, *kept)
-        ctx.kinds = x.dtype, w.dtype
+        index, (T, I), O = x.get_device(), x.shape, w.shape[0]
+        need_x, need_w = ctx.needs_input_grad
+        work = _Work(x, (T, I), (O, I))
+        _quantize_to(index, x, T, I, I, 0, work[0])
+        _quantize_to(index, w, O, I, I, 0, work[1])
+        y = _product(index, work[0], work[1], T, O, I, x.dtype, x)
+        kept = None
+        if need_w:
+            kept = _Work(x, (I, T))
+            _quantize_to(index, x, T, I, I, 1, kept[0])
+        ctx.save_for_backward(w if need_x else None, kept and kept.buffer)
+        ctx.kinds, ctx.sizes, ctx.place = (x.dtype, w.dtype), (T, I, O), kept and kept.places[0]
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        w, xc, xs = ctx.saved_tensors
-        dx = dw = None
+        w, kept = ctx.saved_tensors
+        T, I, O = ctx.sizes
+        index, dx, dw = dy.get_device(), None, None
+        dy = dy.contiguous()
+        work = _Work(dy, *([(T, O), (I, O)] if w is not None else []), *([(O, T)] if kept is not None else []))
         if w is not None:
-            dx = mxfp4_matmul(*mxfp4_quantize(dy), *mxfp4_quantize(w, transpose=True), dtype=ctx.kinds[0])
-        if xc is not None:
-            dw = mxfp4_matmul(*mxfp4_quantize(dy, transpose=True), xc, xs, dtype=ctx.kinds[1])
+            _quantize_to(index, dy, T, O, O, 0, work[0])
+            _quantize_to(index, w, O, I, I, 1, work[1])
+            dx = _product(index, work[0], work[1], T, I, O, ctx.kinds[0], dy)
+        if kept is not None:
+            _quantize_to(index, dy, T, O, O, 1, work[-1])
+            base = kept.data_ptr()
+            dw = _product(index, work[-1], (base + ctx.place[0], base + ctx.place[1]), O, I, T, ctx.kinds[1], dy)
         return dx, dw
 
 
@@ -157,7 +227,8 @@ def mxfp4_linear(x: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
         raise ValueError("x: expected a torch.Tensor with at least one dimension")
     if x.shape[-1] != weight.shape[1]:
         raise ValueError(f"x: last dimension {x.shape[-1]}, weight's {weight.shape[1]}")
-    _matrix(x.reshape(-1, x.shape[-1]) if x.dim() != 2 else x, "x")
-    _dev(x, weight)
-    y = _Linear.apply(x if x.dim() == 2 else x.reshape(-1, x.shape[-1]), weight)
+    x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+    _matrix(x2, "x")
+    _same_gpu(x.get_device(), x, weight)
+    y = _Linear.apply(x2.contiguous(), weight.contiguous())
     return y if x.dim() == 2 else y.view(*x.shape[:-1], weight.shape[0])

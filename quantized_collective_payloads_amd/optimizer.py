@@ -13,8 +13,7 @@ import ctypes
 
 import torch
 
-from . import (DTYPES, FORMATS, _check, _check_n_G, _dev, _ELEMS, _F32, _need, _ptr, _stream, _U8,
-               library, n_blocks)
+from . import (DTYPES, FORMATS, _check_n_G, _dev, _ELEMS, _enqueue, _F32, _need, _U8, n_blocks)
 
 _STATES = {"f32": DTYPES[torch.float32], "e4m3": FORMATS["e4m3"]}
 _COPIES = (torch.float16, torch.bfloat16)
@@ -40,60 +39,73 @@ class AdamW:
              uint8 codes with n_state/G scales.
 
     The tensors must keep their storage: a step on a parameter that was given
-    another one since raises ValueError.
+    another one since raises ValueError.  The attributes are read-only.
     """
+
+    params = property(lambda self: self._params)
+    copies = property(lambda self: self._copies)
+    state = property(lambda self: self._state)
+    G = property(lambda self: self._G)
+    m = property(lambda self: self._m)
+    v = property(lambda self: self._v)
+    m_scales = property(lambda self: self._m_scales)
+    v_scales = property(lambda self: self._v_scales)
+    sizes = property(lambda self: self._sizes)
+    offsets = property(lambda self: self._offsets)
+    n_state = property(lambda self: self._n_state)
 
     def __init__(self, params, copies=None, state: str = "e4m3", G: int = 128, m=None, v=None,
                  m_scales=None, v_scales=None):
-        self.params = _list(params, "params")
-        if not self.params:
+        params = _list(params, "params")
+        if not params:
             raise ValueError("params: empty list")
         if state not in _STATES:
             raise ValueError(f"state {state!r} is not one of {', '.join(map(repr, _STATES))}")
         _check_n_G(0, G)
-        for i, p in enumerate(self.params):
+        for i, p in enumerate(params):
             _need(p, f"params[{i}]", _F32, 0)
-        self.copies = None if copies is None else _list(copies, "copies")
-        if self.copies is not None:
-            if len(self.copies) != len(self.params):
-                raise ValueError(f"copies: {len(self.copies)} tensors for {len(self.params)} parameters")
-            kinds = _COPIES if not self.copies else (self.copies[0].dtype,)
-            for i, (c, p) in enumerate(zip(self.copies, self.params)):
+        if copies is not None:
+            copies = _list(copies, "copies")
+            if len(copies) != len(params):
+                raise ValueError(f"copies: {len(copies)} tensors for {len(params)} parameters")
+            for i, (c, p) in enumerate(zip(copies, params)):
                 _need(c, f"copies[{i}]", _COPIES, p.numel())
-                _need(c, f"copies[{i}]", kinds, p.numel())
-        self.state, self.G = state, G
-        self.sizes = [p.numel() for p in self.params]
-        self.offsets, at = [], 0
-        for n in self.sizes:
-            self.offsets.append(at)
+                _need(c, f"copies[{i}]", (copies[0].dtype,), p.numel())
+        sizes, offsets, at = [p.numel() for p in params], [], 0
+        for n in sizes:
+            offsets.append(at)
             at += n_blocks(n, G) * G
-        self.n_state = at
         eight = state == "e4m3"
         kind, ns = (_U8 if eight else _F32), (at // G if eight else 0)
         for t, what, dt, n in ((m, "m", kind, at), (v, "v", kind, at),
                                (m_scales, "m_scales", _F32, ns), (v_scales, "v_scales", _F32, ns)):
             if t is not None:
                 _need(t, what, dt, n)
-        self.device = _dev(*self.params, *(self.copies or ()), m, v, m_scales, v_scales)
+        device = _dev(*params, *(copies or ()), m, v, m_scales, v_scales)
 
         def own(t, n, dt):
-            return torch.zeros(n, dtype=dt[0], device=self.device) if t is None else t
-        self.m, self.v = own(m, at, kind), own(v, at, kind)
-        self.m_scales = own(m_scales, ns, _F32) if eight else None
-        self.v_scales = own(v_scales, ns, _F32) if eight else None
+            return torch.zeros(n, dtype=dt[0], device=device) if t is None else t
+        self._state, self._G, self._n_state = state, G, at
+        self._params, self._copies = tuple(params), None if copies is None else tuple(copies)
+        self._sizes, self._offsets = tuple(sizes), tuple(offsets)
+        self._m, self._v = own(m, at, kind), own(v, at, kind)
+        self._m_scales = own(m_scales, ns, _F32) if eight else None
+        self._v_scales = own(v_scales, ns, _F32) if eight else None
 
-        n = len(self.params)
-        self._at = self._pointers()
-        self._params = (ctypes.c_void_p * n)(*self._at)
-        self._copies = None if self.copies is None else (ctypes.c_void_p * n)(*(c.data_ptr() for c in self.copies))
-        self._copy_type = DTYPES[self.copies[0].dtype] if self.copies else 0
-        self._sizes = (ctypes.c_int64 * n)(*self.sizes)
-        self._offsets = (ctypes.c_int64 * n)(*self.offsets)
+        # what every step passes on, made once: the tensors above stay alive with it
+        n = len(params)
+        self._index, self._at = device.index, [p.data_ptr() for p in params]
+        self._written = params + (copies or [])
         self._table = ctypes.c_void_p * n
-        self._written = self.params + (self.copies or [])
+        self._arrays = (self._table(*self._at), None if copies is None else self._table(*(c.data_ptr() for c in copies)),
+                        (ctypes.c_int64 * n)(*sizes), (ctypes.c_int64 * n)(*offsets))
+        self._copy_type = DTYPES[copies[0].dtype] if copies else 0
+        self._moments = (self._m.data_ptr(), self._m_scales.data_ptr() if eight else None,
+                         self._v.data_ptr(), self._v_scales.data_ptr() if eight else None)
 
-    def _pointers(self):
-        return [p.data_ptr() for p in self.params]
+
+_numel, _data_ptr, _get_device = torch.Tensor.numel, torch.Tensor.data_ptr, torch.Tensor.get_device
+_is_contiguous = torch.Tensor.is_contiguous
 
 
 def adamw_step(optimizer: AdamW, grads, step: int, lr: float, beta1: float = 0.9,
@@ -110,31 +122,32 @@ def adamw_step(optimizer: AdamW, grads, step: int, lr: float, beta1: float = 0.9
                  and inputs give the same bytes
     """
     o = optimizer
-    grads = _list(grads, "grads")
-    if len(grads) != len(o.sizes):
-        raise ValueError(f"grads: {len(grads)} tensors for {len(o.sizes)} parameters")
-    dev, kind = o.device, getattr(grads[0], "dtype", None)
-    if kind not in DTYPES:
-        _need(grads[0], "grads[0]", _ELEMS, 0)
-    index = dev.index
-    at = []
-    for i, (g, n) in enumerate(zip(grads, o.sizes)):
-        if (type(g) is not torch.Tensor or g.dtype is not kind or g.numel() != n
-                or not g.is_contiguous() or g.get_device() != index):
-            _need(g, f"grads[{i}]", (kind,), n)
+    if type(grads) is not list:
+        grads = _list(grads, "grads")
+    if len(grads) != len(o._sizes):
+        raise ValueError(f"grads: {len(grads)} tensors for {len(o._sizes)} parameters")
+    index, kind = o._index, getattr(grads[0], "dtype", None)
+    # four questions that all valid gradients answer with yes; the loop names the fault
+    try:
+        good = (kind in DTYPES and tuple(map(_numel, grads)) == o._sizes and all(map(_is_contiguous, grads))
+                and {g.dtype for g in grads} == {kind} and set(map(_get_device, grads)) == {index})
+    except (AttributeError, TypeError):
+        good = False
+    if not good:
+        for i, (g, n) in enumerate(zip(grads, o._sizes)):
+            _need(g, f"grads[{i}]", (kind,) if kind in DTYPES else _ELEMS, n)
             if g.numel() != n:
                 raise ValueError(f"grads[{i}]: holds {g.numel()} elements, the parameter {n}")
-            _dev(o.m, g)
-        at.append(g.data_ptr())
+            _dev(o._m, g)
     if grad_scale is not None:
         _need(grad_scale, "grad_scale", _F32, 1)
-        _dev(o.m, grad_scale)
-    if o._pointers() != o._at:
+        _dev(o._m, grad_scale)
+    if list(map(_data_ptr, o._params)) != o._at:
         raise ValueError("params: a parameter was given another storage since the AdamW was made")
-    with torch.cuda.device(dev):
-        _check("adamw_step", library().adamw_step(
-            o._params, o._table(*at), o._copies, o._sizes, o._offsets, len(at), DTYPES[kind],
-            o._copy_type, _STATES[o.state], _ptr(o.m), _ptr(o.m_scales), _ptr(o.v),
-            _ptr(o.v_scales), o.n_state, o.G, step, lr, beta1, beta2, eps, weight_decay,
-            _ptr(grad_scale), seed & 0xFFFFFFFFFFFFFFFF, _stream(dev)))
+    params, copies, sizes, offsets = o._arrays
+    m, ms, v, vs = o._moments
+    _enqueue("adamw_step", index, params, o._table(*map(_data_ptr, grads)), copies, sizes, offsets, len(grads),
+             DTYPES[kind], o._copy_type, _STATES[o._state], m, ms, v, vs, o._n_state, o._G, step, lr, beta1,
+             beta2, eps, weight_decay, None if grad_scale is None else grad_scale.data_ptr(),
+             seed & 0xFFFFFFFFFFFFFFFF)
     torch.autograd.graph.increment_version(o._written)
