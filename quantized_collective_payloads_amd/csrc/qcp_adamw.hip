@@ -28,6 +28,10 @@
 // a work-group belongs to is found in one step: lane i compares the work-group
 // number with tensor i's first, and the ballot's population count is the answer.
 // The table of tensors is a kernel argument: nothing is allocated or copied.
+//
+// Everything is read and written once, so loads and stores are non-temporal: 27.3M
+// elements with fp32 moments 154 -> 137 us (5.97 TB/s), 369M with 8-bit moments
+// 1112 -> 1060 us (5.61 TB/s); either hint alone gains 1 to 3%.
 #include "qcp_device.h"
 #include "qcp_launch.h"
 
@@ -39,14 +43,15 @@ namespace {
 // views of larger buffers at any offset
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 typedef unsigned int u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 template <int GT>
 __device__ __forceinline__ void load4(const void *p, int64_t i, float (&x)[4]) {
     if constexpr (GT == F32) {
-        const f32x4_any v = *(const f32x4_any *)((const float *)p + i);
+        const f32x4_any v = __builtin_nontemporal_load((const f32x4_any *)((const float *)p + i));
         x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
     } else {
-        const u32x2_any v = *(const u32x2_any *)((const uint16_t *)p + i);
+        const u32x2_any v = __builtin_nontemporal_load((const u32x2_any *)((const uint16_t *)p + i));
         x[0] = widen_lo<GT>(v.x); x[1] = widen_hi<GT>(v.x);
         x[2] = widen_lo<GT>(v.y); x[3] = widen_hi<GT>(v.y);
     }
@@ -59,12 +64,12 @@ __device__ __forceinline__ float load1(const void *p, int64_t i) {
 }
 
 __device__ __forceinline__ void store4(float *p, int64_t i, const float (&x)[4]) {
-    *(f32x4_any *)(p + i) = f32x4_any{x[0], x[1], x[2], x[3]};
+    __builtin_nontemporal_store(f32x4_any{x[0], x[1], x[2], x[3]}, (f32x4_any *)(p + i));
 }
 
 template <int YT>
 __device__ __forceinline__ void copy4(void *p, int64_t i, const float (&x)[4]) {
-    *(u32x2_any *)((uint16_t *)p + i) = u32x2_any{narrow2<YT>(x[0], x[1]), narrow2<YT>(x[2], x[3])};
+    __builtin_nontemporal_store(u32x2_any{narrow2<YT>(x[0], x[1]), narrow2<YT>(x[2], x[3])}, (u32x2_any *)((uint16_t *)p + i));
 }
 
 template <int YT>
@@ -142,8 +147,8 @@ __device__ __forceinline__ void adamw_wave(const AdamwTensor &t, const AdamwCons
             }
         } else {
             if (FULL || left[u] > 0) {
-                const float4 a = *(const float4 *)((const float *)c.m + i);
-                const float4 b = *(const float4 *)((const float *)c.v + i);
+                const f32x4_t a = __builtin_nontemporal_load((const f32x4_t *)((const float *)c.m + i));
+                const f32x4_t b = __builtin_nontemporal_load((const f32x4_t *)((const float *)c.v + i));
                 m[u][0] = a.x; m[u][1] = a.y; m[u][2] = a.z; m[u][3] = a.w;
                 v[u][0] = b.x; v[u][1] = b.y; v[u][2] = b.z; v[u][3] = b.w;
             } else {
@@ -193,8 +198,8 @@ __device__ __forceinline__ void adamw_wave(const AdamwTensor &t, const AdamwCons
         if constexpr (!EIGHT) {
             if (FULL || left[u] > 0) {
                 const int64_t i = t.offset + at[u];
-                *(float4 *)((float *)c.m + i) = make_float4(m[u][0], m[u][1], m[u][2], m[u][3]);
-                *(float4 *)((float *)c.v + i) = make_float4(v[u][0], v[u][1], v[u][2], v[u][3]);
+                __builtin_nontemporal_store(f32x4_t{m[u][0], m[u][1], m[u][2], m[u][3]}, (f32x4_t *)((float *)c.m + i));
+                __builtin_nontemporal_store(f32x4_t{v[u][0], v[u][1], v[u][2], v[u][3]}, (f32x4_t *)((float *)c.v + i));
             }
         }
     }
@@ -227,8 +232,8 @@ __device__ __forceinline__ void adamw_wave(const AdamwTensor &t, const AdamwCons
                     vq[j] = v[u][j] > 0.0f ? __builtin_fmaxf(b, 0x1p-9f) : 0.0f;
                 }
                 if (FULL || left[u] > 0) {
-                    *(uint32_t *)((uint8_t *)c.m + i) = e4m3_pack4(mq[0], mq[1], mq[2], mq[3]);
-                    *(uint32_t *)((uint8_t *)c.v + i) = e4m3_pack4(vq[0], vq[1], vq[2], vq[3]);
+                    __builtin_nontemporal_store(e4m3_pack4(mq[0], mq[1], mq[2], mq[3]), (uint32_t *)((uint8_t *)c.m + i));
+                    __builtin_nontemporal_store(e4m3_pack4(vq[0], vq[1], vq[2], vq[3]), (uint32_t *)((uint8_t *)c.v + i));
                 }
             }
             const int64_t i = t.offset + at[u0];

@@ -20,6 +20,9 @@
 // on the 16-bit patterns where the input has them.  Output positions are the same
 // whether rows are padded or not: vector i of the padded matrix has its codes at
 // byte 4i.  A matrix that is one run of whole 128s needs no row arithmetic (FLAT).
+// fp32 moves 4 values a lane (a block is 8 lanes), so that every access of a wave is
+// one contiguous run: 32-byte pieces a lane cost the dequantize to fp32 a third of
+// its rate (28672 x 8192: 317 us).
 //
 // Along the columns: a work-group takes 256 rows x 64 columns.  A lane owns two
 // neighbouring columns of 32 rows, so its two blocks need no other lane: absmax,
@@ -51,7 +54,7 @@ __device__ __forceinline__ void load8(const void *x, int64_t i, int count, uint3
     if (count >= 8) {
 #pragma unroll
         for (int k = 0; k < words8<XT>() / 4; k++) {
-            const u32x4_any v = *((const u32x4_any *)p + k);
+            const u32x4_any v = __builtin_nontemporal_load((const u32x4_any *)p + k);
             w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
         }
     } else {
@@ -65,6 +68,17 @@ __device__ __forceinline__ void load8(const void *x, int64_t i, int count, uint3
                 w[k] = lo | (hi << 16);
             }
         }
+    }
+}
+
+// 4 fp32 values from p, of which `count` exist
+__device__ __forceinline__ void load4(const float *x, int64_t i, int count, uint32_t *w) {
+    if (count >= 4) {
+        const u32x4_any v = __builtin_nontemporal_load((const u32x4_any *)(x + i));
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; k++) w[k] = k < count ? __float_as_uint(x[i + k]) : 0;
     }
 }
 
@@ -137,68 +151,114 @@ __device__ __forceinline__ RowPlace place(int64_t row0, uint32_t col0, uint32_t 
     return RowPlace{row0 + q, c - q * width};
 }
 
+// how many of the `unit` values at place p of a row exist
+__device__ __forceinline__ int values_left(bool inside, int64_t cols, uint32_t col, int unit) {
+    const int64_t left = inside ? cols - (int64_t)col * unit : 0;
+    return left > unit ? unit : left < 0 ? 0 : (int)left;
+}
+
+// fp32 moves as 4 values a lane, 16 bytes, in two runs of 256 values a wave; a lane
+// then has 16 bits of codes of each run (low: the first).  Lanes 2i and 2i+1 trade
+// halves, and hold 8 codes of the first and of the second run, whole dwords.  The
+// trade is its own inverse.
+__device__ __forceinline__ uint32_t trade(uint32_t w, int lane) {
+    const uint32_t other = dpp_u32<0xB1>(w);
+    return lane & 1 ? (other >> 16) | (w & 0xffff0000u) : (w & 0xffffu) | (other << 16);
+}
+
 template <int XT, bool FLAT>
 __global__ __launch_bounds__(kThreads) void k_mx_quantize(const void *__restrict__ x, int64_t vecs,
                                                           uint32_t width, int64_t cols, int64_t ld,
                                                           uint32_t *__restrict__ codes,
-                                                          uint32_t *__restrict__ scales) {
+                                                          uint8_t *__restrict__ scales) {
+    constexpr int UNIT = XT == F32 ? 4 : 8;                  // values of a lane's run
     const int lane = lane_id();
     const int64_t v0 = wave_id() * (64 * kMxVecs);
     if (v0 >= vecs) return;
     const int64_t row0 = FLAT ? 0 : v0 / width;
     const uint32_t col0 = FLAT ? 0 : (uint32_t)(v0 - row0 * width);
     uint32_t w[kMxVecs][words8<XT>()];
+    // where run h of vector group u begins for this lane, in units, and whether inside
+    auto load = [&](int u, int h, uint32_t *to) __attribute__((always_inline)) {
+        constexpr int per = 8 / UNIT;
+        const uint32_t step = (uint32_t)(u * 64 * per + h * 64 + lane);
+        const bool inside = v0 * per + step < vecs * per;
+        int64_t at = (v0 * per + step) * UNIT;
+        int count = inside ? UNIT : 0;
+        if constexpr (!FLAT) {
+            const RowPlace p = place(row0, col0 * per, step, width * per);
+            at = p.row * ld + (int64_t)p.col * UNIT;
+            count = values_left(inside, cols, p.col, UNIT);
+        }
+        if constexpr (XT == F32) load4((const float *)x, at, count, to);
+        else load8<XT>(x, at, count, *(uint32_t(*)[words8<XT>()])to);
+    };
 #pragma unroll
     for (int u = 0; u < kMxVecs; u++) {
-        const int64_t v = v0 + u * 64 + lane;
-        if constexpr (FLAT) {
-            load8<XT>(x, v * 8, v < vecs ? 8 : 0, w[u]);
-        } else {
-            const RowPlace p = place(row0, col0, u * 64 + lane, width);
-            const int64_t left = v < vecs ? cols - (int64_t)p.col * 8 : 0;
-            load8<XT>(x, p.row * ld + (int64_t)p.col * 8, left > 8 ? 8 : left < 0 ? 0 : (int)left, w[u]);
-        }
+        load(u, 0, w[u]);
+        if constexpr (XT == F32) load(u, 1, w[u] + 4);
     }
 #pragma unroll
     for (int u = 0; u < kMxVecs; u++) {
         const int64_t v = v0 + u * 64 + lane;
-        uint32_t m = 0;
+        if constexpr (XT == F32) {
+            // a block is 8 lanes of either run
+            uint32_t e[2], c = 0;
 #pragma unroll
-        for (int k = 0; k < words8<XT>(); k++) m = absmax_of<XT>(m, w[u][k]);
-        m = absmax_of<XT>(m, dpp_u32<0xB1>(m));
-        m = absmax_of<XT>(m, dpp_u32<0x4E>(m));
-        const uint32_t e = scale_byte<XT>(m);
-        const uint32_t c = encode8<XT>(w[u], scale_of(e));
-        // the scale bytes of 4 blocks (16 lanes) in one dword
-        uint32_t d = e << (8 * ((lane >> 2) & 3));
-        d |= dpp_u32<0x141>(d);
-        d |= dpp_u32<0x140>(d);
-        if (v < vecs) {
-            codes[v] = c;
-            if ((lane & 15) == 0) scales[v >> 4] = d;
+            for (int h = 0; h < 2; h++) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int k = 0; k < 4; k++) m = absmax_of<XT>(m, w[u][4 * h + k]);
+                e[h] = scale_byte<XT>(group_max_u32<8>(m));
+            }
+            c = encode2<XT, 0>(c, w[u][0], w[u][1], scale_of(e[0]));
+            c = encode2<XT, 1>(c, w[u][2], w[u][3], scale_of(e[0]));
+            c = encode2<XT, 2>(c, w[u][4], w[u][5], scale_of(e[1]));
+            c = encode2<XT, 3>(c, w[u][6], w[u][7], scale_of(e[1]));
+            c = trade(c, lane);
+            // vectors of 8: the first run's are v0 + 64u + 0..31, the second's 32..63
+            const int64_t at = v0 + u * 64 + (lane & 1) * 32 + (lane >> 1);
+            if (at < vecs) codes[at] = c;
+            const int64_t block = (v0 + u * 64) / 4 + (lane >> 3);
+            if ((lane & 7) == 0) {
+                if (block * 4 < vecs) scales[block] = (uint8_t)e[0];
+                if (block * 4 + 32 < vecs) scales[block + 8] = (uint8_t)e[1];
+            }
+        } else {
+            uint32_t m = 0;
+#pragma unroll
+            for (int k = 0; k < words8<XT>(); k++) m = absmax_of<XT>(m, w[u][k]);
+            m = absmax_of<XT>(m, dpp_u32<0xB1>(m));
+            m = absmax_of<XT>(m, dpp_u32<0x4E>(m));
+            const uint32_t e = scale_byte<XT>(m);
+            const uint32_t c = encode8<XT>(w[u], scale_of(e));
+            // the scale bytes of 4 blocks (16 lanes) in one dword
+            uint32_t d = e << (8 * ((lane >> 2) & 3));
+            d |= dpp_u32<0x141>(d);
+            d |= dpp_u32<0x140>(d);
+            if (v < vecs) {
+                codes[v] = c;
+                if ((lane & 15) == 0) ((uint32_t *)scales)[v >> 4] = d;
+            }
         }
     }
 }
 
-// 8 codes and their scale byte -> 8 values
-template <int YT>
-__device__ __forceinline__ void decode8(uint32_t c, uint32_t e, uint32_t (&w)[words8<YT>()]) {
-    const float s = scale_of(e);
-    static_for<4>([&](auto K) {
-        constexpr int k = K;
-        if constexpr (YT == F32) {
-            const f32x2_t v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, k);
-            w[2 * k] = __float_as_uint(v.x);
-            w[2 * k + 1] = __float_as_uint(v.y);
-        } else if constexpr (YT == BF16) {
-            w[k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, k));
-        } else {
-            w[k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, k));
-        }
-    });
-    constexpr uint32_t nan = YT == F32 ? 0x7fc00000u : YT == BF16 ? 0x7fc07fc0u : 0x7e007e00u;
-#pragma unroll
-    for (int k = 0; k < words8<YT>(); k++) w[k] = e == 255u ? nan : w[k];
+// codes 2k, 2k+1 and their scale -> two values of 16 bits, or one of 32 each
+template <int YT, int K>
+__device__ __forceinline__ void decode2(uint32_t c, float s, uint32_t *w) {
+    if constexpr (YT == F32) {
+        const f32x2_t v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, K);
+        w[0] = __float_as_uint(v.x);
+        w[1] = __float_as_uint(v.y);
+    } else if constexpr (YT == BF16) {
+        w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, K));
+    } else {
+        w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, K));
+    }
+}
+template <int YT> constexpr uint32_t nan_word() {
+    return YT == F32 ? 0x7fc00000u : YT == BF16 ? 0x7fc07fc0u : 0x7e007e00u;
 }
 
 template <int YT>
@@ -220,35 +280,64 @@ __device__ __forceinline__ void store8(void *y, int64_t i, int count, const uint
     }
 }
 
+__device__ __forceinline__ void store4(float *y, int64_t i, int count, const uint32_t *w) {
+    if (count >= 4) {
+        __builtin_nontemporal_store(u32x4_any{w[0], w[1], w[2], w[3]}, (u32x4_any *)(y + i));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (j < count) y[i + j] = __uint_as_float(w[j]);
+    }
+}
+
 template <int YT, bool FLAT>
 __global__ __launch_bounds__(kThreads) void k_mx_dequantize(const uint32_t *__restrict__ codes,
                                                             const uint8_t *__restrict__ scales,
                                                             int64_t vecs, uint32_t width, int64_t cols,
                                                             int64_t ld, void *__restrict__ y) {
+    constexpr int UNIT = YT == F32 ? 4 : 8, per = 8 / UNIT;
     const int lane = lane_id();
     const int64_t v0 = wave_id() * (64 * kMxVecs);
     if (v0 >= vecs) return;
     const int64_t row0 = FLAT ? 0 : v0 / width;
     const uint32_t col0 = FLAT ? 0 : (uint32_t)(v0 - row0 * width);
-    uint32_t c[kMxVecs], e[kMxVecs];
+    uint32_t c[kMxVecs], e[kMxVecs][per];
 #pragma unroll
     for (int u = 0; u < kMxVecs; u++) {
-        const int64_t v = v0 + u * 64 + lane;
+        // fp32: as in the quantize, two runs of 256 values and a trade between lanes
+        const int64_t v = v0 + u * 64 + (YT == F32 ? (lane & 1) * 32 + (lane >> 1) : lane);
         c[u] = v < vecs ? codes[v] : 0;
-        e[u] = v < vecs ? scales[v >> 2] : 0;
+#pragma unroll
+        for (int h = 0; h < per; h++) {
+            const int64_t block = YT == F32 ? (v0 + u * 64) / 4 + h * 8 + (lane >> 3) : (v0 + u * 64 + lane) >> 2;
+            e[u][h] = block * 4 < vecs ? scales[block] : 0;
+        }
     }
 #pragma unroll
     for (int u = 0; u < kMxVecs; u++) {
-        const int64_t v = v0 + u * 64 + lane;
         uint32_t w[words8<YT>()];
-        decode8<YT>(c[u], e[u], w);
-        if constexpr (FLAT) {
-            store8<YT>(y, v * 8, v < vecs ? 8 : 0, w);
-        } else {
-            const RowPlace p = place(row0, col0, u * 64 + lane, width);
-            const int64_t left = v < vecs ? cols - (int64_t)p.col * 8 : 0;
-            store8<YT>(y, p.row * ld + (int64_t)p.col * 8, left > 8 ? 8 : left < 0 ? 0 : (int)left, w);
-        }
+        if constexpr (YT == F32) c[u] = trade(c[u], lane);
+        static_for<4>([&](auto K) __attribute__((always_inline)) {
+            constexpr int k = K, step = YT == F32 ? 2 : 1;
+            decode2<YT, k>(c[u], scale_of(e[u][k * per / 4]), w + k * step);
+#pragma unroll
+            for (int j = k * step; j < (k + 1) * step; j++)
+                if (e[u][k * per / 4] == 255u) w[j] = nan_word<YT>();
+        });
+        static_for<per>([&](auto H) __attribute__((always_inline)) {
+            constexpr int h = H;
+            const uint32_t step = (uint32_t)(u * 64 * per + h * 64 + lane);
+            const bool inside = v0 * per + step < vecs * per;
+            int64_t at = (v0 * per + step) * UNIT;
+            int count = inside ? UNIT : 0;
+            if constexpr (!FLAT) {
+                const RowPlace p = place(row0, col0 * per, step, width * per);
+                at = p.row * ld + (int64_t)p.col * UNIT;
+                count = values_left(inside, cols, p.col, UNIT);
+            }
+            if constexpr (YT == F32) store4((float *)y, at, count, w + 4 * h);
+            else store8<YT>(y, at, count, w);
+        });
     }
 }
 
@@ -256,14 +345,18 @@ constexpr int kTRows = 256, kTCols = 64;       // tile of the column-wise quanti
 
 template <int XT>
 __global__ __launch_bounds__(kThreads) void k_mx_quantize_t(const void *__restrict__ x, int64_t rows,
-                                                            int64_t cols, int64_t ld, uint32_t col_tiles,
+                                                            int64_t cols, int64_t ld, uint32_t col_tiles, uint32_t groups,
                                                             int64_t pad_rows, uint8_t *__restrict__ codes,
                                                             uint8_t *__restrict__ scales) {
     constexpr int B = dtype_traits<XT>::bytes;
     constexpr int kLine = 128 + 16;            // bytes per column in LDS: a shift of 4 banks
     __shared__ __attribute__((aligned(16))) uint8_t lines[kTCols * kLine];
     __shared__ __attribute__((aligned(8))) uint8_t marks[kTCols * 8];
-    const uint32_t wg = __builtin_amdgcn_workgroup_id_x();
+    // Work-groups are dealt round-robin to the 8 XCDs.  16 neighbouring tiles, 2 KB of
+    // a 16-bit row, go to one XCD, so that its reads spread over all its L2 channels;
+    // in launch order they would lie 1 KB apart, a quarter of the channels.
+    uint32_t wg = __builtin_amdgcn_workgroup_id_x();
+    if (wg < (groups & ~127u)) wg = (wg & ~127u) + (wg & 7) * 16 + ((wg >> 3) & 15);
     const int64_t tr = (int64_t)(wg / col_tiles) * kTRows, tc = (int64_t)(wg % col_tiles) * kTCols;
     const int tid = (int)__builtin_amdgcn_workitem_id_x();
     const int block = tid >> 5;                // which 32 rows of the tile
@@ -351,7 +444,7 @@ hipError_t run_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, i
         const int64_t pad = (rows + kMxPad - 1) / kMxPad * kMxPad;
         const int64_t ct = (cols + kTCols - 1) / kTCols, rt = (rows + kTRows - 1) / kTRows;
         hipLaunchKernelGGL((k_mx_quantize_t<XT>), dim3((unsigned)(ct * rt)), dim3(kThreads), 0, st, x, rows,
-                           cols, ld, (uint32_t)ct, pad, codes, scales);
+                           cols, ld, (uint32_t)ct, (uint32_t)(ct * rt), pad, codes, scales);
         return hipGetLastError();
     }
     const int64_t pad = (cols + kMxPad - 1) / kMxPad * kMxPad;
@@ -360,10 +453,10 @@ hipError_t run_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, i
     const unsigned grid = grid_for_waves((vecs + 64 * kMxVecs - 1) / (64 * kMxVecs));
     if (flat)
         hipLaunchKernelGGL((k_mx_quantize<XT, true>), dim3(grid), dim3(kThreads), 0, st, x, vecs, 1u, cols,
-                           ld, (uint32_t *)codes, (uint32_t *)scales);
+                           ld, (uint32_t *)codes, scales);
     else
         hipLaunchKernelGGL((k_mx_quantize<XT, false>), dim3(grid), dim3(kThreads), 0, st, x, vecs,
-                           (uint32_t)(pad / 8), cols, ld, (uint32_t *)codes, (uint32_t *)scales);
+                           (uint32_t)(pad / 8), cols, ld, (uint32_t *)codes, scales);
     return hipGetLastError();
 }
 
