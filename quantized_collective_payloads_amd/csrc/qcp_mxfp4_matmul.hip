@@ -9,6 +9,8 @@
 // first 32 bytes and the upper one the last, and two instructions use them up.
 // The row's 4 scale bytes are one dword; its half is shifted down once per
 // granule, and the instruction picks the byte.
+#include <algorithm>
+
 #include "qcp_device.h"
 #include "qcp_launch.h"
 
@@ -142,10 +144,16 @@ __global__ __launch_bounds__(kThreads) void k_mx_matmul(const uint8_t *__restric
 // at the same piece a cycle, touches each of the 64 banks once.  Scales are copied
 // for 4 granules at a time, 16 bytes a row, into slots of their own.
 //
+// A work-group walks several tiles: the copies of the next one's first stages go out
+// before the results of this one, whose stores then cover their latency (14336 x 4096,
+// K = 2048: 119 us for a work-group per tile with 8-byte stores, 109 so).
+//
 // Rows past the end repeat the last row.  Windows in K are pulled back to end
 // with the row: a last odd granule comes as the second one of its window, and is
 // multiplied by itself as in the kernel above.
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kCUs = 256;
 
 // 64 lanes x 16 bytes from rsrc[voff + soff] to LDS at `lds` + 16 * lane.  The
 // caller waits for it with wait_and_meet; no vector register is written, and nothing
@@ -162,6 +170,50 @@ __device__ __forceinline__ void copy_to_lds(uint32_t lds, uint32_t voff, i32x4_t
 template <int N>
 __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void wait_lds_and_meet() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// A fragment of C: lane r of a half-wave has row m, and of columns n + 8q + 4 * half + 0..3
+// register group q.  16-bit results go out 16 bytes a lane: the half-waves swap groups, so
+// that the lower one has columns n + 16k + 0..7 and the upper one 8..15.
+template <int CT>
+__device__ __forceinline__ void store_fragment(const f32x16_t &v, void *c, int64_t ldc, int64_t m, int64_t n,
+                                               int half, int64_t M, int64_t N, bool whole) {
+    if constexpr (CT == F32) {
+        if (!whole && m >= M) return;
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const int64_t at = n + 8 * q + 4 * half;
+            const float r[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+            store4<CT>(c, m * ldc + at, whole || N - at >= 4 ? 4 : (int)(N - at), r);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            uint32_t w[4];
+#pragma unroll
+            for (int d = 0; d < 2; d++) {
+                const uint32_t lo = narrow2<CT>(v[8 * k + 2 * d], v[8 * k + 2 * d + 1]);
+                const uint32_t hi = narrow2<CT>(v[8 * k + 4 + 2 * d], v[8 * k + 5 + 2 * d]);
+                const auto swapped = __builtin_amdgcn_permlane32_swap(lo, hi, false, false);
+                w[d] = swapped[0];
+                w[2 + d] = swapped[1];
+            }
+            const int64_t at = n + 16 * k + 8 * half;
+            uint16_t *p = (uint16_t *)c + m * ldc + at;
+            typedef u32x4_t u32x4_any __attribute__((aligned(2)));
+            if (whole || (m < M && N - at >= 8)) {
+                *(u32x4_any *)p = u32x4_t{w[0], w[1], w[2], w[3]};
+            } else if (m < M) {
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    if (at + e < N) p[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ i32x4_t buffer_of(const void *p, uint64_t bytes) {
@@ -191,6 +243,8 @@ template <int FM, int FN> struct tgeom {
     static constexpr int reads = 2 * (FM + FN);            // fragment pieces per phase
     static constexpr int copies = rows / 32;               // per stage and wave, 8 rows each
     static constexpr int waves_per_simd = FM * FN <= 4 ? 2 : 1;
+    // 16-byte stores of a wave's whole results
+    template <int CT> static constexpr int stores() { return FM * FN * 16 * dtype_traits<CT>::bytes / 16; }
     static constexpr int ahead = (slots - 2) * copies;     // copies of stages beyond the next
 };
 
@@ -205,64 +259,63 @@ template <int FM, int FN, int CT>
 __global__ __launch_bounds__(kThreads, (tgeom<FM, FN>::waves_per_simd)) void k_mx_matmul_tiled(
     const uint8_t *__restrict__ a, const uint8_t *__restrict__ as, const uint8_t *__restrict__ b,
     const uint8_t *__restrict__ bs, int64_t M, int64_t N, uint32_t granules, uint32_t m_tiles,
-    uint32_t n_tiles, void *__restrict__ c, int64_t ldc) {
+    uint32_t n_tiles, uint32_t groups, void *__restrict__ c, int64_t ldc) {
     using Gm = tgeom<FM, FN>;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[Gm::lds];
     const int tid = (int)__builtin_amdgcn_workitem_id_x();
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = lane_id();
 
-    // work-groups are dealt round-robin to the 8 XCDs: give each XCD a contiguous
-    // run of tiles, and walk it 4 tiles of M by N, so that the tiles an XCD works on
-    // at a time share few operand panels in its L2
-    const uint32_t tiles = m_tiles * n_tiles;
-    uint32_t t = __builtin_amdgcn_workgroup_id_x();
-    const uint32_t per = tiles / 8, extra = tiles % 8, xcd = t % 8, slot8 = t / 8;
-    t = xcd * per + min(xcd, extra) + slot8;
-    const uint32_t band = 4 * n_tiles, first = t / band * 4, height = min(4u, m_tiles - first);
-    const uint32_t in = t - t / band * band;
-    const int64_t m0 = (int64_t)(first + in % height) * Gm::TM, n0 = (int64_t)(in / height) * Gm::TN;
-
-    const uint32_t row_bytes = granules * 64, mark_bytes = granules * 4;
-    const uint32_t m_rows = (uint32_t)min(M - m0, (int64_t)Gm::TM), n_rows = (uint32_t)min(N - n0, (int64_t)Gm::TN);
-    const i32x4_t ra = buffer_of(a + m0 * row_bytes, (uint64_t)m_rows * row_bytes);
-    const i32x4_t rb = buffer_of(b + n0 * row_bytes, (uint64_t)n_rows * row_bytes);
-    const i32x4_t rsa = buffer_of(as + m0 * mark_bytes, (uint64_t)m_rows * mark_bytes);
-    const i32x4_t rsb = buffer_of(bs + n0 * mark_bytes, (uint64_t)n_rows * mark_bytes);
-
-    // copies: a wave brings a quarter of each operand's rows, 8 rows at a time
-    uint32_t va[2 * FM], vb[2 * FN];
-#pragma unroll
-    for (int i = 0; i < 2 * FM; i++) {
-        const uint32_t row = wave * 16 * FM + i * 8 + (lane >> 3);
-        va[i] = min(row, m_rows - 1) * row_bytes + ((lane & 7) ^ ((row >> 1) & 7)) * 16;
-    }
-#pragma unroll
-    for (int i = 0; i < 2 * FN; i++) {
-        const uint32_t row = wave * 16 * FN + i * 8 + (lane >> 3);
-        vb[i] = min(row, n_rows - 1) * row_bytes + ((lane & 7) ^ ((row >> 1) & 7)) * 16;
-    }
-    // scales: 64 rows at a time, FM pieces of A, then FN of B, dealt to the waves (the
-    // last piece twice where they do not divide).  No branches: the loop below stays
-    // one basic block, in which the order written is kept
-    constexpr int mark_rounds = (FM + FN + 3) / 4;
-    uint32_t vs[mark_rounds], mark_at[mark_rounds];
-    i32x4_t rs[mark_rounds];
-#pragma unroll
-    for (int k = 0; k < mark_rounds; k++) {
-        const int q = min(wave + 4 * k, FM + FN - 1);
-        const bool of_a = FM >= 4 * k + 4 || (FM > 4 * k && q < FM);
-        mark_at[k] = q * 1024;
-        vs[k] = (of_a ? min((uint32_t)(64 * q + lane), m_rows - 1) : min((uint32_t)(64 * (q - FM) + lane), n_rows - 1)) * mark_bytes;
-        rs[k] = of_a ? rsa : rsb;
-    }
+    const uint32_t tiles = m_tiles * n_tiles, row_bytes = granules * 64, mark_bytes = granules * 4;
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
     const uint32_t stages = (granules + 1) / 2;
 
+    // the tile that is being copied.  Copies: a wave brings a quarter of each operand's
+    // rows, 8 rows at a time.  Scales: 64 rows at a time, FM pieces of A, then FN of B,
+    // dealt to the waves (the last piece twice where they do not divide).  No branches:
+    // the loop below stays one basic block, in which the order written is kept.
+    constexpr int mark_rounds = (FM + FN + 3) / 4;
+    int64_t m0, n0;
+    i32x4_t ra, rb, rs[mark_rounds];
+    uint32_t vs[mark_rounds], mark_at[mark_rounds], m_rows, n_rows;
+    auto set_tile = [&](uint32_t t) __attribute__((always_inline)) {
+        // work-groups are dealt round-robin to the 8 XCDs: give each XCD a contiguous
+        // run of tiles, and walk it 4 tiles of M by N, so that the tiles an XCD works on
+        // at a time share few operand panels in its L2
+        const uint32_t per = tiles / 8, extra = tiles % 8, xcd = t % 8;
+        t = xcd * per + min(xcd, extra) + t / 8;
+        const uint32_t band = 4 * n_tiles, first = t / band * 4, height = min(4u, m_tiles - first);
+        const uint32_t in = t - t / band * band;
+        m0 = (int64_t)(first + in % height) * Gm::TM;
+        n0 = (int64_t)(in / height) * Gm::TN;
+        m_rows = (uint32_t)min(M - m0, (int64_t)Gm::TM);
+        n_rows = (uint32_t)min(N - n0, (int64_t)Gm::TN);
+        ra = buffer_of(a + m0 * row_bytes, (uint64_t)m_rows * row_bytes);
+        rb = buffer_of(b + n0 * row_bytes, (uint64_t)n_rows * row_bytes);
+        const i32x4_t rsa = buffer_of(as + m0 * mark_bytes, (uint64_t)m_rows * mark_bytes);
+        const i32x4_t rsb = buffer_of(bs + n0 * mark_bytes, (uint64_t)n_rows * mark_bytes);
+        static_for<mark_rounds>([&](auto I) __attribute__((always_inline)) {
+            constexpr int k = I;
+            const int q = min(wave + 4 * k, FM + FN - 1);
+            const bool of_a = FM >= 4 * k + 4 || (FM > 4 * k && q < FM);
+            mark_at[k] = q * 1024;
+            vs[k] = (of_a ? min((uint32_t)(64 * q + lane), m_rows - 1) : min((uint32_t)(64 * (q - FM) + lane), n_rows - 1)) * mark_bytes;
+            rs[k] = of_a ? rsa : rsb;
+        });
+    };
+
     // the n-th copy of a stage into the slot at `to`, from byte k of the rows
+    const uint32_t copy_row = lane >> 3, copy_piece = ((lane & 7) ^ (lane >> 4)) * 16;
     auto copy = [&](auto I, uint32_t to, uint32_t k) __attribute__((always_inline)) {
         constexpr int n = I;
-        if constexpr (n < 2 * FM) copy_to_lds(to + wave * 16 * FM * 128 + n * 1024, va[n], ra, k);
-        else copy_to_lds(to + Gm::TM * 128 + wave * 16 * FN * 128 + (n - 2 * FM) * 1024, vb[n - 2 * FM], rb, k);
+        constexpr bool of_a = n < 2 * FM;
+        constexpr int i = of_a ? n : n - 2 * FM, rows = 16 * (of_a ? FM : FN);   // this wave's rows begin at wave * rows
+        // three operations a copy instead of a register each (the asm keeps them from
+        // being made once): row < 2^8, row_bytes < 2^24
+        uint32_t row = copy_row;
+        asm volatile("" : "+v"(row));
+        row = min(wave * rows + i * 8 + row, (of_a ? m_rows : n_rows) - 1);
+        const uint32_t at = (row & 0xffu) * (row_bytes & 0xffffffu) + (copy_piece ^ (i & 1 ? 64 : 0));
+        copy_to_lds(to + (of_a ? 0 : Gm::TM * 128) + wave * rows * 128 + i * 1024, at, of_a ? ra : rb, k);
     };
     auto copy_marks = [&](uint32_t to, uint32_t k) __attribute__((always_inline)) {
         static_for<mark_rounds>([&](auto I) __attribute__((always_inline)) {
@@ -314,7 +367,7 @@ __global__ __launch_bounds__(kThreads, (tgeom<FM, FN>::waves_per_simd)) void k_m
     auto pick = [&](uint32_t lo, uint32_t up) __attribute__((always_inline)) { return (lo & ~upper) | (up & upper); };
     auto window = [&](uint32_t s) __attribute__((always_inline)) { return min((2 * s) & ~3u, granules - 4); };   // first granule of s's scales
 
-    f32x16_t acc[FM][FN] = {};
+    f32x16_t acc[FM][FN];
     Frag f, h;
     Scale e;
     u32x4_t ga[FM], gb[FN];
@@ -364,75 +417,91 @@ __global__ __launch_bounds__(kThreads, (tgeom<FM, FN>::waves_per_simd)) void k_m
     using no = std::integral_constant<int, 0>;
     using yes = std::integral_constant<int, 1>;
 
-    static_for<Gm::slots>([&](auto Q) __attribute__((always_inline)) {
-        if ((uint32_t)Q < stages) copy_stage((uint32_t)Q);
-    });
+    auto copy_first = [&]() __attribute__((always_inline)) {
+        static_for<Gm::slots>([&](auto Q) __attribute__((always_inline)) {
+            if ((uint32_t)Q < stages) copy_stage((uint32_t)Q);
+        });
+    };
+    uint32_t tile = __builtin_amdgcn_workgroup_id_x();
+    set_tile(tile);
+    copy_first();
     wait_and_meet<0>();
-    read_all(0, 0, f);
-    read_scales(0, half, e);
+    for (;;) {
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+            for (int j = 0; j < FN; j++) acc[i][j] = f32x16_t{};
+        read_all(0, 0, f);
+        read_scales(0, half, e);
 
-    // two stages at a time while there are enough more to copy: every window then lies
-    // where the stage number says, and `ahead` copies follow those waited for
-    uint32_t s = 0;
-    const uint32_t full = granules / 2;
-    if (full >= 2 + Gm::slots) {
+        // two stages at a time while there are enough more to copy: every window then lies
+        // where the stage number says, and `ahead` copies follow those waited for
+        uint32_t s = 0;
+        const uint32_t full = granules / 2;
+        if (full >= 2 + Gm::slots) {
 #pragma unroll
-        for (int i = 0; i < FM; i++) ga[i] = lds16(a_marks + kMarks + i * 512);
+            for (int i = 0; i < FM; i++) ga[i] = lds16(a_marks + kMarks + i * 512);
 #pragma unroll
-        for (int i = 0; i < FN; i++) gb[i] = lds16(b_marks + kMarks + i * 512);
-        for (; s + 2 + Gm::slots <= full; s += 2) {
-            const uint32_t s0 = slot_of(s), s1 = slot_of(s + 1), s2 = slot_of(s + 2);
-            phase(no{}, f, h, s0, no{}, 0, no{}, 0, no{});
-            wait_and_meet<Gm::ahead>();
-            phase(yes{}, h, f, s1, yes{}, s + Gm::slots, no{}, 0, yes{});
+            for (int i = 0; i < FN; i++) gb[i] = lds16(b_marks + kMarks + i * 512);
+            for (; s + 2 + Gm::slots <= full; s += 2) {
+                const uint32_t s0 = slot_of(s), s1 = slot_of(s + 1), s2 = slot_of(s + 2);
+                phase(no{}, f, h, s0, no{}, 0, no{}, 0, no{});
+                wait_and_meet<Gm::ahead>();
+                phase(yes{}, h, f, s1, yes{}, s + Gm::slots, no{}, 0, yes{});
 #pragma unroll
-            for (int i = 0; i < FM; i++) e.a[i] = pick(ga[i].z, ga[i].w);
+                for (int i = 0; i < FM; i++) e.a[i] = pick(ga[i].z, ga[i].w);
 #pragma unroll
-            for (int i = 0; i < FN; i++) e.b[i] = pick(gb[i].z, gb[i].w);
-            phase(no{}, f, h, s1, no{}, 0, no{}, 0, no{});
-            wait_and_meet<Gm::ahead>();
-            phase(yes{}, h, f, s2, yes{}, s + 1 + Gm::slots, yes{}, mark_slot_of(s + 2), no{});
+                for (int i = 0; i < FN; i++) e.b[i] = pick(gb[i].z, gb[i].w);
+                phase(no{}, f, h, s1, no{}, 0, no{}, 0, no{});
+                wait_and_meet<Gm::ahead>();
+                phase(yes{}, h, f, s2, yes{}, s + 1 + Gm::slots, yes{}, mark_slot_of(s + 2), no{});
 #pragma unroll
-            for (int i = 0; i < FM; i++) e.a[i] = pick(ga[i].x, ga[i].y);
+                for (int i = 0; i < FM; i++) e.a[i] = pick(ga[i].x, ga[i].y);
 #pragma unroll
-            for (int i = 0; i < FN; i++) e.b[i] = pick(gb[i].x, gb[i].y);
-        }
-        // the group's scales may have come from a window that is pulled back
-        read_scales(s, 2 * s - window(s) + half, e);
-    }
-    for (; s < full; s++) {
-        read_all(s, 2, h);
-        products(no{}, f);
-        wait_and_meet<0>();
-        if (s + Gm::slots < stages) copy_stage(s + Gm::slots);
-        products(yes{}, h);
-        if (s + 1 < full) {
-            read_all(s + 1, 0, f);
-            read_scales(s + 1, 2 * s + 2 - window(s + 1) + half, e);
-        }
-    }
-    if (granules & 1) {                                  // the last granule, alone: pieces 4 + 2 * half
-        read_all(full, 4 ^ (6 * half), f);
-        read_scales(full, granules - 1 - window(full), e);
-#pragma unroll
-        for (int i = 0; i < FM; i++) e.a[i] >>= 16 * half;
-#pragma unroll
-        for (int i = 0; i < FN; i++) e.b[i] >>= 16 * half;
-        products(no{}, f);
-    }
-
-#pragma unroll
-    for (int i = 0; i < FM; i++) {
-        const int64_t m = m0 + (wave & 1) * 32 * FM + 32 * i + r;
-        if (m >= M) continue;
-#pragma unroll
-        for (int j = 0; j < FN; j++)
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const int64_t n = n0 + (wave >> 1) * 32 * FN + 32 * j + 8 * q + 4 * half;
-                const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-                store4<CT>(c, m * ldc + n, N - n < 4 ? (int)(N - n) : 4, v);
+                for (int i = 0; i < FN; i++) e.b[i] = pick(gb[i].x, gb[i].y);
             }
+            // the group's scales may have come from a window that is pulled back
+            read_scales(s, 2 * s - window(s) + half, e);
+        }
+        for (; s < full; s++) {
+            read_all(s, 2, h);
+            products(no{}, f);
+            wait_and_meet<0>();
+            if (s + Gm::slots < stages) copy_stage(s + Gm::slots);
+            products(yes{}, h);
+            if (s + 1 < full) {
+                read_all(s + 1, 0, f);
+                read_scales(s + 1, 2 * s + 2 - window(s + 1) + half, e);
+            }
+        }
+        if (granules & 1) {                                  // the last granule, alone: pieces 4 + 2 * half
+            read_all(full, 4 ^ (6 * half), f);
+            read_scales(full, granules - 1 - window(full), e);
+#pragma unroll
+            for (int i = 0; i < FM; i++) e.a[i] >>= 16 * half;
+#pragma unroll
+            for (int i = 0; i < FN; i++) e.b[i] >>= 16 * half;
+            products(no{}, f);
+        }
+
+        // the next tile's first copies go out before this one's results
+        const int64_t m_done = m0 + (wave & 1) * 32 * FM + r, n_done = n0 + (wave >> 1) * 32 * FN;
+        const bool whole = m0 + Gm::TM <= M && n0 + Gm::TN <= N;
+        tile += groups;
+        const bool more = tile < tiles;
+        if (more) {
+            wait_lds_and_meet();                             // every wave is done with the slots
+            set_tile(tile);
+            copy_first();
+        }
+        static_for<FM * FN>([&](auto I) __attribute__((always_inline)) {
+            constexpr int i = I / FN, j = I % FN;
+            store_fragment<CT>(acc[i][j], c, ldc, m_done + 32 * i, n_done + 32 * j, half, M, N, whole);
+        });
+        if (!more) break;
+        // the copies are older than the stores, of which a whole tile has `stores` at least
+        if (whole) wait_and_meet<(Gm::template stores<CT>() < 63 ? Gm::template stores<CT>() : 63)>();
+        else wait_and_meet<0>();
     }
 }
 
@@ -441,8 +510,11 @@ hipError_t run_tiled(const uint8_t *a, const uint8_t *as, const uint8_t *b, cons
                      int64_t N, int64_t granules, void *c, int64_t ldc, hipStream_t st) {
     using Gm = tgeom<FM, FN>;
     const int64_t mt = (M + Gm::TM - 1) / Gm::TM, nt = (N + Gm::TN - 1) / Gm::TN;
-    hipLaunchKernelGGL((k_mx_matmul_tiled<FM, FN, CT>), dim3((unsigned)(mt * nt)), dim3(kThreads), 0, st, a,
-                       as, b, bs, M, N, (uint32_t)granules, (uint32_t)mt, (uint32_t)nt, c, ldc);
+    // as many work-groups as the GPU holds walk the tiles (a multiple of 8, so that each
+    // stays on its XCD's tiles)
+    const unsigned groups = (unsigned)std::min<int64_t>(mt * nt, kCUs * Gm::waves_per_simd);
+    hipLaunchKernelGGL((k_mx_matmul_tiled<FM, FN, CT>), dim3(groups), dim3(kThreads), 0, st, a, as, b, bs, M,
+                       N, (uint32_t)granules, (uint32_t)mt, (uint32_t)nt, groups, c, ldc);
     return hipGetLastError();
 }
 
