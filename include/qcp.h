@@ -255,6 +255,8 @@ int adamw_step(float *const *params, const void *const *grads, void *const *copi
  *              elements apart, ld >= cols
  *   transpose  0: the payload of x (lines = rows, blocks along its rows);
  *              1: the payload of x^T (lines = cols, blocks along its columns)
+ * Both: the payloads of x (codes, scales) and of x^T (codes_t, scales_t), reading
+ * x once: what the forward and the backward product of a layer take.
  * Dequantize: y (rows x cols of type yt, rows ld apart) is code * 2^(e-127) rounded
  * once to yt.
  *   codes, scales   16-byte aligned; lines * P <= qcp_max_elements(), n <= 2^31
@@ -262,6 +264,8 @@ int adamw_step(float *const *params, const void *const *grads, void *const *copi
  */
 int mxfp4_quantize(const void *x, int xt, int64_t rows, int64_t cols, int64_t ld, int32_t transpose,
                    uint8_t *codes, uint8_t *scales, void *stream);
+int mxfp4_quantize_both(const void *x, int xt, int64_t rows, int64_t cols, int64_t ld, uint8_t *codes,
+                        uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t, void *stream);
 int mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *y,
                      int yt, int64_t ld, void *stream);
 

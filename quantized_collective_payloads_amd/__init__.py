@@ -18,6 +18,7 @@ Functions (same names as the C entry points):
     fp8_accum_requant(state_codes, state_scales, grad, G)   (in place)
     AdamW(params, copies, state, G), adamw_step(optimizer, grads, step, lr, ...)
     mxfp4_quantize(x, transpose)                       -> (codes, scales)
+    mxfp4_quantize_both(x)                             -> (codes, scales), (codes, scales) of x.t()
     mxfp4_dequantize(codes, scales, cols, dtype)       -> y
     mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, dtype) -> A B^T
     mxfp4_linear(x, weight)                            -> y (differentiable)
@@ -32,7 +33,7 @@ import torch
 
 __all__ = ["quantize_blockwise", "dequantize_blockwise", "pack_subbyte", "unpack_subbyte",
            "dequant_reduce_requant", "fp8_accum_requant", "payload_bytes", "code_bytes",
-           "n_blocks", "AdamW", "adamw_step", "mxfp4_quantize", "mxfp4_dequantize",
+           "n_blocks", "AdamW", "adamw_step", "mxfp4_quantize", "mxfp4_quantize_both", "mxfp4_dequantize",
            "mxfp4_matmul", "mxfp4_linear", "mxfp4_padded", "QcpError", "library", "FORMATS", "DTYPES", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqcp.so")
@@ -75,6 +76,7 @@ def library():
             "adamw_step": [p, p, p, p, p, i32, ci, ci, ci, p, p, p, p, i64, i32, i64, f64, f64, f64,
                            f64, f64, p, ctypes.c_uint64, p],
             "mxfp4_quantize": [p, ci, i64, i64, i64, i32, p, p, p],
+            "mxfp4_quantize_both": [p, ci, i64, i64, i64, p, p, p, p, p],
             "mxfp4_dequantize": [p, p, i64, i64, p, ci, i64, p],
             "mxfp4_matmul": [p, p, p, p, i64, i64, i64, p, ci, i64, p],
             "qcp_aquavit_level": [i64, i64, ctypes.c_double, ctypes.c_double,
@@ -408,5 +410,5 @@ def fp8_accum_requant(state_codes: torch.Tensor, state_scales: torch.Tensor, gra
 
 # these modules use the helpers above
 from .mxfp4 import (mxfp4_dequantize, mxfp4_linear, mxfp4_matmul, mxfp4_padded,  # noqa: E402
-                    mxfp4_quantize)
+                    mxfp4_quantize, mxfp4_quantize_both)
 from .optimizer import AdamW, adamw_step  # noqa: E402

@@ -337,6 +337,26 @@ int mxfp4_quantize(const void *x, int xt, int64_t rows, int64_t cols, int64_t ld
                                              (hipStream_t)stream));
 }
 
+int mxfp4_quantize_both(const void *x, int xt, int64_t rows, int64_t cols, int64_t ld, uint8_t *codes,
+                        uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t, void *stream) {
+    int64_t xb, pad, pad_t;
+    int rc = check_matrix(rows, cols, ld, xt, &xb);
+    if (rc != QCP_OK) return rc;
+    if (rows == 0 || cols == 0) return QCP_OK;
+    if (!mx_payload(rows, cols, &pad) || !mx_payload(cols, rows, &pad_t)) return QCP_EINVAL;
+    if (!x || !codes || !scales || !codes_t || !scales_t) return QCP_EINVAL;
+    if ((uintptr_t)x % dtype_bytes(xt) || !aligned16(codes) || !aligned16(scales) || !aligned16(codes_t) ||
+        !aligned16(scales_t))
+        return QCP_EALIGN;
+    const void *at[5] = {x, codes, scales, codes_t, scales_t};
+    const int64_t bytes[5] = {xb, rows * pad / 2, rows * pad / 32, cols * pad_t / 2, cols * pad_t / 32};
+    for (int i = 0; i < 5; i++)
+        for (int j = i + 1; j < 5; j++)
+            if (overlap(at[i], bytes[i], at[j], bytes[j])) return QCP_EINVAL;
+    return status_of(qcp::launch_mx_quantize_both(x, xt, rows, cols, ld, codes, scales, codes_t, scales_t,
+                                                  (hipStream_t)stream));
+}
+
 int mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, void *y,
                      int yt, int64_t ld, void *stream) {
     int64_t yb, pad;

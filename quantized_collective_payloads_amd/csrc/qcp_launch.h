@@ -66,6 +66,9 @@ hipError_t launch_adamw(const AdamwTensor *t, int n, int gt, int state, int G, c
 // the MXFP4 payload of x (transpose: of x^T), and back; see qcp_mxfp4.hip
 hipError_t launch_mx_quantize(const void *x, int xt, int64_t rows, int64_t cols, int64_t ld,
                               int transpose, uint8_t *codes, uint8_t *scales, hipStream_t st);
+hipError_t launch_mx_quantize_both(const void *x, int xt, int64_t rows, int64_t cols, int64_t ld,
+                                   uint8_t *codes, uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t,
+                                   hipStream_t st);
 hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,
                                 int64_t cols, void *y, int yt, int64_t ld, hipStream_t st);
 

@@ -28,6 +28,9 @@
 // neighbouring columns of 32 rows, so its two blocks need no other lane: absmax,
 // scale and codes all come from its own registers.  One input row of the tile and
 // one output row are both 128 bytes; the codes pass through LDS to be stored so.
+// For both payloads at once the tile is 256 x 128 and also goes through LDS as it is
+// (fp32: is read again, from L2), to be taken by rows, a block of 32 values per thread:
+// memory sees the matrix once.
 #include "qcp_device.h"
 #include "qcp_launch.h"
 
@@ -46,15 +49,17 @@ constexpr int kMxVecs = 4;        // vectors of 8 values per lane
 
 template <int XT> constexpr int words8() { return XT == F32 ? 8 : 4; }   // dwords of 8 values
 
-// 8 values from p, of which `count` exist (the others are zero)
-template <int XT>
+// 8 values from p, of which `count` exist (the others are zero).  STREAM: read once
+template <int XT, bool STREAM = true>
 __device__ __forceinline__ void load8(const void *x, int64_t i, int count, uint32_t (&w)[words8<XT>()]) {
     constexpr int B = dtype_traits<XT>::bytes;
     const uint8_t *p = (const uint8_t *)x + i * B;
     if (count >= 8) {
 #pragma unroll
         for (int k = 0; k < words8<XT>() / 4; k++) {
-            const u32x4_any v = __builtin_nontemporal_load((const u32x4_any *)p + k);
+            u32x4_any v;
+            if constexpr (STREAM) v = __builtin_nontemporal_load((const u32x4_any *)p + k);
+            else v = *((const u32x4_any *)p + k);
             w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
         }
     } else {
@@ -341,17 +346,38 @@ __global__ __launch_bounds__(kThreads) void k_mx_dequantize(const uint32_t *__re
     }
 }
 
-constexpr int kTRows = 256, kTCols = 64;       // tile of the column-wise quantize
+constexpr int kTRows = 256;                    // tile of the column-wise quantize
+template <bool BOTH> constexpr int tile_cols() { return BOTH ? 128 : 64; }
 
+// the codes and the scale byte of one block of a row
 template <int XT>
-__global__ __launch_bounds__(kThreads) void k_mx_quantize_t(const void *__restrict__ x, int64_t rows,
+__device__ __forceinline__ uint4 row_block(const uint32_t (&w)[4][words8<XT>()], uint32_t &e) {
+    uint32_t c[4], m = 0;
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+#pragma unroll
+        for (int j = 0; j < words8<XT>(); j++) m = absmax_of<XT>(m, w[k][j]);
+    e = scale_byte<XT>(m);
+#pragma unroll
+    for (int k = 0; k < 4; k++) c[k] = encode8<XT>(w[k], scale_of(e));
+    return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+template <int XT, bool BOTH>
+__global__ __launch_bounds__(4 * tile_cols<BOTH>()) void k_mx_quantize_t(const void *__restrict__ x, int64_t rows,
                                                             int64_t cols, int64_t ld, uint32_t col_tiles, uint32_t groups,
                                                             int64_t pad_rows, uint8_t *__restrict__ codes,
-                                                            uint8_t *__restrict__ scales) {
-    constexpr int B = dtype_traits<XT>::bytes;
+                                                            uint8_t *__restrict__ scales, int64_t pad_cols,
+                                                            uint8_t *__restrict__ row_codes,
+                                                            uint8_t *__restrict__ row_scales) {
+    constexpr int B = dtype_traits<XT>::bytes, kTCols = tile_cols<BOTH>();
     constexpr int kLine = 128 + 16;            // bytes per column in LDS: a shift of 4 banks
-    __shared__ __attribute__((aligned(16))) uint8_t lines[kTCols * kLine];
-    __shared__ __attribute__((aligned(8))) uint8_t marks[kTCols * 8];
+    // 16-bit input of both payloads: the tile itself lies here first, rows 16 bytes
+    // more than their 256 apart, which spreads the row pass over all banks
+    constexpr bool kStage = BOTH && XT != F32;
+    constexpr int kRow = kTCols * B + 16, kNeed = kTCols * (kLine + 8);
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kStage ? kTRows * kRow : kNeed];
+    uint8_t *const lines = lds, *const marks = lds + kTCols * kLine;
     // Work-groups are dealt round-robin to the 8 XCDs.  16 neighbouring tiles, 2 KB of
     // a 16-bit row, go to one XCD, so that its reads spread over all its L2 channels;
     // in launch order they would lie 1 KB apart, a quarter of the channels.
@@ -359,8 +385,8 @@ __global__ __launch_bounds__(kThreads) void k_mx_quantize_t(const void *__restri
     if (wg < (groups & ~127u)) wg = (wg & ~127u) + (wg & 7) * 16 + ((wg >> 3) & 15);
     const int64_t tr = (int64_t)(wg / col_tiles) * kTRows, tc = (int64_t)(wg % col_tiles) * kTCols;
     const int tid = (int)__builtin_amdgcn_workitem_id_x();
-    const int block = tid >> 5;                // which 32 rows of the tile
-    const int pair = tid & 31;                 // which two columns
+    const int block = tid / (kTCols / 2);      // which 32 rows of the tile
+    const int pair = tid % (kTCols / 2);       // which two columns
     const int64_t r0 = tr + block * 32, c0 = tc + pair * 2;
     const int64_t have = rows - r0;            // rows of this block that exist (may be <= 0)
     const int two = cols - c0 >= 2 ? 2 : cols - c0 == 1 ? 1 : 0;
@@ -384,6 +410,39 @@ __global__ __launch_bounds__(kThreads) void k_mx_quantize_t(const void *__restri
             if (r < have && two == 2) a[r] = *(const u32_any *)q;
             else if (r < have && two == 1) a[r] = *(const uint16_t *)q;
         }
+    }
+    // the tile along its rows: a thread takes a block of 32 at a time, 4 threads the 128
+    // columns of a row, whose scales are one dword
+    if constexpr (BOTH) {
+        if constexpr (kStage) {
+#pragma unroll
+            for (int r = 0; r < 32; r++) *(uint32_t *)(lds + (block * 32 + r) * kRow + pair * 4) = a[r];
+            __syncthreads();
+        }
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            const int unit = tid + 4 * kTCols * k;
+            const int64_t r = tr + (unit >> 2), c = tc + 32 * (unit & 3);
+            uint32_t w[4][words8<XT>()], e;
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                if constexpr (kStage) {
+                    const uint4 v = *(const uint4 *)(lds + (unit >> 2) * kRow + (unit & 3) * 64 + 16 * q);
+                    w[q][0] = v.x; w[q][1] = v.y; w[q][2] = v.z; w[q][3] = v.w;
+                } else {                       // from L2, where the tile has just been
+                    const int64_t left = r < rows ? cols - c - 8 * q : 0;
+                    load8<XT, false>(x, r * ld + c + 8 * q, left > 8 ? 8 : left < 0 ? 0 : (int)left, w[q]);
+                }
+            }
+            const uint4 v = row_block<XT>(w, e);
+            uint32_t d = e << (8 * (unit & 3));
+            d |= dpp_u32<0xB1>(d);
+            d |= dpp_u32<0x4E>(d);
+            if (r >= rows) continue;
+            *(uint4 *)(row_codes + r * (pad_cols / 2) + c / 2) = v;
+            if ((unit & 3) == 0) *(uint32_t *)(row_scales + r * (pad_cols / 32) + tc / 32) = d;
+        }
+        if constexpr (kStage) __syncthreads();
     }
     uint32_t ma = 0, mb = 0;
 #pragma unroll
@@ -418,11 +477,11 @@ __global__ __launch_bounds__(kThreads) void k_mx_quantize_t(const void *__restri
     marks[(2 * pair + 1) * 8 + block] = (uint8_t)eb;
     __syncthreads();
 
-    // 64 output rows of 128 bytes: 8 threads a row; the padded height may end halfway
+    // output rows of 128 bytes: 8 threads a row; the padded height may end halfway
     const int64_t wide = pad_rows - tr;        // 128 or at least 256
 #pragma unroll
     for (int k = 0; k < 2; k++) {
-        const int line = (tid >> 3) + 32 * k, piece = tid & 7;
+        const int line = (tid >> 3) + kTCols / 2 * k, piece = tid & 7;
         const int64_t c = tc + line;
         if (c < cols && 32 * piece < wide)
             *(uint4 *)(codes + c * (pad_rows / 2) + tr / 2 + 16 * piece) =
@@ -442,9 +501,10 @@ hipError_t run_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, i
                         uint8_t *codes, uint8_t *scales, hipStream_t st) {
     if (transpose) {
         const int64_t pad = (rows + kMxPad - 1) / kMxPad * kMxPad;
-        const int64_t ct = (cols + kTCols - 1) / kTCols, rt = (rows + kTRows - 1) / kTRows;
-        hipLaunchKernelGGL((k_mx_quantize_t<XT>), dim3((unsigned)(ct * rt)), dim3(kThreads), 0, st, x, rows,
-                           cols, ld, (uint32_t)ct, (uint32_t)(ct * rt), pad, codes, scales);
+        const int64_t ct = (cols + tile_cols<false>() - 1) / tile_cols<false>(), rt = (rows + kTRows - 1) / kTRows;
+        hipLaunchKernelGGL((k_mx_quantize_t<XT, false>), dim3((unsigned)(ct * rt)), dim3(kThreads), 0, st, x,
+                           rows, cols, ld, (uint32_t)ct, (uint32_t)(ct * rt), pad, codes, scales, (int64_t)0,
+                           (uint8_t *)nullptr, (uint8_t *)nullptr);
         return hipGetLastError();
     }
     const int64_t pad = (cols + kMxPad - 1) / kMxPad * kMxPad;
@@ -457,6 +517,16 @@ hipError_t run_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, i
     else
         hipLaunchKernelGGL((k_mx_quantize<XT, false>), dim3(grid), dim3(kThreads), 0, st, x, vecs,
                            (uint32_t)(pad / 8), cols, ld, (uint32_t *)codes, scales);
+    return hipGetLastError();
+}
+
+template <int XT>
+hipError_t run_quantize_both(const void *x, int64_t rows, int64_t cols, int64_t ld, uint8_t *codes,
+                             uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t, hipStream_t st) {
+    const int64_t pr = (rows + kMxPad - 1) / kMxPad * kMxPad, pc = (cols + kMxPad - 1) / kMxPad * kMxPad;
+    const int64_t ct = pc / tile_cols<true>(), rt = (rows + kTRows - 1) / kTRows;
+    hipLaunchKernelGGL((k_mx_quantize_t<XT, true>), dim3((unsigned)(ct * rt)), dim3(4 * tile_cols<true>()), 0, st, x, rows,
+                       cols, ld, (uint32_t)ct, (uint32_t)(ct * rt), pr, codes_t, scales_t, pc, codes, scales);
     return hipGetLastError();
 }
 
@@ -484,6 +554,17 @@ hipError_t launch_mx_quantize(const void *x, int xt, int64_t rows, int64_t cols,
     case F16: return run_quantize<F16>(x, rows, cols, ld, transpose, codes, scales, st);
     case BF16: return run_quantize<BF16>(x, rows, cols, ld, transpose, codes, scales, st);
     case F32: return run_quantize<F32>(x, rows, cols, ld, transpose, codes, scales, st);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_mx_quantize_both(const void *x, int xt, int64_t rows, int64_t cols, int64_t ld,
+                                   uint8_t *codes, uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t,
+                                   hipStream_t st) {
+    switch (xt) {
+    case F16: return run_quantize_both<F16>(x, rows, cols, ld, codes, scales, codes_t, scales_t, st);
+    case BF16: return run_quantize_both<BF16>(x, rows, cols, ld, codes, scales, codes_t, scales_t, st);
+    case F32: return run_quantize_both<F32>(x, rows, cols, ld, codes, scales, codes_t, scales_t, st);
     default: return hipErrorInvalidValue;
     }
 }

@@ -638,12 +638,14 @@ hipError_t run_matmul(const uint8_t *a, const uint8_t *as, const uint8_t *b, con
     if (rows && small <= 64 && granules <= 32) return run_rows<4, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
     if (staged) {
         // 64 x 64 while they fit the GPU twice over (512 x 4096, K = 4096: 12.6 us
-        // against 13.2 with 128 x 128); then whichever of 128 x 128, of which the GPU
-        // holds 512, and 256 x 256, 256 at a time, has the shorter rounds: a full round
-        // of the former takes 0.63 of the latter's (8192 x 8192, K = 28672: 1177 us
-        // against 917; 2048 x 4096, K = 14336, 512 tiles against 128: 80 us against 93)
+        // against 13.2 with 128 x 128); then 128 x 128, 512 at a time, or 256 x 256, 256
+        // at a time, by what their rounds take: 1.35 us a stage and 3.5 more, or 2.05 and
+        // 11 (measured against the other: 8192 x 8192, K = 28672: 1240 us and 958;
+        // 4096 x 4096, K = 4096: 52 and 45; 14336 x 4096, K = 2048: 104 and 112;
+        // 2048 x 4096, K = 14336: 82 and 95)
+        const int64_t stages = (granules + 1) / 2;
         if (small <= 512) return run_tiled<1, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
-        if (63 * ((middle + 511) / 512) < 100 * ((large + 255) / 256))
+        if ((middle + 511) / 512 * (27 * stages + 70) < (large + 255) / 256 * (41 * stages + 220))
             return run_tiled<2, 2, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
         return run_tiled<4, 4, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
     }

@@ -121,6 +121,34 @@ def mxfp4_quantize(x: torch.Tensor, transpose: bool = False, codes=None, scales=
     return codes, scales
 
 
+def mxfp4_quantize_both(x: torch.Tensor):
+    """The payloads of a 2-D fp16/bf16/fp32 GPU tensor and of its transpose, as
+    mxfp4_quantize(x) and mxfp4_quantize(x, transpose=True) give them, in one pass."""
+    if type(x) is not torch.Tensor or x.dim() != 2 or x.dtype not in DTYPES:
+        _matrix(x, "x")
+    rows, cols = x.shape
+    ld, swap = cols, False
+    if not x.is_contiguous():
+        if x.numel() and x.stride(1) != 1 and x.stride(0) == 1 and x.stride(1) >= rows:
+            x, swap = x.t(), True
+            rows, cols = cols, rows
+            ld = x.stride(0)
+        elif x.stride(1) == 1 and x.stride(0) >= cols:
+            ld = x.stride(0)
+        else:
+            x = x.contiguous()
+    index = x.get_device()
+    if index < 0:
+        _dev(x)
+    pc, pr = _pad(cols), _pad(rows)
+    empty = lambda *s: torch.empty(s, dtype=_u8, device=x.device)  # noqa: E731
+    a = empty(rows, pc // 2), empty(rows, pc // 32)
+    b = empty(cols, pr // 2), empty(cols, pr // 32)
+    _enqueue("mxfp4_quantize_both", index, x.data_ptr(), DTYPES[x.dtype], rows, cols, ld, a[0].data_ptr(),
+             a[1].data_ptr(), b[0].data_ptr(), b[1].data_ptr())
+    return (b, a) if swap else (a, b)
+
+
 def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int, dtype=torch.bfloat16, out=None):
     """The [lines, cols] values that a payload stands for, rounded once to `dtype`."""
     lines, P, index = _payload(codes, scales, "")
@@ -160,15 +188,25 @@ class _Work:
             self.places.append((at, at + lines * P // 2))
             at += lines * P // 2 + (lines * P // 32 + 15) // 16 * 16
         self.buffer = torch.empty(at, dtype=_u8, device=like.device)
-        self.base = self.buffer.data_ptr()
 
     def __getitem__(self, k):
-        codes, scales = self.places[k]
-        return self.base + codes, self.base + scales
+        return _at(self.buffer, self.places[k])
 
 
-def _quantize_to(index, x, rows, cols, ld, transpose, place):
-    _enqueue("mxfp4_quantize", index, x.data_ptr(), DTYPES[x.dtype], rows, cols, ld, transpose, *place)
+def _at(buffer, place):
+    base = buffer.data_ptr()
+    return base + place[0], base + place[1]
+
+
+def _quantize_to(index, x, rows, cols, straight, transposed):
+    """The payload of x, of its transpose, or both, to the addresses given."""
+    if transposed is None:
+        _enqueue("mxfp4_quantize", index, x.data_ptr(), DTYPES[x.dtype], rows, cols, cols, 0, *straight)
+    elif straight is None:
+        _enqueue("mxfp4_quantize", index, x.data_ptr(), DTYPES[x.dtype], rows, cols, cols, 1, *transposed)
+    else:
+        _enqueue("mxfp4_quantize_both", index, x.data_ptr(), DTYPES[x.dtype], rows, cols, cols, *straight,
+                 *transposed)
 
 
 def _product(index, a, b, M, N, K, dtype, like):
@@ -180,41 +218,38 @@ def _product(index, a, b, M, N, K, dtype, like):
 class _Linear(torch.autograd.Function):
     """y = Q(x) Q(w)^T, with Q along the dimension that is summed over; the
     backward products round dy, w and x along theirs, so gradients are those of
-    the products with the rounding passed straight through.  Of x, only the 4-bit
-    payload that dW needs is kept."""
+    the products with the rounding passed straight through.  The forward reads x
+    and w once for both payloads of each, and keeps only the 4-bit ones that the
+    backward needs."""
 
     @staticmethod
     def forward(ctx, x, w):
         index, (T, I), O = x.get_device(), x.shape, w.shape[0]
         need_x, need_w = ctx.needs_input_grad
         work = _Work(x, (T, I), (O, I))
-        _quantize_to(index, x, T, I, I, 0, work[0])
-        _quantize_to(index, w, O, I, I, 0, work[1])
+        kept = _Work(x, *([(I, O)] if need_x else []), *([(I, T)] if need_w else [])) if need_x or need_w else None
+        _quantize_to(index, x, T, I, work[0], kept[-1] if need_w else None)
+        _quantize_to(index, w, O, I, work[1], kept[0] if need_x else None)
         y = _product(index, work[0], work[1], T, O, I, x.dtype, x)
-        kept = None
-        if need_w:
-            kept = _Work(x, (I, T))
-            _quantize_to(index, x, T, I, I, 1, kept[0])
-        ctx.save_for_backward(w if need_x else None, kept and kept.buffer)
-        ctx.kinds, ctx.sizes, ctx.place = (x.dtype, w.dtype), (T, I, O), kept and kept.places[0]
+        if kept is not None:
+            ctx.save_for_backward(kept.buffer)
+            ctx.kinds, ctx.sizes, ctx.places = (x.dtype, w.dtype), (T, I, O), kept.places
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        w, kept = ctx.saved_tensors
+        kept, = ctx.saved_tensors
         T, I, O = ctx.sizes
+        need_x, need_w = ctx.needs_input_grad
         index, dx, dw = dy.get_device(), None, None
         dy = dy.contiguous()
-        work = _Work(dy, *([(T, O), (I, O)] if w is not None else []), *([(O, T)] if kept is not None else []))
-        if w is not None:
-            _quantize_to(index, dy, T, O, O, 0, work[0])
-            _quantize_to(index, w, O, I, I, 1, work[1])
-            dx = _product(index, work[0], work[1], T, I, O, ctx.kinds[0], dy)
-        if kept is not None:
-            _quantize_to(index, dy, T, O, O, 1, work[-1])
-            base = kept.data_ptr()
-            dw = _product(index, work[-1], (base + ctx.place[0], base + ctx.place[1]), O, I, T, ctx.kinds[1], dy)
+        work = _Work(dy, *([(T, O)] if need_x else []), *([(O, T)] if need_w else []))
+        _quantize_to(index, dy, T, O, work[0] if need_x else None, work[-1] if need_w else None)
+        if need_x:
+            dx = _product(index, work[0], _at(kept, ctx.places[0]), T, I, O, ctx.kinds[0], dy)
+        if need_w:
+            dw = _product(index, work[-1], _at(kept, ctx.places[-1]), O, I, T, ctx.kinds[1], dy)
         return dx, dw
 
 

@@ -77,6 +77,17 @@ def test_quantize_and_back(gpu, rows, cols, dt, transpose):
 
 
 @GPU
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,cols", SHAPES + [(513, 449), (1024, 192)])
+def test_both_payloads_in_one_pass(gpu, rows, cols, dt):
+    x = values(rows, cols, dt, rows + 3 * cols)
+    wide_rows = values(rows + 1, cols + 7, dt, 5)[1:, 3:3 + cols]        # rows apart, unaligned
+    for v in (x, x.t(), wide_rows, wide_rows.t(), x[:1].expand(5, cols), x[:, ::2]):
+        for got, want in zip(qcp.mxfp4_quantize_both(v), (qcp.mxfp4_quantize(v), qcp.mxfp4_quantize(v, transpose=True))):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), (tuple(v.shape), v.stride())
+
+
+@GPU
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 def test_every_16_bit_value(gpu, dt):
     """All 65,536 patterns, each the largest of its block and each beside a larger
@@ -143,6 +154,8 @@ def test_nothing_outside_the_payload_is_written(gpu):
 @GPU
 def test_empty(gpu):
     for shape in ((0, 5), (5, 0), (0, 0)):
+        for (c, s), n in zip(qcp.mxfp4_quantize_both(torch.zeros(shape, device="cuda")), (shape[1], shape[0])):
+            assert c.shape[1] == qcp.mxfp4_padded(n) // 2
         for transpose in (False, True):
             c, s = qcp.mxfp4_quantize(torch.zeros(shape, device="cuda"), transpose=transpose)
             lines, n = shape[::-1] if transpose else shape
@@ -373,6 +386,14 @@ def test_c_entries_refuse(lib):
 
     def mul(a=A, sa=A + S, b=A + 2 * S, sb=A + 3 * S, M=64, N=64, K=256, c=A + 4 * S, ct=2, ldc=64):
         return lib.mxfp4_matmul(a, sa, b, sb, M, N, K, c, ct, ldc, None)
+    def both(x=A, xt=2, rows=64, cols=256, ld=256, c=A + S, s=A + 2 * S, ct=A + 3 * S, st=A + 4 * S):
+        return lib.mxfp4_quantize_both(x, xt, rows, cols, ld, c, s, ct, st, None)
+    assert both(rows=0) == OK and both(cols=0, ld=0) == OK
+    for bad in (dict(x=0), dict(xt=5), dict(ct=0), dict(st=0), dict(ld=255), dict(ct=A + S + 64), dict(st=A + 3 * S),
+                dict(s=A), dict(st=A + 2 * S + 16), dict(rows=1 << 33, cols=1, ld=1), dict(cols=1 << 32, ld=1 << 32, rows=1)):
+        assert both(**bad) == EINVAL, bad
+    for bad in (dict(x=A + 1), dict(c=A + S + 8), dict(st=A + 4 * S + 4)):
+        assert both(**bad) == EALIGN, bad
     for f in (quant, dequant):
         assert f(rows=0) == OK and f(cols=0, ld=0) == OK
         for bad in (dict(rows=-1), dict(cols=-1), dict(ld=255), dict(c=0), dict(s=0), dict(rows=1 << 40),
@@ -410,6 +431,8 @@ def test_binding_refuses(lib):
     raises("codes: shape", qcp.mxfp4_quantize, torch.zeros(4, 64), codes=u8(4, 32))
     raises("scales: dtype", qcp.mxfp4_quantize, torch.zeros(4, 64), scales=torch.zeros(4, 4))
     raises("GPU tensors only", qcp.mxfp4_quantize, torch.zeros(4, 64))
+    raises("x: 3 dimensions", qcp.mxfp4_quantize_both, torch.zeros(2, 4, 64))
+    raises("GPU tensors only", qcp.mxfp4_quantize_both, torch.zeros(4, 64))
     raises("codes: rows of 60 bytes", qcp.mxfp4_dequantize, u8(4, 60), u8(4, 4), 100)
     raises("scales: shape", qcp.mxfp4_dequantize, u8(4, 64), u8(4, 8), 100)
     raises("codes: rows of 128 values for 129", qcp.mxfp4_dequantize, u8(4, 64), u8(4, 4), 129)
