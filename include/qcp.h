@@ -20,8 +20,8 @@
  *
  * Conventions shared by every entry point
  *  - Pointers are device pointers (HBM), except where a comment says otherwise.
- *    The caller allocates and frees every buffer; the library allocates no device
- *    memory, keeps no pointer after returning and holds no mutable global state.
+ *    The caller allocates and frees every buffer; the library allocates nothing,
+ *    keeps no pointer after returning and holds no mutable global state.
  *  - `stream` is a hipStream_t (NULL = the legacy default stream).  Every call
  *    enqueues its kernel(s) on `stream` and returns without synchronizing; the
  *    status reports argument validation and launch errors only.
@@ -62,8 +62,7 @@ typedef enum {
     QCP_EINVAL = -1,        /* bad size, G, b, format, dtype, stride, null or overlapping pointer */
     QCP_EALIGN = -2,        /* a pointer or stride is not a multiple of 16 bytes */
     QCP_EUNSUPPORTED = -3,  /* a combination this library does not implement */
-    QCP_EHIP = -4,          /* the HIP runtime reported an error at launch */
-    QCP_ENOMEM = -5         /* no host memory for a call's table of tensors (adamw_step) */
+    QCP_EHIP = -4           /* the HIP runtime reported an error at launch */
 } qcp_status;
 
 typedef enum { QCP_F16 = 1, QCP_BF16 = 2, QCP_F32 = 3 } qcp_dtype;
@@ -226,12 +225,11 @@ int fp8_accum_requant(uint8_t *state_codes, float *state_scales, const void *gra
  *             or unscaling factor, read when the kernel runs
  *   seed      of the hash; unused with QCP_F32
  * The host arrays are read before the call returns.  m, v and the scales are
- * 16-byte aligned.  At most QCP_ADAMW_MAX_TENSORS tensors; tensors without
+ * 16-byte aligned.  At most QCP_ADAMW_MAX_TENSORS tensors a call; tensors without
  * elements are skipped.  No two buffers overlap, except that gradients may.
- * One kernel launch per 64 tensors.  Errors: QCP_EINVAL, QCP_EALIGN, QCP_ENOMEM,
- * QCP_EHIP.
+ * One kernel launch per 64 tensors.  Errors: QCP_EINVAL, QCP_EALIGN, QCP_EHIP.
  */
-#define QCP_ADAMW_MAX_TENSORS 65536
+#define QCP_ADAMW_MAX_TENSORS 1024
 int adamw_step(float *const *params, const void *const *grads, void *const *copies,
                const int64_t *sizes, const int64_t *offsets, int32_t n_tensors, int gt, int ct,
                int state, void *m, float *m_scales, void *v, float *v_scales, int64_t n_state,

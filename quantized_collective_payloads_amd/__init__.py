@@ -41,8 +41,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqcp.so")
 # numbering of include/qcp.h
 DTYPES = {torch.float16: 1, torch.bfloat16: 2, torch.float32: 3}
 FORMATS = {"int2": 2, "int4": 4, "int6": 6, "int8": 8, "e4m3": 0x43}
-_STATUS = {0: "QCP_OK", -1: "QCP_EINVAL", -2: "QCP_EALIGN", -3: "QCP_EUNSUPPORTED", -4: "QCP_EHIP",
-           -5: "QCP_ENOMEM"}
+_STATUS = {0: "QCP_OK", -1: "QCP_EINVAL", -2: "QCP_EALIGN", -3: "QCP_EUNSUPPORTED", -4: "QCP_EHIP"}
 
 _lib = None
 

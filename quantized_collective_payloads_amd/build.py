@@ -23,8 +23,8 @@ LIB = os.path.join(HERE, "libqcp.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["qcp_api.hip", "qcp_codec.hip", "qcp_reduce.hip", "qcp_adamw.hip", "qcp_mxfp4.hip",
-           "qcp_mxfp4_matmul.hip"]
+SOURCES = ["qcp_api.hip", "qcp_codec.hip", "qcp_reduce.hip", "qcp_ops_api.hip", "qcp_adamw.hip",
+           "qcp_mxfp4.hip", "qcp_mxfp4_matmul.hip"]
 
 CXXFLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

@@ -33,7 +33,7 @@
 // elements with fp32 moments 154 -> 137 us (5.97 TB/s), 369M with 8-bit moments
 // 1112 -> 1060 us (5.61 TB/s); either hint alone gains 1 to 3%.
 #include "qcp_device.h"
-#include "qcp_launch.h"
+#include "qcp_ops.h"
 
 namespace qcp {
 

@@ -13,7 +13,9 @@
 // and 4 scale bytes per 128, so every row of codes starts on 64 bytes, every row
 // of scales on 4, and the matrix instructions never see a short block.
 //
-// Bound: HBM; 2 + 0.53 bytes per 16-bit value for a few instructions.
+// Bound: HBM; 2 + 0.53 bytes per 16-bit value for a few instructions.  Measured on
+// 14336 x 4096 bf16: quantize 24.6 us (6.0 TB/s), its transpose 34.4 (4.3), both 40,
+// dequantize 22.9 (6.5); a copy of that matrix runs at 5.3 TB/s.
 //
 // Along the rows: a lane owns 8 consecutive values (one 16-byte load of 16-bit
 // input, one dword of codes), so a block is 4 lanes and its absmax two DPP steps,
@@ -32,7 +34,7 @@
 // (fp32: is read again, from L2), to be taken by rows, a block of 32 values per thread:
 // memory sees the matrix once.
 #include "qcp_device.h"
-#include "qcp_launch.h"
+#include "qcp_ops.h"
 
 namespace qcp {
 

@@ -9,10 +9,13 @@
 // first 32 bytes and the upper one the last, and two instructions use them up.
 // The row's 4 scale bytes are one dword; its half is shifted down once per
 // granule, and the instruction picks the byte.
+//
+// Measured: 8192 x 8192, K = 28672 876 to 958 us (4.4 to 4.0 PFLOP/s, by the GPU's
+// clock); 2048 x 14336, K = 4096 84 us (2.9); 1 x 14336, K = 4096 8.2 us (3.8 TB/s).
 #include <algorithm>
 
 #include "qcp_device.h"
-#include "qcp_launch.h"
+#include "qcp_ops.h"
 
 namespace qcp {
 
@@ -118,8 +121,9 @@ __global__ __launch_bounds__(kThreads) void k_mx_matmul(const uint8_t *__restric
 // ---------------------------------------------------------------------------
 // 64*FM x 64*FN of C per work-group, staged through LDS.
 // ---------------------------------------------------------------------------
-// Bound: the matrix cores, and their power (random codes multiplied in registers
-// alone reach 5.8 PFLOP/s).  Four waves, 2 x 2, hold 32*FM x 32*FN each.  At 4 x 4
+// Bound: the matrix cores, and their power: random codes multiplied in registers alone
+// reach 5.8 PFLOP/s, and the same call on codes of zero takes a fifth less time than on
+// normal values.  Four waves, 2 x 2, hold 32*FM x 32*FN each.  At 4 x 4
 // that is 256 x 256 per work-group and 256 accumulators, one wave per SIMD: a
 // phase is 32 instructions of 32 cycles on 16 KB of operands, a quarter of what LDS
 // gives.  At 2 x 2, 128 x 128, two work-groups share a CU: twice the operand traffic
@@ -521,7 +525,8 @@ hipError_t run_tiled(const uint8_t *a, const uint8_t *as, const uint8_t *b, cons
 // ---------------------------------------------------------------------------
 // Few rows of A (a token, a small batch): 16*FA rows against 16*FB rows of B.
 // ---------------------------------------------------------------------------
-// Bound: reading B once.  v_mfma_scale_f32_16x16x128_f8f6f4 takes 16 rows, so N/16
+// Bound: reading B once, at these sizes the latency of it (1 x 14336, K = 4096: 31 MB in
+// 8.2 us; the smallest calls take 3.3).  v_mfma_scale_f32_16x16x128_f8f6f4 takes 16 rows, so N/16
 // work-groups; the WV waves of one deal out K in steps of 512 and add their sums in
 // LDS in a fixed order, so a few rows still fill the GPU, without a second launch.  Of a step's 4 granules
 // a quarter-wave takes one: a lane reads 64 consecutive bytes of its row and one

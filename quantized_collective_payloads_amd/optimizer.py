@@ -10,6 +10,7 @@ dequantize_blockwise and the collectives take as they are.
 from __future__ import annotations
 
 import ctypes
+from array import array
 
 import torch
 
@@ -17,6 +18,7 @@ from . import (DTYPES, FORMATS, _check_n_G, _dev, _ELEMS, _enqueue, _F32, _need,
 
 _STATES = {"f32": DTYPES[torch.float32], "e4m3": FORMATS["e4m3"]}
 _COPIES = (torch.float16, torch.bfloat16)
+_MAX_TENSORS = 1024                               # QCP_ADAMW_MAX_TENSORS
 
 
 def _list(ts, what: str):
@@ -96,9 +98,10 @@ class AdamW:
         n = len(params)
         self._index, self._at = device.index, [p.data_ptr() for p in params]
         self._written = params + (copies or [])
-        self._table = ctypes.c_void_p * n
-        self._arrays = (self._table(*self._at), None if copies is None else self._table(*(c.data_ptr() for c in copies)),
+        table = ctypes.c_void_p * n
+        self._arrays = (table(*self._at), None if copies is None else table(*(c.data_ptr() for c in copies)),
                         (ctypes.c_int64 * n)(*sizes), (ctypes.c_int64 * n)(*offsets))
+        self._bases = tuple(None if a is None else ctypes.addressof(a) for a in self._arrays)
         self._copy_type = DTYPES[copies[0].dtype] if copies else 0
         self._moments = (self._m.data_ptr(), self._m_scales.data_ptr() if eight else None,
                          self._v.data_ptr(), self._v_scales.data_ptr() if eight else None)
@@ -144,10 +147,14 @@ def adamw_step(optimizer: AdamW, grads, step: int, lr: float, beta1: float = 0.9
         _dev(o._m, grad_scale)
     if list(map(_data_ptr, o._params)) != o._at:
         raise ValueError("params: a parameter was given another storage since the AdamW was made")
-    params, copies, sizes, offsets = o._arrays
+    params, copies, sizes, offsets = o._bases
     m, ms, v, vs = o._moments
-    _enqueue("adamw_step", index, params, o._table(*map(_data_ptr, grads)), copies, sizes, offsets, len(grads),
-             DTYPES[kind], o._copy_type, _STATES[o._state], m, ms, v, vs, o._n_state, o._G, step, lr, beta1,
-             beta2, eps, weight_decay, None if grad_scale is None else grad_scale.data_ptr(),
-             seed & 0xFFFFFFFFFFFFFFFF)
+    at = array("Q", list(map(_data_ptr, grads)))              # a third of the time of a ctypes array
+    table = at.buffer_info()[0]
+    for first in range(0, len(grads), _MAX_TENSORS):
+        k = 8 * first
+        _enqueue("adamw_step", index, params + k, table + k, copies and copies + k, sizes + k, offsets + k,
+                 min(_MAX_TENSORS, len(grads) - first), DTYPES[kind], o._copy_type, _STATES[o._state], m, ms, v, vs,
+                 o._n_state, o._G, step, lr, beta1, beta2, eps, weight_decay,
+                 None if grad_scale is None else grad_scale.data_ptr(), seed & 0xFFFFFFFFFFFFFFFF)
     torch.autograd.graph.increment_version(o._written)

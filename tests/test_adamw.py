@@ -167,6 +167,19 @@ def test_many_tensors_over_several_launches(gpu):
 
 
 @GPU
+def test_more_tensors_than_a_call_takes(gpu):
+    sizes = [1 + i % 37 for i in range(2100)]
+    params, _ = flat_views(sizes, torch.float32, 1, 5, 0.02)
+    grads, _ = flat_views(sizes, torch.float32, 1, 6, 1e-3)
+    copies, _ = flat_views(sizes, torch.float16, 1, 7, 1.0)
+    opt = qcp.AdamW(params, copies=copies, state="e4m3", G=32)
+    p0, g, old = host(params), host(grads), decoded(opt)
+    qcp.adamw_step(opt, grads, 1, seed=9, **HYPER)
+    check_eight(opt, sizes, p0, g, old, 1, 9, HYPER, 1.0, host(params))
+    assert all(torch.equal(c, p.to(torch.float16)) for c, p in zip(copies, params))
+
+
+@GPU
 def test_nothing_outside_the_tensors_is_written(gpu):
     sizes = [5, 1, 4099, 64, 3]
     params, pbuf = flat_views(sizes, torch.float32, 7, 7, 0.02)
@@ -346,7 +359,7 @@ def lib():
 
 def test_c_entry_refuses(lib):
     assert call(n=0) == OK and call(sizes=[0]) == OK                  # nothing to do, no launch
-    for bad in (dict(n=-1), dict(n=65537), dict(G=100), dict(gt=0), dict(gt=9), dict(state=8), dict(step=0),
+    for bad in (dict(n=-1), dict(n=1025), dict(G=100), dict(gt=0), dict(gt=9), dict(state=8), dict(step=0),
                 dict(lr=-1.0), dict(lr=float("nan")), dict(lr=float("inf")), dict(b1=1.0), dict(b1=-0.1),
                 dict(b2=1.0), dict(b2=float("nan")), dict(eps=0.0), dict(eps=1e-60), dict(eps=float("nan")),
                 dict(wd=-0.1), dict(wd=float("inf")), dict(sizes=[-1]), dict(sizes=[1 << 40]),
