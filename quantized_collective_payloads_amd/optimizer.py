@@ -123,6 +123,9 @@ def adamw_step(optimizer: AdamW, grads, step: int, lr: float, beta1: float = 0.9
                  gradient; it is read on the device when the step runs
     seed         of the 8-bit moments' stochastic rounding: the same seed, step
                  and inputs give the same bytes
+
+    Captured into a graph, a step replays with the step number, seed and
+    hyperparameters of its capture.
     """
     o = optimizer
     if type(grads) is not list:

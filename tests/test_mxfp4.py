@@ -218,11 +218,27 @@ def test_product(gpu, M, N, K, dt):
     assert torch.equal(again, out)                       # the same bytes on every run
 
 
+# several rounds of tiles with ragged edges: 256 x 256 and 128 x 128 work-groups that walk
+# more than one tile, with an odd number of granules and with few of them
+@GPU
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(4100, 4130, 4200), (3000, 3010, 1111), (700, 3000, 520), (65, 8200, 900), (5121, 2050, 640)])
+def test_product_over_several_rounds_of_tiles(gpu, M, N, K, dt):
+    a, b = random_payload(M, K, 1), random_payload(N, K, 2)
+    buf = torch.full((M * N + 1024,), 3.0, dtype=DT[dt], device="cuda")
+    out = buf[512:512 + M * N].view(M, N)
+    for _ in range(2):
+        out.fill_(5.0)
+        qcp.mxfp4_matmul(*a, *b, out=out)
+        assert (buf[:512] == 3).all() and (buf[512 + M * N:] == 3).all()
+        check_product(a, b, out, dt, (M, N, K, dt))
+
+
 @GPU
 def test_product_of_integers_is_exact(gpu):
     """Codes at scale 1: every partial sum is a multiple of 1/4 below 2^22, so any
     order of fp32 sums is exact -- each element and each k lands where it should."""
-    for M, N, K in ((3, 50, 700), (40, 40, 1000), (130, 260, 2000), (300, 300, 4096), (520, 1100, 300)):
+    for M, N, K in ((3, 50, 700), (40, 40, 1000), (130, 260, 2000), (300, 300, 4096), (520, 1100, 300), (4100, 4100, 2050)):
         a, b = random_payload(M, K, 1, 127, 128), random_payload(N, K, 2, 127, 128)
         want = torch.from_numpy(R.mx_values(*(t.cpu().numpy() for t in a)) @ R.mx_values(*(t.cpu().numpy() for t in b)).T)
         assert torch.equal(qcp.mxfp4_matmul(*a, *b, dtype=torch.float32).cpu().double(), want), (M, N, K)
