@@ -219,7 +219,9 @@ int fp8_accum_requant(uint8_t *state_codes, float *state_scales, const void *gra
  *             their distance plus u/2^16 reaches 1, where u is 16 bits of a hash of
  *             (place, step, seed): the low half for m, the high half for sqrt(v).
  *             A positive sqrt(v) never becomes 0.  All zeros is the state before
- *             the first step.  Places that pad a tensor's last block stay 0.
+ *             the first step.  Places that pad a tensor's last block stay 0.  A block
+ *             in which m or v is infinite or NaN (from such a gradient, or from one
+ *             whose square overflows) has a NaN scale, from then on.
  *   step >= 1; lr, weight_decay >= 0; 0 <= beta1, beta2 < 1; eps > 0
  *   grad_scale   null (1), or a device pointer to one fp32 factor: the clipping
  *             or unscaling factor, read when the kernel runs

@@ -6,8 +6,9 @@ Compiles each csrc/*.hip translation unit with hipcc for gfx950 in parallel and
 links them into quantized_collective_payloads_amd/libqcp.so.  Flags that matter
 for bit-exact results: -ffp-contract=off (no implicit FMA), correctly rounded
 fp32 division, fp32 denormals kept, and packed-fp32 VALU instructions disabled.
-Inputs are finite by contract, so the library is built without NaN semantics
-(-fno-honor-nans, IEEE mode off): max/max3 then take |x| operands directly.
+The payloads' inputs are finite by contract, so the library is built without NaN
+semantics (-fno-honor-nans, IEEE mode off): max/max3 then take |x| operands directly.
+The files in HONOR_NANS promise something about NaN and keep its semantics.
 """
 import concurrent.futures as cf
 import os
@@ -26,10 +27,13 @@ ARCH = "gfx950"
 SOURCES = ["qcp_api.hip", "qcp_codec.hip", "qcp_reduce.hip", "qcp_ops_api.hip", "qcp_adamw.hip",
            "qcp_mxfp4.hip", "qcp_mxfp4_matmul.hip"]
 
+NO_NANS = ["-fno-honor-nans", "-mno-amdgpu-ieee"]
+HONOR_NANS = {"qcp_ops_api.hip", "qcp_adamw.hip"}     # NaN scalars are refused; NaN moments
+
 CXXFLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
     "-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt",
-    "-fno-honor-nans", "-mno-amdgpu-ieee",
+    *NO_NANS,
     "-fno-gpu-flush-denormals-to-zero",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function",
@@ -39,7 +43,8 @@ CXXFLAGS = [
 
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-    cmd = [HIPCC, *CXXFLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+    flags = [f for f in CXXFLAGS if not (f in NO_NANS and src in HONOR_NANS)]
+    cmd = [HIPCC, *flags, "-c", os.path.join(CSRC, src), "-o", obj]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)

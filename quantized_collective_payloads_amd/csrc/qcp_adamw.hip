@@ -94,6 +94,12 @@ __device__ __forceinline__ uint32_t pow2_scale(uint32_t absmax_bits) {
     return (uint32_t)(e < 1 ? 1 : e);
 }
 
+// the scale that is stored: 0 for a block of zeros; NaN where a value is NaN or
+// infinite (E4M3 codes could lose it, and the block with it: NaN stays for good)
+__device__ __forceinline__ float block_scale(uint32_t absmax_bits, uint32_t e) {
+    return absmax_bits >= 0x7f800000u ? __builtin_nanf("") : absmax_bits ? __uint_as_float(e << 23) : 0.0f;
+}
+
 template <int G> struct ogeom {
     static constexpr int GL = G >= 256 ? 64 : G / 4;        // lanes per block
     static constexpr int VB = G > 256 ? G / 256 : 1;        // vectors per block
@@ -238,8 +244,8 @@ __device__ __forceinline__ void adamw_wave(const AdamwTensor &t, const AdamwCons
             }
             const int64_t i = t.offset + at[u0];
             if ((lane & (Gm::GL - 1)) == 0 && (FULL || left[u0] > 0)) {
-                c.m_scales[i / G] = ma ? __uint_as_float(me << 23) : 0.0f;
-                c.v_scales[i / G] = va ? __uint_as_float(ve << 23) : 0.0f;
+                c.m_scales[i / G] = block_scale(ma, me);
+                c.v_scales[i / G] = block_scale(va, ve);
             }
         }
     }

@@ -331,6 +331,60 @@ def test_moments_past_32_bits(gpu):
         assert ((np.abs(got) >= a) & (np.abs(got) <= b)).all()
 
 
+# bit patterns of NaN (quiet, all ones, negative) and of the infinities
+BAD = {"f32": (0x7fc00000, 0x7fffffff, 0xffffffff, 0x7f800000, 0xff800000), "f16": (0x7e00, 0x7fff, 0xffff, 0x7c00, 0xfc00),
+       "bf16": (0x7fc0, 0x7fff, 0xffff, 0x7f80, 0xff80)}
+
+
+@GPU
+@pytest.mark.parametrize("G", [0, 32, 128, 1024])
+@pytest.mark.parametrize("gt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n,where", [(5000, 2500), (777, 776)])
+def test_a_gradient_that_is_not_finite_stays_visible(gpu, gt, G, n, where):
+    """It makes its parameter NaN and, with 8-bit moments, the scales of its block,
+    for good; every other block goes on as without it.  G = 0: fp32 moments."""
+    one = G or 32
+    block = slice(where // one * one, min((where // one + 1) * one, n)) if G else slice(where, where + 1)
+    for pattern in BAD[gt]:
+        seen = []
+        for bad in (False, True):
+            params, _ = flat_views([n], torch.float32, 1, 3, 0.02)
+            opt = qcp.AdamW(params, state="e4m3" if G else "f32", G=one)
+            for step in (1, 2, 3):
+                g = flat_views([n], DT[gt], 1, 20 + step, 1e-2)[0][0]
+                if bad and step == 2:
+                    bits = g.view(torch.int32 if gt == "f32" else torch.int16)
+                    bits[where] = pattern - (1 << (32 if gt == "f32" else 16)) if pattern >> (31 if gt == "f32" else 15) else pattern
+                qcp.adamw_step(opt, [g], step, seed=7, **HYPER)
+            seen.append((params[0].cpu(), opt.m.cpu(), opt.v.cpu(), *(s.cpu() for s in (opt.m_scales, opt.v_scales) if G)))
+        (p0, *s0), (p1, *s1) = seen
+        rest = torch.ones(n, dtype=torch.bool)
+        rest[block] = False
+        assert p1[block].isnan().all() and torch.equal(p1[rest], p0[rest]), (pattern, where)
+        if G:
+            mine = torch.zeros(len(s1[2]), dtype=torch.bool)
+            mine[where // G] = True
+            for a, b in zip(s0[2:], s1[2:]):
+                assert b[mine].isnan().all() and torch.equal(a[~mine], b[~mine]), pattern
+        for a, b in zip(s0[:2], s1[:2]):
+            assert torch.equal(a[:n][rest], b[:n][rest]) and not b[n:].any(), pattern
+
+
+@GPU
+def test_a_variance_that_overflows_stays_visible(gpu):
+    """A finite gradient whose square is beyond fp32: m stays finite, v does not."""
+    n, G, where = 512, 64, 200
+    params, _ = flat_views([n], torch.float32, 0, 3, 0.02)
+    opt = qcp.AdamW(params, G=G)
+    g = torch.full((n,), 1e-2, device="cuda")
+    g[where] = 1e22
+    qcp.adamw_step(opt, [g], 1, **HYPER)
+    assert opt.v_scales.isnan().nonzero().flatten().tolist() == [where // G] and opt.m_scales.isfinite().all()
+    assert params[0].isfinite().all()
+    qcp.adamw_step(opt, [torch.full_like(g, 1e-2)], 2, **HYPER)
+    assert params[0].isnan().nonzero().flatten().tolist() == list(range(192, 256))
+
+
 # ------------------------------------------------------------------ refusals (CPU)
 
 OK, EINVAL, EALIGN = 0, -1, -2
