@@ -222,7 +222,7 @@ int fp8_accum_requant(uint8_t *state_codes, float *state_scales, const void *gra
  *             the first step.  Places that pad a tensor's last block stay 0.  A block
  *             in which m or v is infinite or NaN (from such a gradient, or from one
  *             whose square overflows) has a NaN scale, from then on.
- *   step >= 1; lr, weight_decay >= 0; 0 <= beta1, beta2 < 1; eps > 0
+ *   step >= 1; lr, weight_decay >= 0; 0 <= beta1, beta2 < 1; eps >= 2^-126
  *   grad_scale   null (1), or a device pointer to one fp32 factor: the clipping
  *             or unscaling factor, read when the kernel runs
  *   seed      of the hash; unused with QCP_F32

@@ -83,8 +83,10 @@ int adamw_step(float *const *params, const void *const *grads, void *const *copi
     if (n_tensors < 0 || n_tensors > QCP_ADAMW_MAX_TENSORS || n_state < 0 || !valid_g(G)) return QCP_EINVAL;
     if (!valid_dtype(gt) || (state != QCP_F32 && state != QCP_E4M3)) return QCP_EINVAL;
     if (copies && ct != QCP_F16 && ct != QCP_BF16) return QCP_EINVAL;
+    // the denominator is at least eps, and the device's reciprocal takes what is below
+    // the least normal number for 0
     const bool scalars = step >= 1 && isfinite(lr) && lr >= 0 && beta1 >= 0 && beta1 < 1 && beta2 >= 0 &&
-                         beta2 < 1 && isfinite(eps) && (float)eps > 0 && isfinite(weight_decay) &&
+                         beta2 < 1 && isfinite(eps) && (float)eps >= 0x1p-126f && isfinite(weight_decay) &&
                          weight_decay >= 0;
     if (!scalars) return QCP_EINVAL;
     if (n_tensors == 0) return QCP_OK;

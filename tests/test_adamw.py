@@ -385,6 +385,18 @@ def test_a_variance_that_overflows_stays_visible(gpu):
     assert params[0].isnan().nonzero().flatten().tolist() == list(range(192, 256))
 
 
+@GPU
+@pytest.mark.parametrize("state", ["e4m3", "f32"])
+def test_the_smallest_eps(gpu, state):
+    """eps = 2^-126, the least normal one, on zero gradients: nothing moves, nothing is NaN."""
+    params, _ = flat_views([1000], torch.float32, 0, 3, 0.02)
+    before = params[0].clone()
+    opt = qcp.AdamW(params, state=state)
+    for step in (1, 2):
+        qcp.adamw_step(opt, [torch.zeros(1000, device="cuda")], step, lr=1e-3, eps=2.0 ** -126, weight_decay=0.0)
+    assert torch.equal(params[0], before) and not opt.m.any() and not opt.v.any()
+
+
 # ------------------------------------------------------------------ refusals (CPU)
 
 OK, EINVAL, EALIGN = 0, -1, -2
@@ -482,3 +494,11 @@ def test_step_refuses(gpu):
         qcp.adamw_step(opt, [z(300), z(5)], 0, 1e-3)
     p.data = z(300)
     raises("another storage", [z(300), z(5)])
+
+
+def test_c_entry_refuses_an_eps_below_normal(lib):
+    """1/(0 + eps) has to be finite in fp32, and the device's reciprocal takes what is
+    below 2^-126 for 0."""
+    for eps in (1e-45, 1e-40, 2.0 ** -127, np.nextafter(2.0 ** -126, 0)):
+        want = EINVAL if np.float32(eps) < np.float32(2.0 ** -126) else OK
+        assert call(eps=float(eps), sizes=[0]) == want, eps
