@@ -215,25 +215,30 @@ def _product(index, a, b, M, N, K, dtype, like):
     return c
 
 
+def _linear(x, w, need_x: bool, need_w: bool):
+    """(y, the payloads that the gradients asked for need): y = Q(x) Q(w)^T.  Reads x
+    and w once for both payloads of each."""
+    index, (T, I), O = x.get_device(), x.shape, w.shape[0]
+    work, kept = _Work(x, (T, I), (O, I)), None
+    if need_x or need_w:
+        kept = _Work(x, *([(I, O)] if need_x else []), *([(I, T)] if need_w else []))
+    _quantize_to(index, x, T, I, work[0], kept[-1] if need_w else None)
+    _quantize_to(index, w, O, I, work[1], kept[0] if need_x else None)
+    return _product(index, work[0], work[1], T, O, I, x.dtype, x), kept
+
+
 class _Linear(torch.autograd.Function):
     """y = Q(x) Q(w)^T, with Q along the dimension that is summed over; the
     backward products round dy, w and x along theirs, so gradients are those of
-    the products with the rounding passed straight through.  The forward reads x
-    and w once for both payloads of each, and keeps only the 4-bit ones that the
-    backward needs."""
+    the products with the rounding passed straight through.  The forward keeps
+    only the 4-bit payloads that the backward needs."""
 
     @staticmethod
     def forward(ctx, x, w):
-        index, (T, I), O = x.get_device(), x.shape, w.shape[0]
-        need_x, need_w = ctx.needs_input_grad
-        work = _Work(x, (T, I), (O, I))
-        kept = _Work(x, *([(I, O)] if need_x else []), *([(I, T)] if need_w else [])) if need_x or need_w else None
-        _quantize_to(index, x, T, I, work[0], kept[-1] if need_w else None)
-        _quantize_to(index, w, O, I, work[1], kept[0] if need_x else None)
-        y = _product(index, work[0], work[1], T, O, I, x.dtype, x)
+        y, kept = _linear(x, w, *ctx.needs_input_grad)
         if kept is not None:
             ctx.save_for_backward(kept.buffer)
-            ctx.kinds, ctx.sizes, ctx.places = (x.dtype, w.dtype), (T, I, O), kept.places
+            ctx.kinds, ctx.sizes, ctx.places = (x.dtype, w.dtype), (*x.shape, w.shape[0]), kept.places
         return y
 
     @staticmethod
@@ -265,5 +270,7 @@ def mxfp4_linear(x: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
     x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
     _matrix(x2, "x")
     _same_gpu(x.get_device(), x, weight)
-    y = _Linear.apply(x2.contiguous(), weight.contiguous())
+    x2, w = x2.contiguous(), weight.contiguous()
+    # without gradients only the product's own payloads: 77 tokens, 520 -> 1032: 26.1 -> 19.7 us
+    y = _Linear.apply(x2, w) if torch.is_grad_enabled() else _linear(x2, w, False, False)[0]
     return y if x.dim() == 2 else y.view(*x.shape[:-1], weight.shape[0])

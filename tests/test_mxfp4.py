@@ -379,6 +379,24 @@ def test_linear_shapes_and_partial_gradients(gpu):
     assert e.grad[0].abs().sum() > 0 and not e.grad[1:].any()
 
 
+@GPU
+def test_linear_without_gradients_does_only_the_product(gpu, monkeypatch):
+    from quantized_collective_payloads_amd import mxfp4
+    calls = []
+    enqueue = mxfp4._enqueue
+    monkeypatch.setattr(mxfp4, "_enqueue", lambda name, *a: (calls.append(name), enqueue(name, *a))[1])
+    x = torch.randn(6, 40, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn(50, 40, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    y = qcp.mxfp4_linear(x, w)
+    assert calls == ["mxfp4_quantize_both", "mxfp4_quantize", "mxfp4_matmul"] and y.requires_grad
+    for mode in (torch.no_grad, torch.inference_mode):
+        calls.clear()
+        with mode():
+            z = qcp.mxfp4_linear(x, w)
+        assert torch.equal(y, z) and not z.requires_grad
+        assert calls == ["mxfp4_quantize", "mxfp4_quantize", "mxfp4_matmul"]
+
+
 # ------------------------------------------------------------------ refusals (CPU)
 
 OK, EINVAL, EALIGN = 0, -1, -2
