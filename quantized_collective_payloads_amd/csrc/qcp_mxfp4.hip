@@ -14,7 +14,7 @@
 // of scales on 4, and the matrix instructions never see a short block.
 //
 // Bound: HBM; 2 + 0.53 bytes per 16-bit value for a few instructions.  Measured on
-// 14336 x 4096 bf16: quantize 24.6 us (6.0 TB/s), its transpose 34.4 (4.3), both 40,
+// 14336 x 4096 bf16: quantize 24.6 us (6.0 TB/s), its transpose 31 (4.8; 25 from cache), both 39 (34),
 // dequantize 22.9 (6.5); a copy of that matrix runs at 5.3 TB/s.
 //
 // Along the rows: a lane owns 8 consecutive values (one 16-byte load of 16-bit
@@ -30,9 +30,9 @@
 // neighbouring columns of 32 rows, so its two blocks need no other lane: absmax,
 // scale and codes all come from its own registers.  One input row of the tile and
 // one output row are both 128 bytes; the codes pass through LDS to be stored so.
-// For both payloads at once the tile is 256 x 128 and also goes through LDS as it is
-// (fp32: is read again, from L2), to be taken by rows, a block of 32 values per thread:
-// memory sees the matrix once.
+// For both payloads at once the tile (of 16 bits: 256 x 128) also goes through LDS as
+// it is, to be taken by rows, a block of 32 values per thread: memory sees the matrix
+// once.  Read again from L2 instead, fp32 took 358 us at 28672 x 8192 against 239.
 #include "qcp_device.h"
 #include "qcp_ops.h"
 
@@ -51,29 +51,17 @@ constexpr int kMxVecs = 4;        // vectors of 8 values per lane
 
 template <int XT> constexpr int words8() { return XT == F32 ? 8 : 4; }   // dwords of 8 values
 
-// 8 values from p, of which `count` exist (the others are zero).  STREAM: read once
-template <int XT, bool STREAM = true>
-__device__ __forceinline__ void load8(const void *x, int64_t i, int count, uint32_t (&w)[words8<XT>()]) {
-    constexpr int B = dtype_traits<XT>::bytes;
-    const uint8_t *p = (const uint8_t *)x + i * B;
+// 8 values of 16 bits from p, of which `count` exist (the others are zero)
+__device__ __forceinline__ void load8(const uint16_t *x, int64_t i, int count, uint32_t *w) {
+    const uint16_t *p = x + i;
     if (count >= 8) {
-#pragma unroll
-        for (int k = 0; k < words8<XT>() / 4; k++) {
-            u32x4_any v;
-            if constexpr (STREAM) v = __builtin_nontemporal_load((const u32x4_any *)p + k);
-            else v = *((const u32x4_any *)p + k);
-            w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
-        }
+        const u32x4_any v = __builtin_nontemporal_load((const u32x4_any *)p);
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
     } else {
 #pragma unroll
-        for (int k = 0; k < words8<XT>(); k++) {
-            if constexpr (XT == F32) {
-                w[k] = k < count ? *(const uint32_t *)(p + 4 * k) : 0;
-            } else {
-                const uint32_t lo = 2 * k < count ? *(const uint16_t *)(p + 4 * k) : 0;
-                const uint32_t hi = 2 * k + 1 < count ? *(const uint16_t *)(p + 4 * k + 2) : 0;
-                w[k] = lo | (hi << 16);
-            }
+        for (int k = 0; k < 4; k++) {
+            const uint32_t lo = 2 * k < count ? p[2 * k] : 0, hi = 2 * k + 1 < count ? p[2 * k + 1] : 0;
+            w[k] = lo | (hi << 16);
         }
     }
 }
@@ -198,7 +186,7 @@ __global__ __launch_bounds__(kThreads) void k_mx_quantize(const void *__restrict
             count = values_left(inside, cols, p.col, UNIT);
         }
         if constexpr (XT == F32) load4((const float *)x, at, count, to);
-        else load8<XT>(x, at, count, *(uint32_t(*)[words8<XT>()])to);
+        else load8((const uint16_t *)x, at, count, to);
     };
 #pragma unroll
     for (int u = 0; u < kMxVecs; u++) {
@@ -348,8 +336,13 @@ __global__ __launch_bounds__(kThreads) void k_mx_dequantize(const uint32_t *__re
     }
 }
 
+// A matrix above the 256 MB of the last cache is read and its column-wise codes are
+// written past it: 28672 x 8192 fp16 122 -> 114 us, both payloads 160 -> 134; fp32 215 ->
+// 200 and 239 -> 225.  A smaller one may lie there already: 8192 x 4096 bf16, just
+// written, 15.9 us and 21.6 against 17.5 and 24.4; 16384 x 5120 37 and 46 against 45 and 56.
+constexpr int64_t kStreamBytes = (int64_t)256 << 20;
 constexpr int kTRows = 256;                    // tile of the column-wise quantize
-template <bool BOTH> constexpr int tile_cols() { return BOTH ? 128 : 64; }
+template <int XT, bool BOTH> constexpr int tile_cols() { return XT != F32 && BOTH ? 128 : 64; }
 
 // the codes and the scale byte of one block of a row
 template <int XT>
@@ -365,20 +358,26 @@ __device__ __forceinline__ uint4 row_block(const uint32_t (&w)[4][words8<XT>()],
     return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
-template <int XT, bool BOTH>
-__global__ __launch_bounds__(4 * tile_cols<BOTH>()) void k_mx_quantize_t(const void *__restrict__ x, int64_t rows,
+// STREAM: the matrix and the codes pass the caches by
+template <bool STREAM, typename T>
+__device__ __forceinline__ T load_words(const T *p) {
+    if constexpr (STREAM) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+
+template <int XT, bool BOTH, bool STREAM>
+__global__ __launch_bounds__((4 * tile_cols<XT, BOTH>())) void k_mx_quantize_t(const void *__restrict__ x, int64_t rows,
                                                             int64_t cols, int64_t ld, uint32_t col_tiles, uint32_t groups,
                                                             int64_t pad_rows, uint8_t *__restrict__ codes,
                                                             uint8_t *__restrict__ scales, int64_t pad_cols,
                                                             uint8_t *__restrict__ row_codes,
                                                             uint8_t *__restrict__ row_scales) {
-    constexpr int B = dtype_traits<XT>::bytes, kTCols = tile_cols<BOTH>();
+    constexpr int B = dtype_traits<XT>::bytes, kTCols = tile_cols<XT, BOTH>();
     constexpr int kLine = 128 + 16;            // bytes per column in LDS: a shift of 4 banks
-    // 16-bit input of both payloads: the tile itself lies here first, rows 16 bytes
-    // more than their 256 apart, which spreads the row pass over all banks
-    constexpr bool kStage = BOTH && XT != F32;
-    constexpr int kRow = kTCols * B + 16, kNeed = kTCols * (kLine + 8);
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kStage ? kTRows * kRow : kNeed];
+    // for both payloads the tile itself lies here first, rows 16 bytes more than their
+    // 256 apart, which spreads the row pass over all banks
+    constexpr int kRow = 256 + 16, kNeed = kTCols * (kLine + 8);
+    __shared__ __attribute__((aligned(16))) uint8_t lds[BOTH ? kTRows * kRow : kNeed];
     uint8_t *const lines = lds, *const marks = lds + kTCols * kLine;
     // Work-groups are dealt round-robin to the 8 XCDs.  16 neighbouring tiles, 2 KB of
     // a 16-bit row, go to one XCD, so that its reads spread over all its L2 channels;
@@ -401,7 +400,7 @@ __global__ __launch_bounds__(4 * tile_cols<BOTH>()) void k_mx_quantize_t(const v
         if constexpr (XT == F32) {
             a[r] = b[r] = 0;
             if (r < have && two == 2) {
-                const u32x2_any v = *(const u32x2_any *)q;
+                const u32x2_any v = load_words<STREAM>((const u32x2_any *)q);
                 a[r] = v.x;
                 b[r] = v.y;
             } else if (r < have && two == 1) {
@@ -409,42 +408,46 @@ __global__ __launch_bounds__(4 * tile_cols<BOTH>()) void k_mx_quantize_t(const v
             }
         } else {
             a[r] = 0;
-            if (r < have && two == 2) a[r] = *(const u32_any *)q;
+            if (r < have && two == 2) a[r] = load_words<STREAM>((const u32_any *)q);
             else if (r < have && two == 1) a[r] = *(const uint16_t *)q;
         }
     }
-    // the tile along its rows: a thread takes a block of 32 at a time, 4 threads the 128
-    // columns of a row, whose scales are one dword
+    // the tile along its rows: a thread takes a block of 32 at a time; the scales of a
+    // row, 4 bytes (fp32: 2), go out at once
     if constexpr (BOTH) {
-        if constexpr (kStage) {
+        constexpr int per = kTCols / 32;       // blocks of a row
 #pragma unroll
-            for (int r = 0; r < 32; r++) *(uint32_t *)(lds + (block * 32 + r) * kRow + pair * 4) = a[r];
-            __syncthreads();
+        for (int r = 0; r < 32; r++) {
+            uint8_t *at = lds + (block * 32 + r) * kRow + pair * 2 * B;
+            if constexpr (XT == F32) *(u32x2_t *)at = u32x2_t{a[r], b[r]};
+            else *(uint32_t *)at = a[r];
         }
+        __syncthreads();
 #pragma unroll
         for (int k = 0; k < 2; k++) {
-            const int unit = tid + 4 * kTCols * k;
-            const int64_t r = tr + (unit >> 2), c = tc + 32 * (unit & 3);
+            const int unit = tid + 4 * kTCols * k, line = unit / per, place = unit % per;
+            const int64_t r = tr + line;
             uint32_t w[4][words8<XT>()], e;
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-                if constexpr (kStage) {
-                    const uint4 v = *(const uint4 *)(lds + (unit >> 2) * kRow + (unit & 3) * 64 + 16 * q);
-                    w[q][0] = v.x; w[q][1] = v.y; w[q][2] = v.z; w[q][3] = v.w;
-                } else {                       // from L2, where the tile has just been
-                    const int64_t left = r < rows ? cols - c - 8 * q : 0;
-                    load8<XT, false>(x, r * ld + c + 8 * q, left > 8 ? 8 : left < 0 ? 0 : (int)left, w[q]);
+            for (int q = 0; q < 4; q++)
+#pragma unroll
+                for (int j = 0; j < words8<XT>(); j += 4) {
+                    const uint4 v = *(const uint4 *)(lds + line * kRow + place * 32 * B + 8 * B * q + 4 * j);
+                    w[q][j] = v.x; w[q][j + 1] = v.y; w[q][j + 2] = v.z; w[q][j + 3] = v.w;
                 }
-            }
             const uint4 v = row_block<XT>(w, e);
-            uint32_t d = e << (8 * (unit & 3));
+            uint32_t d = e << (8 * place);
             d |= dpp_u32<0xB1>(d);
-            d |= dpp_u32<0x4E>(d);
+            if constexpr (per == 4) d |= dpp_u32<0x4E>(d);
             if (r >= rows) continue;
-            *(uint4 *)(row_codes + r * (pad_cols / 2) + c / 2) = v;
-            if ((unit & 3) == 0) *(uint32_t *)(row_scales + r * (pad_cols / 32) + tc / 32) = d;
+            *(uint4 *)(row_codes + r * (pad_cols / 2) + tc / 2 + 16 * place) = v;
+            uint8_t *at = row_scales + r * (pad_cols / 32) + tc / 32;
+            if (place == 0) {
+                if constexpr (per == 4) *(uint32_t *)at = d;
+                else *(uint16_t *)at = (uint16_t)d;
+            }
         }
-        if constexpr (kStage) __syncthreads();
+        __syncthreads();
     }
     uint32_t ma = 0, mb = 0;
 #pragma unroll
@@ -485,9 +488,12 @@ __global__ __launch_bounds__(4 * tile_cols<BOTH>()) void k_mx_quantize_t(const v
     for (int k = 0; k < 2; k++) {
         const int line = (tid >> 3) + kTCols / 2 * k, piece = tid & 7;
         const int64_t c = tc + line;
-        if (c < cols && 32 * piece < wide)
-            *(uint4 *)(codes + c * (pad_rows / 2) + tr / 2 + 16 * piece) =
-                *(const uint4 *)(lines + line * kLine + 16 * piece);
+        if (c < cols && 32 * piece < wide) {
+            u32x4_t *to = (u32x4_t *)(codes + c * (pad_rows / 2) + tr / 2 + 16 * piece);
+            const u32x4_t v = *(const u32x4_t *)(lines + line * kLine + 16 * piece);
+            if constexpr (STREAM) __builtin_nontemporal_store(v, to);
+            else *to = v;
+        }
     }
     if (tid < 2 * kTCols) {
         const int line = tid >> 1, half = tid & 1;
@@ -498,17 +504,29 @@ __global__ __launch_bounds__(4 * tile_cols<BOTH>()) void k_mx_quantize_t(const v
     }
 }
 
+// along the columns, and with BOTH also along the rows
+template <int XT, bool BOTH>
+hipError_t run_quantize_t(const void *x, int64_t rows, int64_t cols, int64_t ld, uint8_t *codes,
+                          uint8_t *scales, uint8_t *row_codes, uint8_t *row_scales, hipStream_t st) {
+    constexpr int TC = tile_cols<XT, BOTH>();
+    const int64_t pr = (rows + kMxPad - 1) / kMxPad * kMxPad, pc = (cols + kMxPad - 1) / kMxPad * kMxPad;
+    const int64_t ct = ((BOTH ? pc : cols) + TC - 1) / TC, rt = (rows + kTRows - 1) / kTRows;
+    const bool stream = rows * cols * dtype_traits<XT>::bytes > kStreamBytes;
+    const dim3 grid((unsigned)(ct * rt)), threads(4 * TC);
+    if (stream)
+        hipLaunchKernelGGL((k_mx_quantize_t<XT, BOTH, true>), grid, threads, 0, st, x, rows, cols, ld, (uint32_t)ct,
+                           (uint32_t)(ct * rt), pr, codes, scales, pc, row_codes, row_scales);
+    else
+        hipLaunchKernelGGL((k_mx_quantize_t<XT, BOTH, false>), grid, threads, 0, st, x, rows, cols, ld, (uint32_t)ct,
+                           (uint32_t)(ct * rt), pr, codes, scales, pc, row_codes, row_scales);
+    return hipGetLastError();
+}
+
 template <int XT>
 hipError_t run_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, int transpose,
                         uint8_t *codes, uint8_t *scales, hipStream_t st) {
-    if (transpose) {
-        const int64_t pad = (rows + kMxPad - 1) / kMxPad * kMxPad;
-        const int64_t ct = (cols + tile_cols<false>() - 1) / tile_cols<false>(), rt = (rows + kTRows - 1) / kTRows;
-        hipLaunchKernelGGL((k_mx_quantize_t<XT, false>), dim3((unsigned)(ct * rt)), dim3(kThreads), 0, st, x,
-                           rows, cols, ld, (uint32_t)ct, (uint32_t)(ct * rt), pad, codes, scales, (int64_t)0,
-                           (uint8_t *)nullptr, (uint8_t *)nullptr);
-        return hipGetLastError();
-    }
+    if (transpose)
+        return run_quantize_t<XT, false>(x, rows, cols, ld, codes, scales, nullptr, nullptr, st);
     const int64_t pad = (cols + kMxPad - 1) / kMxPad * kMxPad;
     const bool flat = cols == pad && (ld == cols || rows == 1);
     const int64_t vecs = rows * pad / 8;
@@ -519,16 +537,6 @@ hipError_t run_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, i
     else
         hipLaunchKernelGGL((k_mx_quantize<XT, false>), dim3(grid), dim3(kThreads), 0, st, x, vecs,
                            (uint32_t)(pad / 8), cols, ld, (uint32_t *)codes, scales);
-    return hipGetLastError();
-}
-
-template <int XT>
-hipError_t run_quantize_both(const void *x, int64_t rows, int64_t cols, int64_t ld, uint8_t *codes,
-                             uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t, hipStream_t st) {
-    const int64_t pr = (rows + kMxPad - 1) / kMxPad * kMxPad, pc = (cols + kMxPad - 1) / kMxPad * kMxPad;
-    const int64_t ct = pc / tile_cols<true>(), rt = (rows + kTRows - 1) / kTRows;
-    hipLaunchKernelGGL((k_mx_quantize_t<XT, true>), dim3((unsigned)(ct * rt)), dim3(4 * tile_cols<true>()), 0, st, x, rows,
-                       cols, ld, (uint32_t)ct, (uint32_t)(ct * rt), pr, codes_t, scales_t, pc, codes, scales);
     return hipGetLastError();
 }
 
@@ -564,9 +572,9 @@ hipError_t launch_mx_quantize_both(const void *x, int xt, int64_t rows, int64_t 
                                    uint8_t *codes, uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t,
                                    hipStream_t st) {
     switch (xt) {
-    case F16: return run_quantize_both<F16>(x, rows, cols, ld, codes, scales, codes_t, scales_t, st);
-    case BF16: return run_quantize_both<BF16>(x, rows, cols, ld, codes, scales, codes_t, scales_t, st);
-    case F32: return run_quantize_both<F32>(x, rows, cols, ld, codes, scales, codes_t, scales_t, st);
+    case F16: return run_quantize_t<F16, true>(x, rows, cols, ld, codes_t, scales_t, codes, scales, st);
+    case BF16: return run_quantize_t<BF16, true>(x, rows, cols, ld, codes_t, scales_t, codes, scales, st);
+    case F32: return run_quantize_t<F32, true>(x, rows, cols, ld, codes_t, scales_t, codes, scales, st);
     default: return hipErrorInvalidValue;
     }
 }

@@ -88,6 +88,21 @@ def test_both_payloads_in_one_pass(gpu, rows, cols, dt):
 
 
 @GPU
+@pytest.mark.parametrize("rows,cols,dt", [(16390, 8211, "bf16"), (16391, 8210, "f16"), (8201, 8291, "f32")])
+def test_matrices_beyond_the_last_cache(gpu, rows, cols, dt):
+    """Above 256 MB the column-wise pass streams: the same bytes as of the parts."""
+    x = values(rows, cols, dt, 7)
+    assert x.numel() * x.element_size() > 256 << 20
+    straight, across = qcp.mxfp4_quantize_both(x)
+    for a, b in zip(straight, qcp.mxfp4_quantize(x)):
+        assert torch.equal(a, b)
+    alone = qcp.mxfp4_quantize(x, transpose=True)
+    for c in range(0, cols, 2100):
+        for a, b, part in zip(across, alone, qcp.mxfp4_quantize(x[:, c:c + 2100], transpose=True)):
+            assert torch.equal(a[c:c + 2100], part) and torch.equal(b[c:c + 2100], part)
+
+
+@GPU
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 def test_every_16_bit_value(gpu, dt):
     """All 65,536 patterns, each the largest of its block and each beside a larger
