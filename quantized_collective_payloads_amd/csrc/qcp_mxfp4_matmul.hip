@@ -54,10 +54,147 @@ __device__ __forceinline__ void store4(void *c, int64_t at, int count, const flo
     }
 }
 
-// The plain form, for the K that the kernels below do not take: a wave computes
-// 64 x 64 of C from 2 + 2 fragments per granule, read straight from memory; a
-// work-group's 4 waves make 128 x 128.  Rows past the end repeat
-// the last one and are not stored.
+// Which tile of C work-group t takes.  Work-groups are dealt round-robin to the 8 XCDs:
+// each gets a contiguous run of tiles and walks it 4 tiles of M by N, so that the tiles
+// an XCD works on at a time share few operand panels in its L2.
+struct TilePlace {
+    uint32_t m, n;
+};
+__device__ __forceinline__ TilePlace tile_place(uint32_t t, uint32_t m_tiles, uint32_t n_tiles) {
+    const uint32_t tiles = m_tiles * n_tiles, per = tiles / 8, extra = tiles % 8, xcd = t % 8;
+    t = xcd * per + min(xcd, extra) + t / 8;
+    const uint32_t band = 4 * n_tiles, first = t / band * 4, height = min(4u, m_tiles - first);
+    const uint32_t in = t - t / band * band;
+    return TilePlace{first + in % height, in / height};
+}
+
+// A fragment of C: lane r of a half-wave has row m, and of columns n + 8q + 4 * half + 0..3
+// register group q.  16-bit results go out 16 bytes a lane: the half-waves swap groups, so
+// that the lower one has columns n + 16k + 0..7 and the upper one 8..15.
+template <int CT>
+__device__ __forceinline__ void store_fragment(const f32x16_t &v, void *c, int64_t ldc, int64_t m, int64_t n,
+                                               int half, int64_t M, int64_t N, bool whole) {
+    if constexpr (CT == F32) {
+        if (!whole && m >= M) return;
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const int64_t at = n + 8 * q + 4 * half;
+            const float r[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+            store4<CT>(c, m * ldc + at, whole || N - at >= 4 ? 4 : (int)(N - at), r);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            uint32_t w[4];
+#pragma unroll
+            for (int d = 0; d < 2; d++) {
+                const uint32_t lo = narrow2<CT>(v[8 * k + 2 * d], v[8 * k + 2 * d + 1]);
+                const uint32_t hi = narrow2<CT>(v[8 * k + 4 + 2 * d], v[8 * k + 5 + 2 * d]);
+                const auto swapped = __builtin_amdgcn_permlane32_swap(lo, hi, false, false);
+                w[d] = swapped[0];
+                w[2 + d] = swapped[1];
+            }
+            const int64_t at = n + 16 * k + 8 * half;
+            uint16_t *p = (uint16_t *)c + m * ldc + at;
+            typedef u32x4_t u32x4_any __attribute__((aligned(2)));
+            if (whole || (m < M && N - at >= 8)) {
+                *(u32x4_any *)p = u32x4_t{w[0], w[1], w[2], w[3]};
+            } else if (m < M) {
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    if (at + e < N) p[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+            }
+        }
+    }
+}
+
+// A wave's 64 x 64 of C from fragments of 32 rows
+template <int CT>
+__device__ __forceinline__ void store_wave(const f32x16_t (&acc)[2][2], void *c, int64_t ldc, int64_t m0, int64_t n0,
+                                           int lane, int64_t M, int64_t N) {
+    const bool whole = m0 + 64 <= M && n0 + 64 <= N;
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+            store_fragment<CT>(acc[i][j], c, ldc, m0 + 32 * i + (lane & 31), n0 + 32 * j, lane >> 5, M, N, whole);
+}
+
+// K of G = 1 to 3 granules: 128 x 128 of C per work-group.  The payload rows of a tile are
+// one run of memory, 16 KB of A and B per granule, that goes to LDS at once; 4 waves,
+// 2 x 2, then compute 64 x 64 each from fragments there.  Rows past the end repeat the last
+// one and are not stored.
+// Bound: writing C.  14336 x 4096 to bf16, 23 us of writing: K = 128, 256, 384 27, 32 and
+// 36 us; with fragments straight from memory 31, 48 and 56 (both operands read twice, in
+// pieces of 16 bytes), and that a granule at a time with 8-byte stores 47, 63 and 70.
+//
+// LDS holds a row's pieces of 16 bytes in an order that gives the 16 rows that a fragment
+// read touches in a cycle all 64 banks: rows are 64 G bytes apart, so for odd G 4
+// consecutive rows lie side by side in the banks, and the low bits of the piece follow row / 4;
+// for G = 2 2 rows do, and the piece's 3 bits follow row / 2.
+template <int G, int CT>
+__global__ __launch_bounds__(kThreads) void k_mx_matmul_short(
+    const uint8_t *__restrict__ a, const uint8_t *__restrict__ as, const uint8_t *__restrict__ b,
+    const uint8_t *__restrict__ bs, int64_t M, int64_t N, uint32_t m_tiles, uint32_t n_tiles, void *__restrict__ c,
+    int64_t ldc) {
+    constexpr int kPieces = 4 * G, kSide = 128 * 64 * G;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kSide];
+    const TilePlace t = tile_place(__builtin_amdgcn_workgroup_id_x(), m_tiles, n_tiles);
+    const int64_t mt = (int64_t)t.m * 128, nt = (int64_t)t.n * 128;
+    const int tid = (int)__builtin_amdgcn_workitem_id_x(), wave = tid >> 6, lane = lane_id();
+    auto where = [](int row, int piece) __attribute__((always_inline)) {
+        const int x = G == 2 ? (row >> 1) & 7 : (row >> 2) & 3;
+        return row * 64 * G + (piece ^ x) * 16;
+    };
+    u32x4_t v[2][2 * G];
+#pragma unroll
+    for (int k = 0; k < 2 * G; k++) {
+        const int at = tid + kThreads * k, row = at / kPieces, piece = at % kPieces;
+        v[0][k] = *(const u32x4_t *)(a + min(mt + row, M - 1) * (64 * G) + piece * 16);
+        v[1][k] = *(const u32x4_t *)(b + min(nt + row, N - 1) * (64 * G) + piece * 16);
+    }
+    const int row = lane & 31, half = lane >> 5, ra = (wave & 1) * 64 + row, rb = (wave >> 1) * 64 + row;
+    uint32_t sa[2][G], sb[2][G];
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+            sa[i][g] = *(const uint32_t *)(as + min(mt + ra + 32 * i, M - 1) * (4 * G) + 4 * g) >> (16 * half);
+            sb[i][g] = *(const uint32_t *)(bs + min(nt + rb + 32 * i, N - 1) * (4 * G) + 4 * g) >> (16 * half);
+        }
+#pragma unroll
+    for (int k = 0; k < 2 * G; k++) {
+        const int at = tid + kThreads * k, to = where(at / kPieces, at % kPieces);
+        *(u32x4_t *)(lds + to) = v[0][k];
+        *(u32x4_t *)(lds + kSide + to) = v[1][k];
+    }
+    __syncthreads();
+    f32x16_t acc[2][2] = {};
+#pragma unroll
+    for (int g = 0; g < G; g++) {
+        u32x4_t fa[2][2], fb[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int u = 0; u < 2; u++) {
+                fa[i][u] = *(const u32x4_t *)(lds + where(ra + 32 * i, 4 * g + 2 * half + u));
+                fb[i][u] = *(const u32x4_t *)(lds + kSide + where(rb + 32 * i, 4 * g + 2 * half + u));
+            }
+        // B first: a lane then holds 4 consecutive n of one m per group of registers
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                acc[i][j] = mma<0>(fb[j][0], sb[j][g], fa[i][0], sa[i][g], acc[i][j]);
+                acc[i][j] = mma<1>(fb[j][1], sb[j][g], fa[i][1], sa[i][g], acc[i][j]);
+            }
+    }
+    store_wave<CT>(acc, c, ldc, mt + (wave & 1) * 64, nt + (wave >> 1) * 64, lane, M, N);
+}
+
+// The plain form, for K from 2^25 on, whose rows are beyond the 32-bit offsets within a
+// tile of the kernels below: a wave computes 64 x 64 of C from 2 + 2 fragments per granule,
+// read straight from memory; a work-group's 4 waves make 128 x 128.
 template <int CT>
 __global__ __launch_bounds__(kThreads) void k_mx_matmul(const uint8_t *__restrict__ a,
                                                         const uint8_t *__restrict__ as,
@@ -94,7 +231,6 @@ __global__ __launch_bounds__(kThreads) void k_mx_matmul(const uint8_t *__restric
             sa[i] = *(const uint32_t *)(qa[i] + g * 4) >> (16 * half);
             sb[i] = *(const uint32_t *)(qb[i] + g * 4) >> (16 * half);
         }
-        // B first: a lane then holds 4 consecutive n of one m per group of registers
 #pragma unroll
         for (int i = 0; i < 2; i++)
 #pragma unroll
@@ -103,19 +239,7 @@ __global__ __launch_bounds__(kThreads) void k_mx_matmul(const uint8_t *__restric
                 acc[i][j] = mma<1>(fb[j][1], sb[j], fa[i][1], sa[i], acc[i][j]);
             }
     }
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        const int64_t m = m0 + 32 * i + row;
-        if (m >= M) continue;
-#pragma unroll
-        for (int j = 0; j < 2; j++)
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const int64_t n = n0 + 32 * j + 8 * q + 4 * half;
-                const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-                store4<CT>(c, m * ldc + n, N - n < 4 ? (int)(N - n) : 4, v);
-            }
-    }
+    store_wave<CT>(acc, c, ldc, m0, n0, lane, M, N);
 }
 
 // ---------------------------------------------------------------------------
@@ -180,46 +304,6 @@ __device__ __forceinline__ void wait_lds_and_meet() {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// A fragment of C: lane r of a half-wave has row m, and of columns n + 8q + 4 * half + 0..3
-// register group q.  16-bit results go out 16 bytes a lane: the half-waves swap groups, so
-// that the lower one has columns n + 16k + 0..7 and the upper one 8..15.
-template <int CT>
-__device__ __forceinline__ void store_fragment(const f32x16_t &v, void *c, int64_t ldc, int64_t m, int64_t n,
-                                               int half, int64_t M, int64_t N, bool whole) {
-    if constexpr (CT == F32) {
-        if (!whole && m >= M) return;
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-            const int64_t at = n + 8 * q + 4 * half;
-            const float r[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-            store4<CT>(c, m * ldc + at, whole || N - at >= 4 ? 4 : (int)(N - at), r);
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-            uint32_t w[4];
-#pragma unroll
-            for (int d = 0; d < 2; d++) {
-                const uint32_t lo = narrow2<CT>(v[8 * k + 2 * d], v[8 * k + 2 * d + 1]);
-                const uint32_t hi = narrow2<CT>(v[8 * k + 4 + 2 * d], v[8 * k + 5 + 2 * d]);
-                const auto swapped = __builtin_amdgcn_permlane32_swap(lo, hi, false, false);
-                w[d] = swapped[0];
-                w[2 + d] = swapped[1];
-            }
-            const int64_t at = n + 16 * k + 8 * half;
-            uint16_t *p = (uint16_t *)c + m * ldc + at;
-            typedef u32x4_t u32x4_any __attribute__((aligned(2)));
-            if (whole || (m < M && N - at >= 8)) {
-                *(u32x4_any *)p = u32x4_t{w[0], w[1], w[2], w[3]};
-            } else if (m < M) {
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    if (at + e < N) p[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
-            }
-        }
-    }
-}
-
 __device__ __forceinline__ i32x4_t buffer_of(const void *p, uint64_t bytes) {
     const uint64_t at = (uint64_t)p;
     const uint32_t n = bytes > 0xfffffffcull ? 0xfffffffcu : (uint32_t)bytes;
@@ -282,15 +366,9 @@ __global__ __launch_bounds__(kThreads, (tgeom<FM, FN>::waves_per_simd)) void k_m
     i32x4_t ra, rb, rs[mark_rounds];
     uint32_t vs[mark_rounds], mark_at[mark_rounds], m_rows, n_rows;
     auto set_tile = [&](uint32_t t) __attribute__((always_inline)) {
-        // work-groups are dealt round-robin to the 8 XCDs: give each XCD a contiguous
-        // run of tiles, and walk it 4 tiles of M by N, so that the tiles an XCD works on
-        // at a time share few operand panels in its L2
-        const uint32_t per = tiles / 8, extra = tiles % 8, xcd = t % 8;
-        t = xcd * per + min(xcd, extra) + t / 8;
-        const uint32_t band = 4 * n_tiles, first = t / band * 4, height = min(4u, m_tiles - first);
-        const uint32_t in = t - t / band * band;
-        m0 = (int64_t)(first + in % height) * Gm::TM;
-        n0 = (int64_t)(in / height) * Gm::TN;
+        const TilePlace at = tile_place(t, m_tiles, n_tiles);
+        m0 = (int64_t)at.m * Gm::TM;
+        n0 = (int64_t)at.n * Gm::TN;
         m_rows = (uint32_t)min(M - m0, (int64_t)Gm::TM);
         n_rows = (uint32_t)min(N - n0, (int64_t)Gm::TN);
         ra = buffer_of(a + m0 * row_bytes, (uint64_t)m_rows * row_bytes);
@@ -654,11 +732,15 @@ hipError_t run_matmul(const uint8_t *a, const uint8_t *as, const uint8_t *b, con
             return run_tiled<2, 2, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
         return run_tiled<4, 4, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
     }
-    // K below 4 granules, or too long for 32-bit offsets within a tile
-    const int64_t mt = (M + 127) / 128, nt = (N + 127) / 128;
-    if (mt * nt > kMaxGroups) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_mx_matmul<CT>), dim3((unsigned)(mt * nt)), dim3(kThreads), 0, st, a, as, b, bs, M,
-                       N, granules, (uint32_t)mt, c, ldc);
+    if (middle > kMaxGroups) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)middle);
+    const uint32_t mt = (uint32_t)((M + 127) / 128), nt = (uint32_t)((N + 127) / 128);
+    switch (granules) {
+    case 1: hipLaunchKernelGGL((k_mx_matmul_short<1, CT>), grid, dim3(kThreads), 0, st, a, as, b, bs, M, N, mt, nt, c, ldc); break;
+    case 2: hipLaunchKernelGGL((k_mx_matmul_short<2, CT>), grid, dim3(kThreads), 0, st, a, as, b, bs, M, N, mt, nt, c, ldc); break;
+    case 3: hipLaunchKernelGGL((k_mx_matmul_short<3, CT>), grid, dim3(kThreads), 0, st, a, as, b, bs, M, N, mt, nt, c, ldc); break;
+    default: hipLaunchKernelGGL((k_mx_matmul<CT>), grid, dim3(kThreads), 0, st, a, as, b, bs, M, N, granules, mt, c, ldc);
+    }
     return hipGetLastError();
 }
 

@@ -250,6 +250,33 @@ def test_product_over_several_rounds_of_tiles(gpu, M, N, K, dt):
 
 
 @GPU
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", [(700, 900, 1), (1100, 1000, 128), (1025, 1290, 200), (129, 4097, 256), (2049, 700, 384), (1300, 1301, 300)])
+def test_product_over_a_short_k(gpu, M, N, K, dt):
+    a, b = random_payload(M, K, M, 110, 126), random_payload(N, K, N, 110, 126)
+    a[1][M // 2, 0] = 255
+    out = qcp.mxfp4_matmul(*a, *b, dtype=DT[dt])
+    assert out[M // 2].isnan().all()
+    keep = [i for i in range(M) if i != M // 2]
+    check_product((a[0][keep], a[1][keep]), b, out[keep], dt, (M, N, K))
+
+
+@GPU
+def test_product_over_a_very_long_k(gpu):
+    """K = 2^25, zeros but for the last 128: as the product of these."""
+    K, M, N = 1 << 25, 40, 33
+    parts, wide_ones = [], []
+    for lines, seed in ((M, 5), (N, 6)):
+        tail = random_payload(lines, 128, seed, 120, 125)
+        codes = torch.zeros(lines, K // 2, dtype=torch.uint8, device="cuda")
+        scales = torch.full((lines, K // 32), 127, dtype=torch.uint8, device="cuda")
+        codes[:, -64:], scales[:, -4:] = tail
+        parts.append(tail)
+        wide_ones += [codes, scales]
+    check_product(*parts, qcp.mxfp4_matmul(*wide_ones, dtype=torch.float32), "f32", K)
+
+
+@GPU
 def test_product_of_integers_is_exact(gpu):
     """Codes at scale 1: every partial sum is a multiple of 1/4 below 2^22, so any
     order of fp32 sums is exact -- each element and each k lands where it should."""
