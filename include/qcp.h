@@ -283,6 +283,21 @@ int mxfp4_matmul(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t 
                  const uint8_t *b_scales, int64_t M, int64_t N, int64_t K, void *c, int ct, int64_t ldc,
                  void *stream);
 
+/*
+ * The same with scratch memory of at least qcp_mxfp4_matmul_work(M, N, K) bytes,
+ * 16-byte aligned, on the device.  Where that is not 0 (few tiles of C and a long K)
+ * slices of K are multiplied side by side into fp32 sums there and added up, always in
+ * the same order, in a second launch; else `work` is not used and may be null.  The
+ * order of the sums, and with it their last bits, differs from mxfp4_matmul's.
+ */
+int mxfp4_matmul_sliced(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *b_codes,
+                        const uint8_t *b_scales, int64_t M, int64_t N, int64_t K, void *c, int ct,
+                        int64_t ldc, void *work, int64_t work_bytes, void *stream);
+
+/* Bytes of scratch memory for mxfp4_matmul_sliced, at most 4 MB; -1 for a negative or
+ * too large size.  Host only. */
+int64_t qcp_mxfp4_matmul_work(int64_t M, int64_t N, int64_t K);
+
 /* n rounded up to whole 128s, the row length of an MXFP4 payload; -1 if n is
  * negative or above qcp_max_elements().  Host only. */
 int64_t qcp_mxfp4_padded(int64_t n);

@@ -78,6 +78,7 @@ def library():
             "mxfp4_quantize_both": [p, ci, i64, i64, i64, p, p, p, p, p],
             "mxfp4_dequantize": [p, p, i64, i64, p, ci, i64, p],
             "mxfp4_matmul": [p, p, p, p, i64, i64, i64, p, ci, i64, p],
+            "mxfp4_matmul_sliced": [p, p, p, p, i64, i64, i64, p, ci, i64, p, i64, p],
             "qcp_aquavit_level": [i64, i64, ctypes.c_double, ctypes.c_double,
                                   ctypes.POINTER(i32), ctypes.POINTER(i32)],
         }
@@ -91,6 +92,8 @@ def library():
         lib.qcp_payload_bytes.restype = i64
         lib.qcp_mxfp4_padded.argtypes = [i64]
         lib.qcp_mxfp4_padded.restype = i64
+        lib.qcp_mxfp4_matmul_work.argtypes = [i64, i64, i64]
+        lib.qcp_mxfp4_matmul_work.restype = i64
         lib.qcp_strerror.argtypes = [ci]
         lib.qcp_strerror.restype = ctypes.c_char_p
         lib.qcp_version.argtypes = []

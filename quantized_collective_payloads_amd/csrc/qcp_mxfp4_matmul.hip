@@ -343,19 +343,22 @@ template <int FM, int FN> struct Scales {
     uint32_t a[FM], b[FN];
 };
 
-template <int FM, int FN, int CT>
+// SLICED: the tiles are those of `slices` parts of K, one part after the other; c is fp32,
+// an M x N for each.
+template <int FM, int FN, int CT, bool SLICED>
 __global__ __launch_bounds__(kThreads, (tgeom<FM, FN>::waves_per_simd)) void k_mx_matmul_tiled(
     const uint8_t *__restrict__ a, const uint8_t *__restrict__ as, const uint8_t *__restrict__ b,
-    const uint8_t *__restrict__ bs, int64_t M, int64_t N, uint32_t granules, uint32_t m_tiles,
+    const uint8_t *__restrict__ bs, int64_t M, int64_t N, uint32_t row_granules, uint32_t slices, uint32_t m_tiles,
     uint32_t n_tiles, uint32_t groups, void *__restrict__ c, int64_t ldc) {
     using Gm = tgeom<FM, FN>;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[Gm::lds];
     const int tid = (int)__builtin_amdgcn_workitem_id_x();
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = lane_id();
 
-    const uint32_t tiles = m_tiles * n_tiles, row_bytes = granules * 64, mark_bytes = granules * 4;
+    const uint32_t tiles = m_tiles * n_tiles * (SLICED ? slices : 1);
+    const uint32_t row_bytes = row_granules * 64, mark_bytes = row_granules * 4;
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
-    const uint32_t stages = (granules + 1) / 2;
+    uint32_t granules = row_granules, stages = (granules + 1) / 2, slice = 0;   // of the tile
 
     // the tile that is being copied.  Copies: a wave brings a quarter of each operand's
     // rows, 8 rows at a time.  Scales: 64 rows at a time, FM pieces of A, then FN of B,
@@ -366,15 +369,24 @@ __global__ __launch_bounds__(kThreads, (tgeom<FM, FN>::waves_per_simd)) void k_m
     i32x4_t ra, rb, rs[mark_rounds];
     uint32_t vs[mark_rounds], mark_at[mark_rounds], m_rows, n_rows;
     auto set_tile = [&](uint32_t t) __attribute__((always_inline)) {
+        uint32_t skip = 0;                                   // granules before the slice
+        if constexpr (SLICED) {
+            slice = t / (m_tiles * n_tiles);
+            t -= slice * (m_tiles * n_tiles);
+            const uint32_t pairs = row_granules / 2, each = pairs / slices, over = pairs % slices;
+            skip = 2 * (slice * each + min(slice, over));
+            granules = slice + 1 == slices ? row_granules - skip : 2 * (each + (slice < over ? 1 : 0));
+            stages = (granules + 1) / 2;
+        }
         const TilePlace at = tile_place(t, m_tiles, n_tiles);
         m0 = (int64_t)at.m * Gm::TM;
         n0 = (int64_t)at.n * Gm::TN;
         m_rows = (uint32_t)min(M - m0, (int64_t)Gm::TM);
         n_rows = (uint32_t)min(N - n0, (int64_t)Gm::TN);
-        ra = buffer_of(a + m0 * row_bytes, (uint64_t)m_rows * row_bytes);
-        rb = buffer_of(b + n0 * row_bytes, (uint64_t)n_rows * row_bytes);
-        const i32x4_t rsa = buffer_of(as + m0 * mark_bytes, (uint64_t)m_rows * mark_bytes);
-        const i32x4_t rsb = buffer_of(bs + n0 * mark_bytes, (uint64_t)n_rows * mark_bytes);
+        ra = buffer_of(a + m0 * row_bytes + skip * 64, (uint64_t)m_rows * row_bytes - skip * 64);
+        rb = buffer_of(b + n0 * row_bytes + skip * 64, (uint64_t)n_rows * row_bytes - skip * 64);
+        const i32x4_t rsa = buffer_of(as + m0 * mark_bytes + skip * 4, (uint64_t)m_rows * mark_bytes - skip * 4);
+        const i32x4_t rsb = buffer_of(bs + n0 * mark_bytes + skip * 4, (uint64_t)n_rows * mark_bytes - skip * 4);
         static_for<mark_rounds>([&](auto I) __attribute__((always_inline)) {
             constexpr int k = I;
             const int q = min(wave + 4 * k, FM + FN - 1);
@@ -569,6 +581,7 @@ __global__ __launch_bounds__(kThreads, (tgeom<FM, FN>::waves_per_simd)) void k_m
         // the next tile's first copies go out before this one's results
         const int64_t m_done = m0 + (wave & 1) * 32 * FM + r, n_done = n0 + (wave >> 1) * 32 * FN;
         const bool whole = m0 + Gm::TM <= M && n0 + Gm::TN <= N;
+        void *const to = SLICED ? (float *)c + slice * M * N : c;
         tile += groups;
         const bool more = tile < tiles;
         if (more) {
@@ -578,7 +591,7 @@ __global__ __launch_bounds__(kThreads, (tgeom<FM, FN>::waves_per_simd)) void k_m
         }
         static_for<FM * FN>([&](auto I) __attribute__((always_inline)) {
             constexpr int i = I / FN, j = I % FN;
-            store_fragment<CT>(acc[i][j], c, ldc, m_done + 32 * i, n_done + 32 * j, half, M, N, whole);
+            store_fragment<CT>(acc[i][j], to, ldc, m_done + 32 * i, n_done + 32 * j, half, M, N, whole);
         });
         if (!more) break;
         // the copies are older than the stores, of which a whole tile has `stores` at least
@@ -587,17 +600,41 @@ __global__ __launch_bounds__(kThreads, (tgeom<FM, FN>::waves_per_simd)) void k_m
     }
 }
 
-template <int FM, int FN, int CT>
+template <int FM, int FN, int CT, bool SLICED = false>
 hipError_t run_tiled(const uint8_t *a, const uint8_t *as, const uint8_t *b, const uint8_t *bs, int64_t M,
-                     int64_t N, int64_t granules, void *c, int64_t ldc, hipStream_t st) {
+                     int64_t N, int64_t granules, void *c, int64_t ldc, hipStream_t st, int slices = 1) {
     using Gm = tgeom<FM, FN>;
     const int64_t mt = (M + Gm::TM - 1) / Gm::TM, nt = (N + Gm::TN - 1) / Gm::TN;
     // as many work-groups as the GPU holds walk the tiles (a multiple of 8, so that each
     // stays on its XCD's tiles)
-    const unsigned groups = (unsigned)std::min<int64_t>(mt * nt, kCUs * Gm::waves_per_simd);
-    hipLaunchKernelGGL((k_mx_matmul_tiled<FM, FN, CT>), dim3(groups), dim3(kThreads), 0, st, a, as, b, bs, M,
-                       N, (uint32_t)granules, (uint32_t)mt, (uint32_t)nt, groups, c, ldc);
+    const unsigned groups = (unsigned)std::min<int64_t>(mt * nt * slices, kCUs * Gm::waves_per_simd);
+    hipLaunchKernelGGL((k_mx_matmul_tiled<FM, FN, CT, SLICED>), dim3(groups), dim3(kThreads), 0, st, a, as, b, bs, M,
+                       N, (uint32_t)granules, (uint32_t)slices, (uint32_t)mt, (uint32_t)nt, groups, c, ldc);
     return hipGetLastError();
+}
+
+// The sum of the slices, in their order, rounded once: 4 columns a lane.
+template <int CT>
+__global__ __launch_bounds__(kThreads) void k_mx_matmul_join(const float *__restrict__ parts, int slices, int64_t M,
+                                                             int64_t N, void *__restrict__ c, int64_t ldc) {
+    typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+    const int64_t m = group_y();
+    const int64_t n = ((int64_t)__builtin_amdgcn_workgroup_id_x() * kThreads + __builtin_amdgcn_workitem_id_x()) * 4;
+    if (n >= N) return;
+    const int count = N - n < 4 ? (int)(N - n) : 4;
+    const float *p = parts + m * N + n;
+    float v[4] = {};
+    for (int s = 0; s < slices; s++, p += M * N) {
+        if (count == 4) {
+            const f32x4_any x = *(const f32x4_any *)p;
+            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 3; j++)
+                if (j < count) v[j] += p[j];
+        }
+    }
+    store4<CT>(c, m * ldc + n, count, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -705,7 +742,15 @@ hipError_t run_rows(const uint8_t *a, const uint8_t *as, const uint8_t *b, const
 
 template <int CT>
 hipError_t run_matmul(const uint8_t *a, const uint8_t *as, const uint8_t *b, const uint8_t *bs,
-                      int64_t M, int64_t N, int64_t granules, void *c, int64_t ldc, hipStream_t st) {
+                      int64_t M, int64_t N, int64_t granules, void *c, int64_t ldc, float *work, hipStream_t st) {
+    const int slices = work ? mx_matmul_slices(M, N, granules) : 1;
+    if (slices > 1) {
+        const hipError_t e = run_tiled<1, 1, F32, true>(a, as, b, bs, M, N, granules, work, N, st, slices);
+        if (e != hipSuccess) return e;
+        const dim3 grid((unsigned)((N + 4 * kThreads - 1) / (4 * kThreads)), (unsigned)M);
+        hipLaunchKernelGGL((k_mx_matmul_join<CT>), grid, dim3(kThreads), 0, st, work, slices, M, N, c, ldc);
+        return hipGetLastError();
+    }
     const auto tiles = [&](int64_t m, int64_t n) { return ((M + m - 1) / m) * ((N + n - 1) / n); };
     // Few rows: one pass over B by as many work-groups as it has 16 rows; also for more
     // rows of A where 64 x 64 tiles would leave most of the GPU idle and K is short
@@ -746,13 +791,29 @@ hipError_t run_matmul(const uint8_t *a, const uint8_t *as, const uint8_t *b, con
 
 }  // namespace
 
+// A long K and too few tiles for the GPU: slices of K, each a share of the work-groups,
+// added up in a second launch.  256 work-groups measured best (128 and 512 a tenth to a
+// third slower), up to 8 slices: 64 x 512, K = 28672 47 us and 13; 256 x 256 31 and 13.5;
+// 500 x 700, K = 10000 19 and 14; 64 x 4096, K = 14336 27 and 15, K = 8192 17.6 and 14.  The
+// second launch and the scratch memory take the host 4 us: 128 x 1024, K = 8192 11.9 and
+// 13.7.  Against the kernel for few rows: 32 x 512, K = 28672 27 and 14; 32 x 4096,
+// K = 14336 15 and 15.5; 16 x 4096, K = 28672 19.5 and 18.8 at best.  Slices of 128 x 128
+// for more tiles gain up to a fifth (384 x 4096, K = 14336: 41 and 33) for six times the
+// scratch memory, and are left out.
+int mx_matmul_slices(int64_t M, int64_t N, int64_t granules) {
+    const int64_t stages = (granules + 1) / 2, rows = (M + 63) / 64, cols = (N + 63) / 64;
+    if (M <= 16 || N < 1 || rows > 128 || cols > 128 || rows * cols > 128 || granules >= (1 << 18)) return 1;
+    if (stages < (M <= 32 ? 64 : rows * cols < 48 ? 48 : 32)) return 1;
+    return (int)std::min<int64_t>(8, 256 / (rows * cols));
+}
+
 hipError_t launch_mx_matmul(const uint8_t *a, const uint8_t *as, const uint8_t *b, const uint8_t *bs,
                             int64_t M, int64_t N, int64_t granules, void *c, int ct, int64_t ldc,
-                            hipStream_t st) {
+                            float *work, hipStream_t st) {
     switch (ct) {
-    case F16: return run_matmul<F16>(a, as, b, bs, M, N, granules, c, ldc, st);
-    case BF16: return run_matmul<BF16>(a, as, b, bs, M, N, granules, c, ldc, st);
-    case F32: return run_matmul<F32>(a, as, b, bs, M, N, granules, c, ldc, st);
+    case F16: return run_matmul<F16>(a, as, b, bs, M, N, granules, c, ldc, work, st);
+    case BF16: return run_matmul<BF16>(a, as, b, bs, M, N, granules, c, ldc, work, st);
+    case F32: return run_matmul<F32>(a, as, b, bs, M, N, granules, c, ldc, work, st);
     default: return hipErrorInvalidValue;
     }
 }

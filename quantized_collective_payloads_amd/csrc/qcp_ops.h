@@ -38,10 +38,12 @@ hipError_t launch_mx_quantize_both(const void *x, int xt, int64_t rows, int64_t 
 hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,
                                 int64_t cols, void *y, int yt, int64_t ld, hipStream_t st);
 
-// C[M, N] = A B^T, rows of `granules` times 128 values; see qcp_mxfp4_matmul.hip
+// C[M, N] = A B^T, rows of `granules` times 128 values; see qcp_mxfp4_matmul.hip.
+// work: null, or room for slices * M * N floats, slices of K as many as said here
+int mx_matmul_slices(int64_t M, int64_t N, int64_t granules);
 hipError_t launch_mx_matmul(const uint8_t *a, const uint8_t *as, const uint8_t *b, const uint8_t *bs,
                             int64_t M, int64_t N, int64_t granules, void *c, int ct, int64_t ldc,
-                            hipStream_t st);
+                            float *work, hipStream_t st);
 
 // the counter hash of the stochastic rounding: an invertible scramble of 32 bits
 // (two rounds of xor-shift and an odd multiplier, the fractions of sqrt 2 and sqrt 3)

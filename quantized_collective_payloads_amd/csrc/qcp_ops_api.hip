@@ -3,8 +3,8 @@
 //
 // As in qcp_api.hip: each validates its arguments on the host (no HIP call is made for
 // a rejected call or one without work), enqueues on the caller's stream (one kernel;
-// adamw_step one per 64 tensors) and maps a launch error to QCP_EHIP.  Nothing is
-// allocated and no state is kept between calls.
+// adamw_step one per 64 tensors, the sliced product two) and maps a launch error to
+// QCP_EHIP.  Nothing is allocated and no state is kept between calls.
 #include <math.h>
 #include <stdint.h>
 
@@ -210,9 +210,9 @@ int mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, 
     return status_of(qcp::launch_mx_dequantize(codes, scales, rows, cols, y, yt, ld, (hipStream_t)stream));
 }
 
-int mxfp4_matmul(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *b_codes,
-                 const uint8_t *b_scales, int64_t M, int64_t N, int64_t K, void *c, int ct, int64_t ldc,
-                 void *stream) {
+int mxfp4_matmul_sliced(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *b_codes,
+                        const uint8_t *b_scales, int64_t M, int64_t N, int64_t K, void *c, int ct,
+                        int64_t ldc, void *work, int64_t work_bytes, void *stream) {
     int64_t cb, pad;
     int rc = check_matrix(M, N, ldc, ct, &cb);
     if (rc != QCP_OK) return rc;
@@ -221,14 +221,30 @@ int mxfp4_matmul(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t 
     if (!mx_payload(M, K, &pad) || !mx_payload(N, K, &pad)) return QCP_EINVAL;
     if ((M + 127) / 128 > qcp::kMaxGroups / ((N + 127) / 128)) return QCP_EINVAL;   // tiles of C
     if (!c || (K > 0 && (!a_codes || !a_scales || !b_codes || !b_scales))) return QCP_EINVAL;
+    const int64_t need = work ? qcp_mxfp4_matmul_work(M, N, K) : 0;
+    if (work_bytes < need) return QCP_EINVAL;
     if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(b_codes) || !aligned16(b_scales) ||
-        (uintptr_t)c % dtype_bytes(ct))
+        !aligned16(work) || (uintptr_t)c % dtype_bytes(ct))
         return QCP_EALIGN;
-    if (overlap(c, cb, a_codes, M * pad / 2) || overlap(c, cb, a_scales, M * pad / 32) ||
-        overlap(c, cb, b_codes, N * pad / 2) || overlap(c, cb, b_scales, N * pad / 32))
-        return QCP_EINVAL;
+    const void *in[4] = {a_codes, a_scales, b_codes, b_scales};
+    const int64_t bytes[4] = {M * pad / 2, M * pad / 32, N * pad / 2, N * pad / 32};
+    if (overlap(c, cb, work, need)) return QCP_EINVAL;
+    for (int i = 0; i < 4; i++)
+        if (overlap(c, cb, in[i], bytes[i]) || overlap(work, need, in[i], bytes[i])) return QCP_EINVAL;
     return status_of(qcp::launch_mx_matmul(a_codes, a_scales, b_codes, b_scales, M, N, pad / 128, c, ct,
-                                           ldc, (hipStream_t)stream));
+                                           ldc, need ? (float *)work : nullptr, (hipStream_t)stream));
+}
+
+int mxfp4_matmul(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *b_codes,
+                 const uint8_t *b_scales, int64_t M, int64_t N, int64_t K, void *c, int ct, int64_t ldc,
+                 void *stream) {
+    return mxfp4_matmul_sliced(a_codes, a_scales, b_codes, b_scales, M, N, K, c, ct, ldc, nullptr, 0, stream);
+}
+
+int64_t qcp_mxfp4_matmul_work(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0 || M > kMaxElems || N > kMaxElems || K > kMaxElems) return -1;
+    const int slices = qcp::mx_matmul_slices(M, N, (K + 127) / 128);
+    return slices > 1 ? 4 * slices * M * N : 0;
 }
 
 int64_t qcp_mxfp4_padded(int64_t n) { return n < 0 || n > kMaxElems ? -1 : (n + 127) / 128 * 128; }

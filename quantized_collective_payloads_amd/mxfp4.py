@@ -173,9 +173,20 @@ def mxfp4_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.T
     if index < 0 or index != other or out is not None:
         _same_gpu(index, a_codes, b_codes, *(() if out is None else (_result(out, M, N, dtype, a_codes),)))
     c = _result(out, M, N, dtype, a_codes)
-    _enqueue("mxfp4_matmul", index, a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(),
-             b_scales.data_ptr(), M, N, K, c.data_ptr(), DTYPES[c.dtype], N)
+    _multiply(index, a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(), M, N, K, c)
     return c
+
+
+def _multiply(index, a, sa, b, sb, M, N, K, c):
+    """The product into c; with scratch memory where the library has a use for it,
+    which it never has for rows of fewer than 8000 values."""
+    work = library().qcp_mxfp4_matmul_work(M, N, K) if K >= 8000 else 0
+    if work:
+        scratch = torch.empty(work, dtype=_u8, device=c.device)
+        _enqueue("mxfp4_matmul_sliced", index, a, sa, b, sb, M, N, K, c.data_ptr(), DTYPES[c.dtype], N,
+                 scratch.data_ptr(), work)
+    else:
+        _enqueue("mxfp4_matmul", index, a, sa, b, sb, M, N, K, c.data_ptr(), DTYPES[c.dtype], N)
 
 
 class _Work:
@@ -211,7 +222,7 @@ def _quantize_to(index, x, rows, cols, straight, transposed):
 
 def _product(index, a, b, M, N, K, dtype, like):
     c = torch.empty((M, N), dtype=dtype, device=like.device)
-    _enqueue("mxfp4_matmul", index, *a, *b, M, N, K, c.data_ptr(), DTYPES[dtype], N)
+    _multiply(index, *a, *b, M, N, K, c)
     return c
 
 

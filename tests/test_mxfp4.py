@@ -276,6 +276,61 @@ def test_product_over_a_very_long_k(gpu):
     check_product(*parts, qcp.mxfp4_matmul(*wide_ones, dtype=torch.float32), "f32", K)
 
 
+SLICED = [(33, 100, 12288), (100, 200, 20000), (64, 512, 28672), (17, 50, 16400), (500, 700, 10000), (128, 4096, 8200),
+          (40, 33, 12161), (129, 257, 13001), (1000, 31, 12345)]
+
+
+@GPU
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", SLICED)
+def test_product_in_slices_of_k(gpu, M, N, K, dt):
+    assert 0 < qcp.library().qcp_mxfp4_matmul_work(M, N, K) <= 4 << 20
+    a, b = random_payload(M, K, M, 110, 124), random_payload(N, K, N, 110, 124)
+    out = qcp.mxfp4_matmul(*a, *b, dtype=DT[dt])
+    check_product(a, b, out, dt, (M, N, K))
+    assert torch.equal(out, qcp.mxfp4_matmul(*a, *b, dtype=DT[dt]))
+    a[1][M // 2, -1] = 255                               # in the last slice, of one row
+    bad = qcp.mxfp4_matmul(*a, *b, dtype=DT[dt])
+    assert bad[M // 2].isnan().all() and torch.equal(bad[:M // 2], out[:M // 2])
+    # without scratch memory: one sum, within the same bound
+    a[1][M // 2, -1] = 120
+    whole = torch.empty(M, N, dtype=DT[dt], device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    assert qcp.library().mxfp4_matmul(a[0].data_ptr(), a[1].data_ptr(), b[0].data_ptr(), b[1].data_ptr(), M, N, K,
+                                      whole.data_ptr(), qcp.DTYPES[DT[dt]], N, stream) == 0
+    check_product(a, b, whole, dt, (M, N, K))
+
+
+@GPU
+def test_slices_stay_in_their_scratch_memory_and_rows(gpu):
+    M, N, K, ldc = 70, 130, 13000, 137
+    a, b = random_payload(M, K, 1, 110, 124), random_payload(N, K, 2, 110, 124)
+    need = qcp.library().qcp_mxfp4_matmul_work(M, N, K)
+    work = torch.full((need + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+    c = torch.full((M, ldc), 7.0, device="cuda")
+    assert qcp.library().mxfp4_matmul_sliced(
+        a[0].data_ptr(), a[1].data_ptr(), b[0].data_ptr(), b[1].data_ptr(), M, N, K, c.data_ptr(), qcp.DTYPES[c.dtype],
+        ldc, work.data_ptr(), need, torch.cuda.current_stream().cuda_stream) == 0
+    check_product(a, b, c[:, :N], "f32", "rows apart")
+    assert (c[:, N:] == 7).all() and (work[need:] == 0x5a).all()
+
+
+@GPU
+def test_slices_in_a_graph(gpu):
+    M, N, K = 48, 96, 12288
+    a, b = random_payload(M, K, 1, 110, 124), random_payload(N, K, 2, 110, 124)
+    out = torch.empty(M, N, device="cuda")
+    qcp.mxfp4_matmul(*a, *b, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qcp.mxfp4_matmul(*a, *b, out=out)
+    for seed in (3, 4, 5):
+        for t, new in zip(a, random_payload(M, K, seed, 110, 124)):
+            t.copy_(new)
+        graph.replay()
+        assert torch.equal(out, qcp.mxfp4_matmul(*a, *b, dtype=torch.float32))
+
+
 @GPU
 def test_product_of_integers_is_exact(gpu):
     """Codes at scale 1: every partial sum is a multiple of 1/4 below 2^22, so any
@@ -522,3 +577,18 @@ def test_binding_refuses(lib):
     raises("last dimension 63", qcp.mxfp4_linear, torch.zeros(4, 63), torch.zeros(8, 64))
     raises("weight: 1 dimensions", qcp.mxfp4_linear, torch.zeros(4, 63), torch.zeros(8))
     raises("GPU tensors only", qcp.mxfp4_linear, torch.zeros(4, 64), torch.zeros(8, 64))
+
+
+def test_c_entry_of_the_sliced_product_refuses(lib):
+    work = lib.qcp_mxfp4_matmul_work
+    assert work(64, 512, 28672) == 4 * 8 * 64 * 512 and work(64, 512, 4096) == 0 and work(8, 512, 28672) == 0
+    assert work(0, 64, 28672) == work(64, 64, 0) == 0 and work(-1, 64, 8192) == work(64, 1 << 40, 8192) == -1
+    need = work(64, 64, 12288)
+
+    def mul(a=A, sa=A + S, b=A + 2 * S, sb=A + 3 * S, M=64, N=64, K=12288, c=A + 4 * S, ct=2, ldc=64, w=A + 5 * S, n=need):
+        return lib.mxfp4_matmul_sliced(a, sa, b, sb, M, N, K, c, ct, ldc, w, n, None)
+    assert need > 0 and mul(M=0) == OK and mul(N=0, ldc=0, w=None, n=0) == OK
+    for bad in (dict(n=need - 1), dict(n=-1), dict(w=A), dict(w=A + 4 * S), dict(w=A + 3 * S + 16), dict(K=-1), dict(c=0),
+                dict(a=0), dict(ldc=63), dict(ct=9)):
+        assert mul(**bad) == EINVAL, bad
+    assert mul(w=A + 5 * S + 4) == EALIGN and mul(c=A + 4 * S + 1) == EALIGN
