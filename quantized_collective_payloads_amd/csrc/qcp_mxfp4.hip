@@ -336,10 +336,12 @@ __global__ __launch_bounds__(kThreads) void k_mx_dequantize(const uint32_t *__re
     }
 }
 
-// A matrix above the 256 MB of the last cache is read and its column-wise codes are
-// written past it: 28672 x 8192 fp16 122 -> 114 us, both payloads 160 -> 134; fp32 215 ->
-// 200 and 239 -> 225.  A smaller one may lie there already: 8192 x 4096 bf16, just
-// written, 15.9 us and 21.6 against 17.5 and 24.4; 16384 x 5120 37 and 46 against 45 and 56.
+// A matrix above the 256 MB of the last cache is read past it, which leaves the codes
+// there: 28672 x 8192 fp16 with the dequantize behind it 211 -> 198 us, both payloads and
+// a product 268 -> 236; fp32 408 -> 365 and 352 -> 315.  (Codes written past it too: the
+// quantize alone 119 -> 114, the pair 211.)  A smaller matrix may lie there already:
+// 8192 x 4096 bf16, just written, 15.9 us and 21.6 (both) against 17.5 and 24.4;
+// 16384 x 5120 37 and 46 against 45 and 56.
 constexpr int64_t kStreamBytes = (int64_t)256 << 20;
 constexpr int kTRows = 256;                    // tile of the column-wise quantize
 template <int XT, bool BOTH> constexpr int tile_cols() { return XT != F32 && BOTH ? 128 : 64; }
@@ -358,7 +360,7 @@ __device__ __forceinline__ uint4 row_block(const uint32_t (&w)[4][words8<XT>()],
     return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
-// STREAM: the matrix and the codes pass the caches by
+// STREAM: the matrix passes the caches by
 template <bool STREAM, typename T>
 __device__ __forceinline__ T load_words(const T *p) {
     if constexpr (STREAM) return __builtin_nontemporal_load(p);
@@ -488,12 +490,9 @@ __global__ __launch_bounds__((4 * tile_cols<XT, BOTH>())) void k_mx_quantize_t(c
     for (int k = 0; k < 2; k++) {
         const int line = (tid >> 3) + kTCols / 2 * k, piece = tid & 7;
         const int64_t c = tc + line;
-        if (c < cols && 32 * piece < wide) {
-            u32x4_t *to = (u32x4_t *)(codes + c * (pad_rows / 2) + tr / 2 + 16 * piece);
-            const u32x4_t v = *(const u32x4_t *)(lines + line * kLine + 16 * piece);
-            if constexpr (STREAM) __builtin_nontemporal_store(v, to);
-            else *to = v;
-        }
+        if (c < cols && 32 * piece < wide)
+            *(uint4 *)(codes + c * (pad_rows / 2) + tr / 2 + 16 * piece) =
+                *(const uint4 *)(lines + line * kLine + 16 * piece);
     }
     if (tid < 2 * kTCols) {
         const int line = tid >> 1, half = tid & 1;
