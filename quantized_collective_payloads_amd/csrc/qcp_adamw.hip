@@ -30,8 +30,12 @@
 // The table of tensors is a kernel argument: nothing is allocated or copied.
 //
 // Everything is read and written once, so loads and stores are non-temporal: 27.3M
-// elements with fp32 moments 154 -> 137 us (5.97 TB/s), 369M with 8-bit moments
-// 1112 -> 1060 us (5.61 TB/s); either hint alone gains 1 to 3%.
+// elements with fp32 moments 154 -> 137 us, 369M with 8-bit moments 1112 -> 1060 us
+// (5.61 TB/s); either hint alone gains 1 to 3%.  Only the 16-bit copies, which are read
+// next, stay in the last cache where the moments are fp32 and the copies of a call are at
+// most half of it: 27.3M elements 127 -> 120 us and with a quantize of the copy behind it
+// 141 -> 131, 58.7M 270 -> 252.  Beside 8-bit moments that gains nothing (27.3M elements 70
+// us either way) and loses where they are larger (50.3M 126 -> 141).
 #include "qcp_device.h"
 #include "qcp_ops.h"
 
@@ -67,9 +71,12 @@ __device__ __forceinline__ void store4(float *p, int64_t i, const float (&x)[4])
     __builtin_nontemporal_store(f32x4_any{x[0], x[1], x[2], x[3]}, (f32x4_any *)(p + i));
 }
 
-template <int YT>
+template <int YT, bool KEEP>
 __device__ __forceinline__ void copy4(void *p, int64_t i, const float (&x)[4]) {
-    __builtin_nontemporal_store(u32x2_any{narrow2<YT>(x[0], x[1]), narrow2<YT>(x[2], x[3])}, (u32x2_any *)((uint16_t *)p + i));
+    const u32x2_any v = {narrow2<YT>(x[0], x[1]), narrow2<YT>(x[2], x[3])};
+    u32x2_any *to = (u32x2_any *)((uint16_t *)p + i);
+    if constexpr (KEEP) *to = v;
+    else __builtin_nontemporal_store(v, to);
 }
 
 template <int YT>
@@ -105,12 +112,14 @@ template <int G> struct ogeom {
     static constexpr int VB = G > 256 ? G / 256 : 1;        // vectors per block
 };
 
+constexpr int64_t kKeepCopies = (int64_t)128 << 20;        // bytes
 constexpr int kVec = 4;                                     // vectors per wave
 constexpr int kWaveElems = 256 * kVec;
 constexpr int kGroupElems = kWaveElems * kWavesPerGroup;
 
-// a wave's 1024 elements; FULL: all of them lie within the tensor
-template <int GT, int G, bool FULL>
+// a wave's 1024 elements; FULL: all of them lie within the tensor; KEEP: the copies are
+// not written past the caches
+template <int GT, int G, bool KEEP, bool FULL>
 __device__ __forceinline__ void adamw_wave(const AdamwTensor &t, const AdamwConst &c, float gs,
                                            int64_t base) {
     constexpr bool EIGHT = G != 0;
@@ -188,8 +197,8 @@ __device__ __forceinline__ void adamw_wave(const AdamwTensor &t, const AdamwCons
         if (FULL || left[u] == 4) {
             store4(t.param, at[u], p[u]);
             if (t.copy) {
-                if (c.copy_type == BF16) copy4<BF16>(t.copy, at[u], p[u]);
-                else copy4<F16>(t.copy, at[u], p[u]);
+                if (c.copy_type == BF16) copy4<BF16, KEEP>(t.copy, at[u], p[u]);
+                else copy4<F16, KEEP>(t.copy, at[u], p[u]);
             }
         } else {
 #pragma unroll
@@ -251,7 +260,7 @@ __device__ __forceinline__ void adamw_wave(const AdamwTensor &t, const AdamwCons
     }
 }
 
-template <int GT, int G, int CAP>
+template <int GT, int G, bool KEEP, int CAP>
 __global__ __launch_bounds__(kThreads) void k_adamw(const AdamwTable<CAP> table, const AdamwConst c) {
     const uint32_t wg = __builtin_amdgcn_workgroup_id_x();
     const int lane = lane_id();
@@ -262,11 +271,11 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamwTable<CAP> table,
     const int64_t base = (int64_t)(wg - table.first[which]) * kGroupElems + wave * kWaveElems;
     if (base >= t.n) return;
     const float gs = c.grad_scale ? *c.grad_scale : 1.0f;
-    if (base + kWaveElems <= t.n) adamw_wave<GT, G, true>(t, c, gs, base);
-    else adamw_wave<GT, G, false>(t, c, gs, base);
+    if (base + kWaveElems <= t.n) adamw_wave<GT, G, KEEP, true>(t, c, gs, base);
+    else adamw_wave<GT, G, KEEP, false>(t, c, gs, base);
 }
 
-template <int GT, int G, int CAP>
+template <int GT, int G, bool KEEP, int CAP>
 hipError_t run_cap(const AdamwTensor *t, int n, const AdamwConst &c, hipStream_t st) {
     AdamwTable<CAP> table;
     uint32_t groups = 0;
@@ -275,13 +284,13 @@ hipError_t run_cap(const AdamwTensor *t, int n, const AdamwConst &c, hipStream_t
         table.t[i] = i < n ? t[i] : AdamwTensor{};
         if (i < n) groups += (uint32_t)((t[i].n + kGroupElems - 1) / kGroupElems);
     }
-    hipLaunchKernelGGL((k_adamw<GT, G, CAP>), dim3(groups), dim3(kThreads), 0, st, table, c);
+    hipLaunchKernelGGL((k_adamw<GT, G, KEEP, CAP>), dim3(groups), dim3(kThreads), 0, st, table, c);
     return hipGetLastError();
 }
 
 // as few launches as the table's 64 places and the grid's limit allow
-template <int GT, int G>
-hipError_t run_adamw(const AdamwTensor *t, int n, const AdamwConst &c, hipStream_t st) {
+template <int GT, int G, bool KEEP>
+hipError_t run_tables(const AdamwTensor *t, int n, const AdamwConst &c, hipStream_t st) {
     for (int at = 0; at < n;) {
         int64_t groups = 0;
         int k = 0;
@@ -291,12 +300,22 @@ hipError_t run_adamw(const AdamwTensor *t, int n, const AdamwConst &c, hipStream
             groups += more;
             k++;
         }
-        const hipError_t e = k <= 8 ? run_cap<GT, G, 8>(t + at, k, c, st)
-                                    : run_cap<GT, G, 64>(t + at, k, c, st);
+        const hipError_t e = k <= 8 ? run_cap<GT, G, KEEP, 8>(t + at, k, c, st)
+                                    : run_cap<GT, G, KEEP, 64>(t + at, k, c, st);
         if (e != hipSuccess) return e;
         at += k;
     }
     return hipSuccess;
+}
+
+template <int GT, int G>
+hipError_t run_adamw(const AdamwTensor *t, int n, const AdamwConst &c, hipStream_t st) {
+    if constexpr (G == 0) {
+        int64_t copies = 0;
+        for (int i = 0; i < n; i++) copies += t[i].copy ? 2 * t[i].n : 0;
+        if (copies && copies <= kKeepCopies) return run_tables<GT, G, true>(t, n, c, st);
+    }
+    return run_tables<GT, G, false>(t, n, c, st);
 }
 
 template <int GT>

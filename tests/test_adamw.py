@@ -331,6 +331,29 @@ def test_moments_past_32_bits(gpu):
         assert ((np.abs(got) >= a) & (np.abs(got) <= b)).all()
 
 
+@GPU
+@pytest.mark.parametrize("ct", ["f16", "bf16"])
+def test_copies_beyond_half_the_last_cache(gpu, ct):
+    """Above 128 MB of copies they are written past the caches: the same bits as of parts."""
+    n, cut = 67_200_003, 33_600_001
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    p0, grad = torch.randn(n, generator=g, device="cuda") * 0.02, torch.randn(n, generator=g, device="cuda") * 1e-3
+    got = []
+    for parts in ([slice(0, n)], [slice(0, cut), slice(cut, n)]):
+        p, c = p0.clone(), torch.empty(n, dtype=DT[ct], device="cuda")
+        m, v = [], []
+        for part in parts:
+            opt = qcp.AdamW([p[part]], copies=[c[part]], state="f32")
+            for step in (1, 2):
+                qcp.adamw_step(opt, [grad[part]], step, **HYPER)
+            k = part.stop - part.start
+            m.append(opt.m[:k])
+            v.append(opt.v[:k])
+        got.append((p, c, torch.cat(m), torch.cat(v)))
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and torch.equal(got[0][1], got[0][0].to(DT[ct]))
+
+
 # bit patterns of NaN (quiet, all ones, negative) and of the infinities
 BAD = {"f32": (0x7fc00000, 0x7fffffff, 0xffffffff, 0x7f800000, 0xff800000), "f16": (0x7e00, 0x7fff, 0xffff, 0x7c00, 0xfc00),
        "bf16": (0x7fc0, 0x7fff, 0xffff, 0x7f80, 0xff80)}
