@@ -67,7 +67,7 @@ def _result(out, rows: int, cols: int, dtype, like):
     if out is None:
         if dtype not in DTYPES:
             _dtype_code(dtype)
-        return torch.empty((rows, cols), dtype=dtype, device=like.device)
+        return like.new_empty((rows, cols), dtype=dtype)
     _matrix(out, "out")
     _need(out, "out", _ELEMS, 0)
     if tuple(out.shape) != (rows, cols):
@@ -113,9 +113,9 @@ def mxfp4_quantize(x: torch.Tensor, transpose: bool = False, codes=None, scales=
     if index < 0:
         _dev(x)
     if codes is None:
-        codes = torch.empty((lines, P // 2), dtype=_u8, device=x.device)
+        codes = x.new_empty((lines, P // 2), dtype=_u8)
     if scales is None:
-        scales = torch.empty((lines, P // 32), dtype=_u8, device=x.device)
+        scales = codes.new_empty((lines, P // 32))
     _enqueue("mxfp4_quantize", index, x.data_ptr(), DTYPES[x.dtype], rows, cols, ld, 1 if transpose else 0,
              codes.data_ptr(), scales.data_ptr())
     return codes, scales
@@ -141,9 +141,9 @@ def mxfp4_quantize_both(x: torch.Tensor):
     if index < 0:
         _dev(x)
     pc, pr = _pad(cols), _pad(rows)
-    empty = lambda *s: torch.empty(s, dtype=_u8, device=x.device)  # noqa: E731
-    a = empty(rows, pc // 2), empty(rows, pc // 32)
-    b = empty(cols, pr // 2), empty(cols, pr // 32)
+    codes = x.new_empty((rows, pc // 2), dtype=_u8)
+    a = codes, codes.new_empty((rows, pc // 32))
+    b = codes.new_empty((cols, pr // 2)), codes.new_empty((cols, pr // 32))
     _enqueue("mxfp4_quantize_both", index, x.data_ptr(), DTYPES[x.dtype], rows, cols, ld, a[0].data_ptr(),
              a[1].data_ptr(), b[0].data_ptr(), b[1].data_ptr())
     return (b, a) if swap else (a, b)
@@ -182,7 +182,7 @@ def _multiply(index, a, sa, b, sb, M, N, K, c):
     which it never has for rows of fewer than 8000 values."""
     work = library().qcp_mxfp4_matmul_work(M, N, K) if K >= 8000 else 0
     if work:
-        scratch = torch.empty(work, dtype=_u8, device=c.device)
+        scratch = c.new_empty(work, dtype=_u8)
         _enqueue("mxfp4_matmul_sliced", index, a, sa, b, sb, M, N, K, c.data_ptr(), DTYPES[c.dtype], N,
                  scratch.data_ptr(), work)
     else:
@@ -198,7 +198,7 @@ class _Work:
             P = _pad(n)
             self.places.append((at, at + lines * P // 2))
             at += lines * P // 2 + (lines * P // 32 + 15) // 16 * 16
-        self.buffer = torch.empty(at, dtype=_u8, device=like.device)
+        self.buffer = like.new_empty(at, dtype=_u8)
 
     def __getitem__(self, k):
         return _at(self.buffer, self.places[k])
@@ -221,7 +221,7 @@ def _quantize_to(index, x, rows, cols, straight, transposed):
 
 
 def _product(index, a, b, M, N, K, dtype, like):
-    c = torch.empty((M, N), dtype=dtype, device=like.device)
+    c = like.new_empty((M, N), dtype=dtype)
     _multiply(index, *a, *b, M, N, K, c)
     return c
 
