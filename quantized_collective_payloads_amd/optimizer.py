@@ -40,8 +40,9 @@ class AdamW:
              Flat, tensor i at offsets[i]; n_state elements and, for "e4m3",
              uint8 codes with n_state/G scales.
 
-    The tensors must keep their storage: a step on a parameter that was given
-    another one since raises ValueError.  The attributes are read-only.
+    The tensors must keep their storage: a step after a parameter, a copy or a
+    moment was given another one, or one of another size, raises ValueError.  The
+    attributes are read-only.
     """
 
     params = property(lambda self: self._params)
@@ -94,21 +95,36 @@ class AdamW:
         self._m_scales = own(m_scales, ns, _F32) if eight else None
         self._v_scales = own(v_scales, ns, _F32) if eight else None
 
-        # what every step passes on, made once: the tensors above stay alive with it
+        # what every step passes on, made once: the tensors above stay alive with it.  Every
+        # step asks whether they still lie there and whether their storages (the distinct
+        # ones) still have their sizes: one that shrank may lie where it did
         n = len(params)
-        self._index, self._at = device.index, [p.data_ptr() for p in params]
+        moments = tuple(t for t in (self._m, self._v, self._m_scales, self._v_scales) if t is not None)
+        self._tensors = (*params, *(copies or ()), *moments)
+        self._index, self._at = device.index, [t.data_ptr() for t in self._tensors]
+        self._storages = tuple({s._cdata: s for s in map(torch.Tensor.untyped_storage, self._tensors)}.values())
+        self._bytes = [s.nbytes() for s in self._storages]
         self._written = params + (copies or [])
         table = ctypes.c_void_p * n
-        self._arrays = (table(*self._at), None if copies is None else table(*(c.data_ptr() for c in copies)),
+        self._arrays = (table(*self._at[:n]), None if copies is None else table(*(c.data_ptr() for c in copies)),
                         (ctypes.c_int64 * n)(*sizes), (ctypes.c_int64 * n)(*offsets))
         self._bases = tuple(None if a is None else ctypes.addressof(a) for a in self._arrays)
         self._copy_type = DTYPES[copies[0].dtype] if copies else 0
         self._moments = (self._m.data_ptr(), self._m_scales.data_ptr() if eight else None,
                          self._v.data_ptr(), self._v_scales.data_ptr() if eight else None)
 
+    def _moved(self):
+        """The names of the tensors that no longer have the storage they were given with."""
+        names = [f"params[{i}]" for i in range(len(self._params))]
+        names += [f"copies[{i}]" for i in range(len(self._copies or ()))]
+        names += ["m", "v", "m_scales", "v_scales"][:len(self._tensors) - len(names)]
+        size = {s._cdata: n for s, n in zip(self._storages, self._bytes)}
+        return [name for name, t, at in zip(names, self._tensors, self._at)
+                if t.data_ptr() != at or t.untyped_storage().nbytes() != size.get(t.untyped_storage()._cdata)]
+
 
 _numel, _data_ptr, _get_device = torch.Tensor.numel, torch.Tensor.data_ptr, torch.Tensor.get_device
-_is_contiguous = torch.Tensor.is_contiguous
+_is_contiguous, _nbytes = torch.Tensor.is_contiguous, torch.UntypedStorage.nbytes
 
 
 def adamw_step(optimizer: AdamW, grads, step: int, lr: float, beta1: float = 0.9,
@@ -148,8 +164,8 @@ def adamw_step(optimizer: AdamW, grads, step: int, lr: float, beta1: float = 0.9
     if grad_scale is not None:
         _need(grad_scale, "grad_scale", _F32, 1)
         _dev(o._m, grad_scale)
-    if list(map(_data_ptr, o._params)) != o._at:
-        raise ValueError("params: a parameter was given another storage since the AdamW was made")
+    if list(map(_data_ptr, o._tensors)) != o._at or list(map(_nbytes, o._storages)) != o._bytes:
+        raise ValueError(f"{', '.join(o._moved())}: given another storage since the AdamW was made")
     params, copies, sizes, offsets = o._bases
     m, ms, v, vs = o._moments
     at = array("Q", list(map(_data_ptr, grads)))              # a third of the time of a ctypes array

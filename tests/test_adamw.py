@@ -525,3 +525,78 @@ def test_c_entry_refuses_an_eps_below_normal(lib):
     for eps in (1e-45, 1e-40, 2.0 ** -127, np.nextafter(2.0 ** -126, 0)):
         want = EINVAL if np.float32(eps) < np.float32(2.0 ** -126) else OK
         assert call(eps=float(eps), sizes=[0]) == want, eps
+
+
+# ------------------------------------------------------------------ tensors that moved
+
+
+@pytest.fixture()
+def on_cpu(monkeypatch):
+    """The binding on CPU tensors, with the launch replaced: the list of calls it would make."""
+    from quantized_collective_payloads_amd import optimizer
+    calls = []
+    monkeypatch.setattr(optimizer, "_dev", lambda *ts: torch.device("cpu"))
+    monkeypatch.setattr(optimizer, "_enqueue", lambda name, index, *args: calls.append((name, args)))
+    return calls
+
+
+def small(device, state="e4m3", separate=True):
+    """An AdamW over two tensors with everything that a step reads or writes given to it."""
+    z = lambda n, dt=torch.float32: torch.zeros(n, dtype=dt, device=device)  # noqa: E731
+    eight = state == "e4m3"
+    kind = torch.uint8 if eight else torch.float32
+    params = [z(300), z(5)] if separate else list(z(305).split([300, 5]))
+    opt = qcp.AdamW(params, copies=[z(300, torch.bfloat16), z(5, torch.bfloat16)], state=state, m=z(512, kind),
+                    v=z(512, kind), m_scales=z(4) if eight else None, v_scales=z(4) if eight else None)
+    return opt, [z(300), z(5)]
+
+
+def tensors_of(opt):
+    got = {f"params[{i}]": p for i, p in enumerate(opt.params)} | {f"copies[{i}]": c for i, c in enumerate(opt.copies)}
+    got |= {"m": opt.m, "v": opt.v}
+    return got | ({} if opt.m_scales is None else {"m_scales": opt.m_scales, "v_scales": opt.v_scales})
+
+
+# how a tensor comes to lie elsewhere, or to hold less than it did where it was
+MOVES = {"data": lambda t: setattr(t, "data", t.clone()), "set": lambda t: t.set_(t.clone()),
+         "freed": lambda t: t.untyped_storage().resize_(0),
+         "shrunk": lambda t: t.untyped_storage().resize_(t.untyped_storage().nbytes() // 2)}
+
+
+@pytest.mark.parametrize("how", MOVES)
+@pytest.mark.parametrize("state", ["e4m3", "f32"])
+def test_a_tensor_with_another_storage_is_refused(on_cpu, state, how):
+    names = list(tensors_of(small("cpu", state)[0]))
+    assert len(names) == (8 if state == "e4m3" else 6)
+    for name in names:
+        opt, grads = small("cpu", state)
+        qcp.adamw_step(opt, grads, 1, 1e-3)
+        assert len(on_cpu) == 1
+        on_cpu.clear()
+        MOVES[how](tensors_of(opt)[name])
+        with pytest.raises(ValueError, match=f"^{name.replace('[', '.').replace(']', '.')}: given another storage"):
+            qcp.adamw_step(opt, grads, 2, 1e-3)
+        assert not on_cpu
+
+
+def test_a_storage_shared_by_several_tensors_is_named_for_each(on_cpu):
+    opt, grads = small("cpu", separate=False)
+    qcp.adamw_step(opt, grads, 1, 1e-3)
+    opt.params[0].untyped_storage().resize_(1240)                  # more than it was
+    with pytest.raises(ValueError, match="params.0., params.1.: given another storage"):
+        qcp.adamw_step(opt, grads, 2, 1e-3)
+    assert len(on_cpu) == 1
+
+
+@GPU
+def test_a_moved_copy_is_not_written(gpu):
+    """What the copies and moments were given instead, and where they were, stays as it is."""
+    for name in ("copies[0]", "m", "v_scales"):
+        opt, grads = small("cuda")
+        t = tensors_of(opt)[name]
+        old, new = t.detach(), torch.ones_like(t)
+        t.data = new
+        with pytest.raises(ValueError, match="another storage"):
+            qcp.adamw_step(opt, [g + 1 for g in grads], 1, 1e-3)
+        torch.cuda.synchronize()
+        assert not old.any() and (new == 1).all() and not opt.params[0].any(), name
