@@ -104,7 +104,6 @@ class AdamW:
         self._index, self._at = device.index, [t.data_ptr() for t in self._tensors]
         self._storages = tuple({s._cdata: s for s in map(torch.Tensor.untyped_storage, self._tensors)}.values())
         self._bytes = [s.nbytes() for s in self._storages]
-        self._written = params + (copies or [])
         table = ctypes.c_void_p * n
         self._arrays = (table(*self._at[:n]), None if copies is None else table(*(c.data_ptr() for c in copies)),
                         (ctypes.c_int64 * n)(*sizes), (ctypes.c_int64 * n)(*offsets))
@@ -176,4 +175,4 @@ def adamw_step(optimizer: AdamW, grads, step: int, lr: float, beta1: float = 0.9
                  min(_MAX_TENSORS, len(grads) - first), DTYPES[kind], o._copy_type, _STATES[o._state], m, ms, v, vs,
                  o._n_state, o._G, step, lr, beta1, beta2, eps, weight_decay,
                  None if grad_scale is None else grad_scale.data_ptr(), seed & 0xFFFFFFFFFFFFFFFF)
-    torch.autograd.graph.increment_version(o._written)
+    torch.autograd.graph.increment_version(o._tensors)

@@ -600,3 +600,20 @@ def test_a_moved_copy_is_not_written(gpu):
             qcp.adamw_step(opt, [g + 1 for g in grads], 1, 1e-3)
         torch.cuda.synchronize()
         assert not old.any() and (new == 1).all() and not opt.params[0].any(), name
+
+
+@pytest.mark.parametrize("state", ["e4m3", "f32"])
+def test_every_written_tensor_gets_a_new_version(on_cpu, state):
+    opt, grads = small("cpu", state)
+    before = {name: t._version for name, t in tensors_of(opt).items()}
+    qcp.adamw_step(opt, grads, 1, 1e-3)
+    assert all(t._version > before[name] for name, t in tensors_of(opt).items())
+
+
+def test_a_step_after_a_moment_entered_a_graph_is_seen(on_cpu):
+    opt, grads = small("cpu", "f32")
+    w = torch.ones(512, requires_grad=True)
+    y = (w * opt.m).sum()
+    qcp.adamw_step(opt, grads, 1, 1e-3)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
