@@ -239,6 +239,19 @@ int adamw_step(float *const *params, const void *const *grads, void *const *copi
                double weight_decay, const float *grad_scale, uint64_t seed, void *stream);
 
 /*
+ * What adamw_step would refuse, for any number of tensors: a step over more than
+ * QCP_ADAMW_MAX_TENSORS is several calls, each of which sees its own tensors only, so
+ * its caller asks here first and makes none of them where one would be refused.
+ * Host only.  Errors: QCP_EINVAL, QCP_EALIGN; QCP_EUNSUPPORTED where the host has no
+ * memory to compare the buffers.
+ */
+int qcp_adamw_check(float *const *params, const void *const *grads, void *const *copies,
+                    const int64_t *sizes, const int64_t *offsets, int64_t n_tensors, int gt, int ct,
+                    int state, void *m, float *m_scales, void *v, float *v_scales, int64_t n_state,
+                    int32_t G, int64_t step, double lr, double beta1, double beta2, double eps,
+                    double weight_decay, const float *grad_scale);
+
+/*
  * The MXFP4 payload of a matrix (OCP Microscaling: E2M1 codes, one E8M0 scale per
  * 32): 4.25 bits per weight, which the matrix cores multiply as it is
  * (mxfp4_matmul).  A payload of `lines` rows of n values holds each row padded

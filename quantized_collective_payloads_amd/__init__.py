@@ -74,6 +74,8 @@ def library():
             "unpack_subbyte_records": [p, i64, i32, i32, p, ci, p],
             "adamw_step": [p, p, p, p, p, i32, ci, ci, ci, p, p, p, p, i64, i32, i64, f64, f64, f64,
                            f64, f64, p, ctypes.c_uint64, p],
+            "qcp_adamw_check": [p, p, p, p, p, i64, ci, ci, ci, p, p, p, p, i64, i32, i64, f64, f64, f64,
+                                f64, f64, p],
             "mxfp4_quantize": [p, ci, i64, i64, i64, i32, p, p, p],
             "mxfp4_quantize_both": [p, ci, i64, i64, i64, p, p, p, p, p],
             "mxfp4_dequantize": [p, p, i64, i64, p, ci, i64, p],

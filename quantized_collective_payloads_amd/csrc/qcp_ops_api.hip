@@ -4,11 +4,12 @@
 // As in qcp_api.hip: each validates its arguments on the host (no HIP call is made for
 // a rejected call or one without work), enqueues on the caller's stream (one kernel;
 // adamw_step one per 64 tensors, the sliced product two) and maps a launch error to
-// QCP_EHIP.  Nothing is allocated and no state is kept between calls.
+// QCP_EHIP.  Nothing is allocated on the device and no state is kept between calls.
 #include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <new>
 
 #include "qcp.h"
 #include "qcp_ops.h"
@@ -71,71 +72,129 @@ bool mx_payload(int64_t lines, int64_t n, int64_t *pad) {
     return *pad == 0 || (n <= (int64_t)1 << 31 && lines <= kMaxElems / *pad);
 }
 
+// The arguments that adamw_step checks, by their names there
+struct AdamwArgs {
+    float *const *params;
+    const void *const *grads;
+    void *const *copies;
+    const int64_t *sizes, *offsets;
+    int64_t n_tensors;
+    int gt, ct, state;
+    void *m;
+    float *m_scales;
+    void *v;
+    float *v_scales;
+    int64_t n_state;
+    int32_t G;
+    int64_t step;
+    double lr, beta1, beta2, eps, weight_decay;
+    const float *grad_scale;
+};
+
+// ranges that a step over n tensors touches, at most
+constexpr int64_t adamw_ranges(int64_t n) { return 3 * n + 5; }
+
+// All but the overlaps.  *live: tensors with elements; *past: the end of the last
+// tensor's blocks in the moments
+int check_adamw(const AdamwArgs &a, int64_t *live, int64_t *past) {
+    *live = *past = 0;
+    if (a.n_tensors < 0 || a.n_state < 0 || !valid_g(a.G)) return QCP_EINVAL;
+    if (!valid_dtype(a.gt) || (a.state != QCP_F32 && a.state != QCP_E4M3)) return QCP_EINVAL;
+    if (a.copies && a.ct != QCP_F16 && a.ct != QCP_BF16) return QCP_EINVAL;
+    // the denominator is at least eps, and the device's reciprocal takes what is below
+    // the least normal number for 0
+    const bool scalars = a.step >= 1 && isfinite(a.lr) && a.lr >= 0 && a.beta1 >= 0 && a.beta1 < 1 && a.beta2 >= 0 &&
+                         a.beta2 < 1 && isfinite(a.eps) && (float)a.eps >= 0x1p-126f && isfinite(a.weight_decay) &&
+                         a.weight_decay >= 0;
+    if (!scalars) return QCP_EINVAL;
+    if (a.n_tensors == 0) return QCP_OK;
+    if (!a.params || !a.grads || !a.sizes || !a.offsets) return QCP_EINVAL;
+    const bool eight = a.state == QCP_E4M3;
+    for (int64_t i = 0; i < a.n_tensors; i++) {
+        const int64_t n = a.sizes[i];
+        if (n < 0 || n > kMaxElems) return QCP_EINVAL;
+        if (a.offsets[i] < *past || a.offsets[i] % a.G != 0) return QCP_EINVAL;
+        if (a.offsets[i] > a.n_state || n_blocks(n, a.G) > (a.n_state - a.offsets[i]) / a.G) return QCP_EINVAL;
+        *past = a.offsets[i] + n_blocks(n, a.G) * a.G;
+        if (n == 0) continue;
+        ++*live;
+        if (!a.params[i] || !a.grads[i] || (a.copies && !a.copies[i])) return QCP_EINVAL;
+        if ((uintptr_t)a.params[i] % 4 || (uintptr_t)a.grads[i] % dtype_bytes(a.gt)) return QCP_EALIGN;
+        if (a.copies && (uintptr_t)a.copies[i] % 2) return QCP_EALIGN;
+    }
+    if (*live == 0) return QCP_OK;
+    if (!a.m || !a.v || (eight && (!a.m_scales || !a.v_scales))) return QCP_EINVAL;
+    if (!aligned16(a.m) || !aligned16(a.v)) return QCP_EALIGN;
+    if (eight && (!aligned16(a.m_scales) || !aligned16(a.v_scales))) return QCP_EALIGN;
+    if ((uintptr_t)a.grad_scale % 4) return QCP_EALIGN;
+    return QCP_OK;
+}
+
+// does a buffer that a step writes meet another one?  r: room for adamw_ranges(n_tensors)
+bool adamw_clash(const AdamwArgs &a, int64_t past, Range *r) {
+    const bool eight = a.state == QCP_E4M3;
+    int64_t k = 0;
+    auto range = [&](const void *p, int64_t bytes, bool written) {
+        if (p && bytes > 0) r[k++] = Range{(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, written};
+    };
+    for (int64_t i = 0; i < a.n_tensors; i++) {
+        const int64_t n = a.sizes[i];
+        if (n == 0) continue;
+        range(a.params[i], 4 * n, true);
+        range(a.grads[i], n * dtype_bytes(a.gt), false);
+        if (a.copies) range(a.copies[i], 2 * n, true);
+    }
+    range(a.m, eight ? past : 4 * past, true);
+    range(a.v, eight ? past : 4 * past, true);
+    if (eight) {
+        range(a.m_scales, past / a.G * 4, true);
+        range(a.v_scales, past / a.G * 4, true);
+    }
+    range(a.grad_scale, 4, false);
+    return ranges_clash(r, k);
+}
+
 }  // namespace
 
 extern "C" {
+
+int qcp_adamw_check(float *const *params, const void *const *grads, void *const *copies,
+                    const int64_t *sizes, const int64_t *offsets, int64_t n_tensors, int gt, int ct,
+                    int state, void *m, float *m_scales, void *v, float *v_scales, int64_t n_state,
+                    int32_t G, int64_t step, double lr, double beta1, double beta2, double eps,
+                    double weight_decay, const float *grad_scale) {
+    const AdamwArgs a = {params, grads, copies, sizes, offsets, n_tensors, gt, ct, state, m, m_scales, v, v_scales,
+                         n_state, G, step, lr, beta1, beta2, eps, weight_decay, grad_scale};
+    int64_t live, past;
+    const int rc = check_adamw(a, &live, &past);
+    if (rc != QCP_OK || live == 0) return rc;
+    // live tensors were all looked at, so their number is that of a real array
+    Range *r = new (std::nothrow) Range[adamw_ranges(n_tensors)];
+    if (!r) return QCP_EUNSUPPORTED;
+    const bool clash = adamw_clash(a, past, r);
+    delete[] r;
+    return clash ? QCP_EINVAL : QCP_OK;
+}
 
 int adamw_step(float *const *params, const void *const *grads, void *const *copies,
                const int64_t *sizes, const int64_t *offsets, int32_t n_tensors, int gt, int ct,
                int state, void *m, float *m_scales, void *v, float *v_scales, int64_t n_state,
                int32_t G, int64_t step, double lr, double beta1, double beta2, double eps,
                double weight_decay, const float *grad_scale, uint64_t seed, void *stream) {
-    if (n_tensors < 0 || n_tensors > QCP_ADAMW_MAX_TENSORS || n_state < 0 || !valid_g(G)) return QCP_EINVAL;
-    if (!valid_dtype(gt) || (state != QCP_F32 && state != QCP_E4M3)) return QCP_EINVAL;
-    if (copies && ct != QCP_F16 && ct != QCP_BF16) return QCP_EINVAL;
-    // the denominator is at least eps, and the device's reciprocal takes what is below
-    // the least normal number for 0
-    const bool scalars = step >= 1 && isfinite(lr) && lr >= 0 && beta1 >= 0 && beta1 < 1 && beta2 >= 0 &&
-                         beta2 < 1 && isfinite(eps) && (float)eps >= 0x1p-126f && isfinite(weight_decay) &&
-                         weight_decay >= 0;
-    if (!scalars) return QCP_EINVAL;
-    if (n_tensors == 0) return QCP_OK;
-    if (!params || !grads || !sizes || !offsets) return QCP_EINVAL;
-    const bool eight = state == QCP_E4M3;
-    int64_t past = 0;                                       // end of the last tensor's blocks
-    int32_t live = 0;
-    for (int32_t i = 0; i < n_tensors; i++) {
-        const int64_t n = sizes[i];
-        if (n < 0 || n > kMaxElems) return QCP_EINVAL;
-        if (offsets[i] < past || offsets[i] % G != 0) return QCP_EINVAL;
-        if (offsets[i] > n_state || n_blocks(n, G) > (n_state - offsets[i]) / G) return QCP_EINVAL;
-        past = offsets[i] + n_blocks(n, G) * G;
-        if (n == 0) continue;
-        live++;
-        if (!params[i] || !grads[i] || (copies && !copies[i])) return QCP_EINVAL;
-        if ((uintptr_t)params[i] % 4 || (uintptr_t)grads[i] % dtype_bytes(gt)) return QCP_EALIGN;
-        if (copies && (uintptr_t)copies[i] % 2) return QCP_EALIGN;
-    }
-    if (live == 0) return QCP_OK;
-    if (!m || !v || (eight && (!m_scales || !v_scales))) return QCP_EINVAL;
-    if (!aligned16(m) || !aligned16(v)) return QCP_EALIGN;
-    if (eight && (!aligned16(m_scales) || !aligned16(v_scales))) return QCP_EALIGN;
-    if ((uintptr_t)grad_scale % 4) return QCP_EALIGN;
+    if (n_tensors > QCP_ADAMW_MAX_TENSORS) return QCP_EINVAL;
+    const AdamwArgs a = {params, grads, copies, sizes, offsets, n_tensors, gt, ct, state, m, m_scales, v, v_scales,
+                         n_state, G, step, lr, beta1, beta2, eps, weight_decay, grad_scale};
+    int64_t live, past;
+    const int rc = check_adamw(a, &live, &past);
+    if (rc != QCP_OK || live == 0) return rc;
 
     // 41 KB and 74 KB of the caller's stack
     qcp::AdamwTensor t[QCP_ADAMW_MAX_TENSORS];
-    Range r[3 * QCP_ADAMW_MAX_TENSORS + 5];
-    int64_t k = 0, at = 0;
-    auto range = [&](const void *p, int64_t bytes, bool written) {
-        if (p && bytes > 0) r[k++] = Range{(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, written};
-    };
-    for (int32_t i = 0; i < n_tensors; i++) {
-        const int64_t n = sizes[i];
-        if (n == 0) continue;
-        void *copy = copies ? copies[i] : nullptr;
-        t[at++] = qcp::AdamwTensor{params[i], grads[i], copy, n, offsets[i]};
-        range(params[i], 4 * n, true);
-        range(grads[i], n * dtype_bytes(gt), false);
-        range(copy, 2 * n, true);
-    }
-    range(m, eight ? past : 4 * past, true);
-    range(v, eight ? past : 4 * past, true);
-    if (eight) {
-        range(m_scales, past / G * 4, true);
-        range(v_scales, past / G * 4, true);
-    }
-    range(grad_scale, 4, false);
-    if (ranges_clash(r, k)) return QCP_EINVAL;
+    Range r[adamw_ranges(QCP_ADAMW_MAX_TENSORS)];
+    if (adamw_clash(a, past, r)) return QCP_EINVAL;
+    for (int32_t i = 0, at = 0; i < n_tensors; i++)
+        if (sizes[i] > 0)
+            t[at++] = qcp::AdamwTensor{params[i], grads[i], copies ? copies[i] : nullptr, sizes[i], offsets[i]};
 
     uint32_t key = 0;
     for (uint32_t word : {(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)step, (uint32_t)((uint64_t)step >> 32)})
@@ -156,7 +215,7 @@ int adamw_step(float *const *params, const void *const *grads, void *const *copi
     c.eps = (float)eps;
     c.key = key;
     c.copy_type = ct;
-    return status_of(qcp::launch_adamw(t, live, gt, state, G, c, (hipStream_t)stream));
+    return status_of(qcp::launch_adamw(t, (int)live, gt, state, G, c, (hipStream_t)stream));
 }
 
 int mxfp4_quantize(const void *x, int xt, int64_t rows, int64_t cols, int64_t ld, int32_t transpose,

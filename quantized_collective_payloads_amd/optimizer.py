@@ -14,7 +14,7 @@ from array import array
 
 import torch
 
-from . import (DTYPES, FORMATS, _check_n_G, _dev, _ELEMS, _enqueue, _F32, _need, _U8, n_blocks)
+from . import (DTYPES, FORMATS, _check, _check_n_G, _dev, _ELEMS, _enqueue, _F32, _need, _U8, library, n_blocks)
 
 _STATES = {"f32": DTYPES[torch.float32], "e4m3": FORMATS["e4m3"]}
 _COPIES = (torch.float16, torch.bfloat16)
@@ -169,10 +169,13 @@ def adamw_step(optimizer: AdamW, grads, step: int, lr: float, beta1: float = 0.9
     m, ms, v, vs = o._moments
     at = array("Q", list(map(_data_ptr, grads)))              # a third of the time of a ctypes array
     table = at.buffer_info()[0]
-    for first in range(0, len(grads), _MAX_TENSORS):
+    n, scale = len(grads), None if grad_scale is None else grad_scale.data_ptr()
+    rest = (DTYPES[kind], o._copy_type, _STATES[o._state], m, ms, v, vs, o._n_state, o._G, step, lr, beta1, beta2,
+            eps, weight_decay, scale)
+    if n > _MAX_TENSORS:                                      # several calls: all of them or none
+        _check("adamw_step", library().qcp_adamw_check(params, table, copies, sizes, offsets, n, *rest))
+    for first in range(0, n, _MAX_TENSORS):
         k = 8 * first
         _enqueue("adamw_step", index, params + k, table + k, copies and copies + k, sizes + k, offsets + k,
-                 min(_MAX_TENSORS, len(grads) - first), DTYPES[kind], o._copy_type, _STATES[o._state], m, ms, v, vs,
-                 o._n_state, o._G, step, lr, beta1, beta2, eps, weight_decay,
-                 None if grad_scale is None else grad_scale.data_ptr(), seed & 0xFFFFFFFFFFFFFFFF)
+                 min(_MAX_TENSORS, n - first), *rest, seed & 0xFFFFFFFFFFFFFFFF)
     torch.autograd.graph.increment_version(o._tensors)

@@ -617,3 +617,90 @@ def test_a_step_after_a_moment_entered_a_graph_is_seen(on_cpu):
     qcp.adamw_step(opt, grads, 1, 1e-3)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
+
+
+# ------------------------------------------------------------------ more tensors than one call takes
+
+
+def check(n, **kw):
+    """qcp_adamw_check for n tensors of 4 elements (G = 32) at addresses of their own."""
+    base = {"params": A, "grads": A + (1 << 30), "copies": A + (2 << 30)}
+    a = {k: [b + 64 * i for i in range(n)] for k, b in base.items()}
+    a |= dict(sizes=[4] * n, offsets=[32 * i for i in range(n)], gt=3, ct=2, state=0x43, m=A + (3 << 30), ms=A + (4 << 30),
+              v=A + (5 << 30), vs=A + (6 << 30), n_state=32 * n, G=32, step=1, eps=1e-8, scale=A + (7 << 30))
+    for k, v in kw.items():
+        if isinstance(v, dict):                                    # one place of an array
+            for i, x in v.items():
+                a[k][i] = x
+        else:
+            a[k] = v
+    arr = lambda t, x: None if x is None else (t * n)(*x)  # noqa: E731
+    return qcp.library().qcp_adamw_check(
+        *(arr(ctypes.c_void_p, a[k]) for k in ("params", "grads", "copies")), arr(ctypes.c_int64, a["sizes"]),
+        arr(ctypes.c_int64, a["offsets"]), n, a["gt"], a["ct"], a["state"], a["m"], a["ms"], a["v"], a["vs"],
+        a["n_state"], a["G"], a["step"], 1e-3, 0.9, 0.999, a["eps"], 0.0, a["scale"])
+
+
+@pytest.mark.parametrize("n", [6, 1024, 2100])
+def test_check_over_any_number_of_tensors(lib, n):
+    first, last = 1, n - 2
+    assert check(n) == OK and check(n, copies=None) == OK and check(n, scale=None) == OK
+    assert check(n, sizes=[0] * n, params=[0] * n) == OK           # nothing to do
+    # gradients may meet one another
+    assert check(n, grads={first: A + (1 << 30) + 64 * last}) == OK
+    for bad in (dict(params={first: A + 64 * last + 12}), dict(params={last: A + 64 * first}),
+                dict(grads={last: A + 64 * first + 8}), dict(grads={first: A + (3 << 30) + 32 * last}),
+                dict(copies={last: A + 64 * first}), dict(copies={first: A + (2 << 30) + 64 * last + 2}),
+                dict(scale=A + 64 * last), dict(m=A), dict(v=A + (3 << 30)), dict(params={last: 0}), dict(copies={last: 0}),
+                dict(sizes={last: -1}), dict(sizes={last: 33}), dict(offsets={last: 0}), dict(n_state=32 * n - 1),
+                dict(step=0), dict(eps=0.0), dict(G=33), dict(gt=9), dict(state=1), dict(ct=3)):
+        assert check(n, **bad) == EINVAL, bad
+    for bad in (dict(params={last: A + 64 * last + 2}), dict(copies={last: A + (2 << 30) + 64 * last + 1}),
+                dict(vs=A + (6 << 30) + 8), dict(scale=A + (7 << 30) + 1)):
+        assert check(n, **bad) == EALIGN, bad
+
+
+def test_check_without_arguments(lib):
+    c = qcp.library().qcp_adamw_check
+    none = [None] * 5
+    rest = (3, 2, 0x43, None, None, None, None, 0, 32, 1, 1e-3, 0.9, 0.999, 1e-8, 0.0, None)
+    assert c(*none, 0, *rest) == OK and c(*none, -1, *rest) == EINVAL and c(*none, 1 << 62, *rest) == EINVAL
+
+
+def many(device, n=2100):
+    z = lambda k: torch.zeros(k, device=device)  # noqa: E731
+    opt = qcp.AdamW([z(8) for _ in range(n)], state="f32", G=32)
+    return opt, [z(8) + 1 for _ in range(n)]
+
+
+BROKEN = {"a parameter twice, far apart": lambda p, g: p.__setitem__(1500, p[5]),
+          "a later gradient that is an earlier parameter": lambda p, g: g.__setitem__(2000, p[3]),
+          "an earlier gradient that is a later parameter": lambda p, g: g.__setitem__(3, p[2000]),
+          "a gradient that is its parameter, in the last call": lambda p, g: g.__setitem__(2060, p[2060])}
+
+
+@pytest.mark.parametrize("what", BROKEN)
+def test_a_step_of_several_calls_is_refused_whole(on_cpu, lib, what):
+    opt, grads = many("cpu")
+    params = list(opt.params)
+    BROKEN[what](params, grads)
+    opt = qcp.AdamW(params, state="f32", G=32)
+    with pytest.raises(qcp.QcpError, match="adamw_step"):
+        qcp.adamw_step(opt, grads, 1, 1e-3)
+    assert not on_cpu and params[7]._version == 0
+    opt, grads = many("cpu")
+    qcp.adamw_step(opt, grads, 1, 1e-3)
+    assert [args[5] for _, args in on_cpu] == [1024, 1024, 52]
+
+
+@GPU
+@pytest.mark.parametrize("what", BROKEN)
+def test_a_refused_step_of_several_calls_changes_nothing(gpu, what):
+    opt, grads = many("cuda")
+    params = list(opt.params)
+    BROKEN[what](params, grads)
+    opt = qcp.AdamW(params, state="f32", G=32)
+    with pytest.raises(qcp.QcpError, match="adamw_step"):
+        qcp.adamw_step(opt, grads, 1, 1e-3)
+    torch.cuda.synchronize()
+    assert not opt.m.any() and not opt.v.any() and not torch.cat(params).any()
