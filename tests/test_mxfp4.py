@@ -592,3 +592,29 @@ def test_c_entry_of_the_sliced_product_refuses(lib):
                 dict(a=0), dict(ldc=63), dict(ct=9)):
         assert mul(**bad) == EINVAL, bad
     assert mul(w=A + 5 * S + 4) == EALIGN and mul(c=A + 4 * S + 1) == EALIGN
+
+
+@pytest.fixture()
+def layer_on_cpu(monkeypatch):
+    """The layer on CPU tensors, its launches replaced: quantizing does nothing and a product is zero."""
+    from quantized_collective_payloads_amd import mxfp4
+    monkeypatch.setattr(mxfp4, "_same_gpu", lambda index, *ts: None)
+    monkeypatch.setattr(mxfp4, "_quantize_to", lambda *args: None)
+    monkeypatch.setattr(mxfp4, "_product", lambda index, a, b, M, N, K, dtype, like: like.new_zeros((M, N), dtype=dtype))
+
+
+@pytest.mark.parametrize("which", ["x", "weight", "both"])
+@pytest.mark.parametrize("grad", [True, False])
+def test_linear_refuses_forward_mode_tangents(layer_on_cpu, grad, which):
+    """With and without gradients: it has no rule for them, and an output without a tangent
+    would say that the derivative is zero."""
+    from torch.autograd import forward_ad
+    x, w = torch.ones(3, 32), torch.ones(4, 32)
+    with torch.set_grad_enabled(grad), forward_ad.dual_level():
+        a = forward_ad.make_dual(x, x) if which != "weight" else x
+        b = forward_ad.make_dual(w, w) if which != "x" else w
+        for v in (a, a.view(3, 1, 32), a.t().contiguous().t()):
+            with pytest.raises(NotImplementedError):
+                qcp.mxfp4_linear(v, b)
+        assert qcp.mxfp4_linear(x, w).shape == (3, 4)
+    assert qcp.mxfp4_linear(x, w).shape == (3, 4)
