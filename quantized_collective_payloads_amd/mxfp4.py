@@ -280,7 +280,8 @@ def mxfp4_linear(x: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
         raise ValueError("x: expected a torch.Tensor with at least one dimension")
     if x.shape[-1] != weight.shape[1]:
         raise ValueError(f"x: last dimension {x.shape[-1]}, weight's {weight.shape[1]}")
-    x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+    # flatten, where reshape(-1, 0) would not know how many rows
+    x2 = x if x.dim() == 2 else x.flatten(0, -2) if x.dim() > 2 else x.unsqueeze(0)
     _matrix(x2, "x")
     _same_gpu(x.get_device(), x, weight)
     x2, w = x2.contiguous(), weight.contiguous()

@@ -618,3 +618,35 @@ def test_linear_refuses_forward_mode_tangents(layer_on_cpu, grad, which):
                 qcp.mxfp4_linear(v, b)
         assert qcp.mxfp4_linear(x, w).shape == (3, 4)
     assert qcp.mxfp4_linear(x, w).shape == (3, 4)
+
+
+EMPTY = [(2, 3, 0), (0,), (3, 0), (0, 3, 0), (0, 0), (2, 0, 64), (0, 64), (64,), (2, 1, 3, 64)]
+
+
+def like_torch(shape, device):
+    """y and the gradients have the shapes of torch's own layer, and its zeros where there is nothing to sum."""
+    x, w = (torch.ones(s, device=device, requires_grad=True) for s in (shape, (5, shape[-1])))
+    y = qcp.mxfp4_linear(x, w)
+    want = torch.nn.functional.linear(x, w)
+    assert y.shape == want.shape
+    with torch.no_grad():
+        assert qcp.mxfp4_linear(x, w).shape == want.shape
+    dx, dw = torch.autograd.grad(y.sum(), (x, w))
+    assert dx.shape == x.shape and dw.shape == w.shape
+    return y, dx, dw, x.numel() == 0
+
+
+@pytest.mark.parametrize("shape", EMPTY)
+def test_linear_shapes_without_elements(layer_on_cpu, shape):
+    like_torch(shape, "cpu")
+
+
+@GPU
+@pytest.mark.parametrize("shape", EMPTY)
+def test_linear_of_nothing_is_zero(gpu, shape):
+    y, dx, dw, nothing = like_torch(shape, "cuda")
+    torch.cuda.synchronize()
+    if nothing:
+        assert not y.any() and not dx.any() and not dw.any()
+    else:                                                  # ones are exact
+        assert (y == shape[-1]).all() and (dx == 5).all() and (dw == y.numel() / 5).all()
