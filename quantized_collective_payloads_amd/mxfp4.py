@@ -16,6 +16,7 @@ from torch.autograd.forward_ad import unpack_dual
 from . import (DTYPES, _dev, _dtype_code, _ELEMS, _enqueue, _need, _U8, library)
 
 _u8 = torch.uint8
+_UNSLICED = 62 * 128              # 31 stages of 256: slices of K begin at 32
 
 
 def mxfp4_padded(n: int) -> int:
@@ -180,8 +181,8 @@ def mxfp4_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.T
 
 def _multiply(index, a, sa, b, sb, M, N, K, c):
     """The product into c; with scratch memory where the library has a use for it,
-    which it never has for rows of fewer than 8000 values."""
-    work = library().qcp_mxfp4_matmul_work(M, N, K) if K >= 8000 else 0
+    which it never has for rows of up to _UNSLICED values."""
+    work = library().qcp_mxfp4_matmul_work(M, N, K) if K > _UNSLICED else 0
     if work:
         scratch = c.new_empty(work, dtype=_u8)
         _enqueue("mxfp4_matmul_sliced", index, a, sa, b, sb, M, N, K, c.data_ptr(), DTYPES[c.dtype], N,

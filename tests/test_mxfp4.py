@@ -650,3 +650,28 @@ def test_linear_of_nothing_is_zero(gpu, shape):
         assert not y.any() and not dx.any() and not dw.any()
     else:                                                  # ones are exact
         assert (y == shape[-1]).all() and (dx == 5).all() and (dw == y.numel() / 5).all()
+
+
+def test_rows_below_the_bound_have_no_slices(lib):
+    """The binding asks for scratch memory only above this length: the library has no use for
+    it at any shape up to there, and one right above."""
+    from quantized_collective_payloads_amd.mxfp4 import _UNSLICED
+    work = qcp.library().qcp_mxfp4_matmul_work
+    shapes = [(M, N) for M in (17, 32, 33, 64, 128, 200, 500, 2048, 8192) for N in (1, 16, 64, 500, 700, 2048, 4096, 8192)]
+    for K in (1, 128, 4096, _UNSLICED - 127, _UNSLICED):
+        assert not any(work(M, N, K) for M, N in shapes), K
+    for K in (_UNSLICED + 1, 7950, 7999, 8000, 8064):
+        assert work(128, 2048, K) > 0 and work(500, 700, K) > 0, K
+
+
+@GPU
+@pytest.mark.parametrize("K", [7936, 7937, 7950, 7999, 8000])
+def test_layer_and_product_agree_bit_for_bit(gpu, K):
+    """A layer passes the length of its rows, a product of payloads the padded one: the same
+    kernel for both."""
+    x, w = values(128, K, "bf16", 3), values(2048, K, "bf16", 4)
+    y = qcp.mxfp4_linear(x, w)
+    c = qcp.mxfp4_matmul(*qcp.mxfp4_quantize(x), *qcp.mxfp4_quantize(w))
+    assert torch.equal(y.view(torch.int16), c.view(torch.int16))
+    x32, w32 = x.float(), w.float()                        # every bit of the fp32 sums
+    assert torch.equal(qcp.mxfp4_linear(x32, w32), qcp.mxfp4_matmul(*qcp.mxfp4_quantize(x), *qcp.mxfp4_quantize(w), torch.float32))
