@@ -284,13 +284,14 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 constexpr int kCUs = 256;
 
 // 64 lanes x 16 bytes from rsrc[voff + soff] to LDS at `lds` + 16 * lane.  The
-// caller waits for it with wait_and_meet; no vector register is written, and nothing
-// else in these kernels uses m0.
+// caller waits for it with wait_and_meet; no vector register is written.  The
+// instruction takes the LDS address from m0, which is an operand here, so that the
+// compiler knows what it holds; s_nop is the wait state between the two.
 __device__ __forceinline__ void copy_to_lds(uint32_t lds, uint32_t voff, i32x4_t rsrc, uint32_t soff) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                  :
-                 : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(voff), "s"(rsrc),
-                   "s"(__builtin_amdgcn_readfirstlane((int)soff))
+                 : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane((int)soff)),
+                   "{m0}"(__builtin_amdgcn_readfirstlane((int)lds))
                  : "memory");
 }
 
