@@ -729,15 +729,17 @@ template <int FA, int FB, int CT>
 hipError_t run_rows(const uint8_t *a, const uint8_t *as, const uint8_t *b, const uint8_t *bs, int64_t M,
                     int64_t N, int64_t granules, void *c, int64_t ldc, hipStream_t st) {
     const dim3 grid((unsigned)((N + 16 * FB - 1) / (16 * FB)), (unsigned)((M + 16 * FA - 1) / (16 * FA)));
-    const int64_t groups = (int64_t)grid.x * grid.y, steps = (granules + 3) / 4;
-    // enough waves to cover the latency of memory, each with a step at least
-    const int wv = groups * 4 >= 4096 || steps <= 4 ? 4 : groups * 8 >= 2048 || steps <= 8 ? 8 : 16;
-    if (wv == 4)
+    // A wave for each step of K up to 4, else 8 (us with 4 and with 8, warm and cold): 1 x
+    // 14336, K = 512 2.6 and 2.7, 3.4 and 3.5; 1 x 28672, K = 1024 4.3 and 4.6, 5.5 and 6.6; but
+    // 1 x 256, K = 2560 2.7 and 2.7, 3.3 and 3.1; 1 x 4096, K = 14336 7.5 and 6.8, 10.6 and 8.2;
+    // 32 x 4096, K = 4096 5.4 and 5.5, 6.8 and 6.4; 1 x 28672, K = 8192 23.9 both, 27.7 and 27.5.
+    // 16 waves took 2 to 5% more than 8 from 1 to 512 work-groups (1 x 1024, K = 14336 6.7
+    // and 7.6 against 6.5 and 7.4) and a third more beyond, where K is short.  (8 waves: rows
+    // of more than 2048 values, of which a payload holds fewer than 2^25, so the grid is small.)
+    if (granules <= 16)
         hipLaunchKernelGGL((k_mx_matmul_rows<FA, FB, 4, CT>), grid, dim3(256), 0, st, a, as, b, bs, M, N, granules, c, ldc);
-    else if (wv == 8)
-        hipLaunchKernelGGL((k_mx_matmul_rows<FA, FB, 8, CT>), grid, dim3(512), 0, st, a, as, b, bs, M, N, granules, c, ldc);
     else
-        hipLaunchKernelGGL((k_mx_matmul_rows<FA, FB, 16, CT>), grid, dim3(1024), 0, st, a, as, b, bs, M, N, granules, c, ldc);
+        hipLaunchKernelGGL((k_mx_matmul_rows<FA, FB, 8, CT>), grid, dim3(512), 0, st, a, as, b, bs, M, N, granules, c, ldc);
     return hipGetLastError();
 }
 
