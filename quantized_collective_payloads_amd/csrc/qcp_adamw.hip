@@ -1,4 +1,4 @@
-// qcp_adamw.hip -- AdamW over the many tensors of an optimizer shard in one launch.
+// qcp_adamw.hip -- AdamW over the many tensors of an optimizer shard, 64 to a launch.
 //
 // The step that stands between the gradient reduce-scatter (whose last reduce
 // leaves fp32 sums on each rank) and the weight all-gather.  Per element, with
@@ -30,12 +30,13 @@
 // The table of tensors is a kernel argument: nothing is allocated or copied.
 //
 // Everything is read and written once, so loads and stores are non-temporal: 27.3M
-// elements with fp32 moments 154 -> 137 us, 369M with 8-bit moments 1112 -> 1060 us
-// (5.61 TB/s); either hint alone gains 1 to 3%.  Only the 16-bit copies, which are read
-// next, stay in the last cache where the moments are fp32 and the copies of a call are at
-// most half of it: 27.3M elements 127 -> 120 us and with a quantize of the copy behind it
-// 141 -> 131, 58.7M 270 -> 252.  Beside 8-bit moments that gains nothing (27.3M elements 70
-// us either way) and loses where they are larger (50.3M 126 -> 141).
+// elements with fp32 moments 153 -> 134 us, with 8-bit ones 86 -> 70, 369M 1105 -> 1042
+// (5.7 TB/s).  Only the 16-bit copies, which are read next, stay in the last cache where
+// the moments are fp32 and the copies of a call are at most half of it: 27.3M elements
+// 134 -> 128 us and with a quantize of the copy behind it 147 -> 140; 58.7M with the
+// quantize 316 -> 293, alone 289 -> 271 on the same tensors again and 289 -> 297 on three
+// sets in turn.  Beside 8-bit moments the step alone loses by it (27.3M 70 -> 73, 50.3M
+// 138 -> 144; with the quantize 82 -> 81 and 160 -> 150), so there they pass it by.
 #include "qcp_device.h"
 #include "qcp_ops.h"
 

@@ -10,8 +10,9 @@
 // The row's 4 scale bytes are one dword; its half is shifted down once per
 // granule, and the instruction picks the byte.
 //
-// Measured: 8192 x 8192, K = 28672 876 to 958 us (4.4 to 4.0 PFLOP/s, by the GPU's
-// clock); 2048 x 14336, K = 4096 84 us (2.9); 1 x 14336, K = 4096 8.2 us (3.8 TB/s).
+// Measured, by the GPU's clock: 8192 x 8192, K = 28672 850 to 960 us (4.5 to 4.0 PFLOP/s);
+// 2048 x 14336, K = 4096 78 us (3.1), 81 with operands from HBM; 1 x 14336, K = 4096 7.4 us
+// with B in the last cache, 8.7 from HBM (3.6 TB/s).
 #include <algorithm>
 
 #include "qcp_device.h"
@@ -193,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void k_mx_matmul_short(
 }
 
 // The plain form, for K from 2^25 on, whose rows are beyond the 32-bit offsets within a
-// tile of the kernels below: a wave computes 64 x 64 of C from 2 + 2 fragments per granule,
+// tile of the kernels below, and for more than 2^24 tiles of 64 x 64: a wave computes 64 x 64 of C from 2 + 2 fragments per granule,
 // read straight from memory; a work-group's 4 waves make 128 x 128.
 template <int CT>
 __global__ __launch_bounds__(kThreads) void k_mx_matmul(const uint8_t *__restrict__ a,
@@ -245,22 +246,25 @@ __global__ __launch_bounds__(kThreads) void k_mx_matmul(const uint8_t *__restric
 // ---------------------------------------------------------------------------
 // 64*FM x 64*FN of C per work-group, staged through LDS.
 // ---------------------------------------------------------------------------
-// Bound: the matrix cores, and their power: random codes multiplied in registers alone
-// reach 5.8 PFLOP/s, and the same call on codes of zero takes a fifth less time than on
-// normal values.  Four waves, 2 x 2, hold 32*FM x 32*FN each.  At 4 x 4
-// that is 256 x 256 per work-group and 256 accumulators, one wave per SIMD: a
+// Bound: the matrix cores' clock and the waits between their instructions.  Normal values
+// multiplied in registers alone reach 6.5 PFLOP/s, zeros 9.7: the clock follows the energy
+// (here 1.3 to 1.7 GHz against 2.1).  8192 x 8192, K = 28672 takes 860 us and 710 (4.5 and
+// 5.4): in cycles the cores are busy 61 to 65% and 57%, and a wave waits at barriers and
+// for memory 20% and 25% of the time.  Four waves, 2 x 2, hold 32*FM x 32*FN each.  At
+// 4 x 4 that is 256 x 256 per work-group and 256 accumulators, one wave per SIMD: a
 // phase is 32 instructions of 32 cycles on 16 KB of operands, a quarter of what LDS
 // gives.  At 2 x 2, 128 x 128, two work-groups share a CU: twice the operand traffic
 // per product, but four times as many tiles, and one's stores run beside the
 // other's products.  A stage is 256 of K: 128 bytes of each operand row, whole cache
-// lines, in one of two slots.
+// lines, in one of two slots; with two, the barrier of each stage waits for all copies
+// in flight (1 x 1 has four slots, and two stages' copies stay in flight).
 //
 // Within a stage the lower half-wave takes the first granule (64 bytes of its row)
 // and the upper one the second, so a lane's four blocks have their scales in one
 // dword and the instruction picks the byte.  A stage is two phases of 128 of K.
 //
-// Copies go from memory to LDS without registers (buffer_load ... lds), so their
-// latency is covered by the matrix instructions of a whole stage or more: with the
+// Copies go from memory to LDS without registers (buffer_load ... lds), and run beside
+// the matrix instructions of a stage or more: with the
 // fragments of phase 0 in registers a wave issues its products and reads those of
 // phase 1; one barrier, at which every wave has read this stage and holds no
 // outstanding copy of the next; the copies of the stage after that go into the
@@ -273,8 +277,13 @@ __global__ __launch_bounds__(kThreads) void k_mx_matmul(const uint8_t *__restric
 // for 4 granules at a time, 16 bytes a row, into slots of their own.
 //
 // A work-group walks several tiles: the copies of the next one's first stages go out
-// before the results of this one, whose stores then cover their latency (14336 x 4096,
-// K = 2048: 119 us for a work-group per tile with 8-byte stores, 109 so).
+// before the results of this one, and its stores stay in flight into the next tile
+// (14336 x 4096, K = 2048: 119 us for a work-group per tile with 8-byte stores, 109 so).
+// At 4 x 4 less overlaps than this order says: the compiler keeps 41 vector registers (66
+// with fp32 results) in scratch memory around a tile.  None is reloaded in the loop of
+// stages, but each reload elsewhere waits for everything in flight, so the results
+// follow the copies' arrival and the next tile's first products that of the results.
+// The forms of 1 x 1 and 2 x 2 keep all in registers.
 //
 // Rows past the end repeat the last row.  Windows in K are pulled back to end
 // with the row: a last odd granule comes as the second one of its window, and is
@@ -642,7 +651,7 @@ __global__ __launch_bounds__(kThreads) void k_mx_matmul_join(const float *__rest
 // Few rows of A (a token, a small batch): 16*FA rows against 16*FB rows of B.
 // ---------------------------------------------------------------------------
 // Bound: reading B once, at these sizes the latency of it (1 x 14336, K = 4096: 31 MB in
-// 8.2 us; the smallest calls take 3.3).  v_mfma_scale_f32_16x16x128_f8f6f4 takes 16 rows, so N/16
+// 7.4 us from the last cache, 8.7 from HBM; the smallest calls take 2.5).  v_mfma_scale_f32_16x16x128_f8f6f4 takes 16 rows, so N/16
 // work-groups; the WV waves of one deal out K in steps of 512 and add their sums in
 // LDS in a fixed order, so a few rows still fill the GPU, without a second launch.  Of a step's 4 granules
 // a quarter-wave takes one: a lane reads 64 consecutive bytes of its row and one
@@ -757,10 +766,10 @@ hipError_t run_matmul(const uint8_t *a, const uint8_t *as, const uint8_t *b, con
     const auto tiles = [&](int64_t m, int64_t n) { return ((M + m - 1) / m) * ((N + n - 1) / n); };
     // Few rows: one pass over B by as many work-groups as it has 16 rows; also for more
     // rows of A where 64 x 64 tiles would leave most of the GPU idle and K is short
-    // (64 x 4096, K = 4096: 8.5 us warm and 10.0 cold against 7.4 and 12.1; 77 x 1001,
-    // K = 1111: 4.6 and 4.6 against 4.7 and 5.6; but 200 x 520, K = 8192: 13.4 and 14.2
-    // against 10.4 and 14.1).  32 x 28672, K = 8192 is 1792 work-groups of rows and 448
-    // tiles: 50 us and 58 against 21 and 53.
+    // (64 x 4096, K = 4096: 8.2 us warm and 8.9 cold against 7.3 and 10.9; 32 x 4096, the
+    // same K: 5.7 and 6.4 against 7.3 and 9.8; 77 x 1001, K = 1111: 3.6 and 3.5 against 4.7
+    // and 5.0; but 200 x 520, K = 8192: 13.6 and 14.4 against 11.2 and 14.1).  32 x 28672,
+    // K = 8192 is 1792 work-groups of rows and 448 tiles: 49 us and 52 against 22 and 32.
     const int64_t small = tiles(64, 64), middle = tiles(128, 128), large = tiles(256, 256);
     const bool staged = granules >= 4 && granules < (1 << 18) && small <= kMaxGroups;
     const bool rows = (N + 15) / 16 <= kMaxGroups;
@@ -768,12 +777,12 @@ hipError_t run_matmul(const uint8_t *a, const uint8_t *as, const uint8_t *b, con
     if (rows && M <= 32 && (small < 128 || !staged)) return run_rows<2, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
     if (rows && small <= 64 && granules <= 32) return run_rows<4, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
     if (staged) {
-        // 64 x 64 while they fit the GPU twice over (512 x 4096, K = 4096: 12.6 us
-        // against 13.2 with 128 x 128); then 128 x 128, 512 at a time, or 256 x 256, 256
+        // 64 x 64 while they fit the GPU twice over (512 x 4096, K = 4096: 11.2 us
+        // against 12.6 with 128 x 128); then 128 x 128, 512 at a time, or 256 x 256, 256
         // at a time, by what their rounds take: 1.35 us a stage and 3.5 more, or 2.05 and
-        // 11 (measured against the other: 8192 x 8192, K = 28672: 1240 us and 958;
-        // 4096 x 4096, K = 4096: 52 and 45; 14336 x 4096, K = 2048: 104 and 112;
-        // 2048 x 4096, K = 14336: 82 and 95)
+        // 11 (measured against the other: 8192 x 8192, K = 28672: 1116 us and 865;
+        // 4096 x 4096, K = 4096: 47 and 42; 14336 x 4096, K = 2048: 89 and 107;
+        // 2048 x 4096, K = 14336: 74 and 90; 2048 x 14336, K = 4096: 80 and 82)
         const int64_t stages = (granules + 1) / 2;
         if (small <= 512) return run_tiled<1, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
         if ((middle + 511) / 512 * (27 * stages + 70) < (large + 255) / 256 * (41 * stages + 220))
@@ -796,8 +805,8 @@ hipError_t run_matmul(const uint8_t *a, const uint8_t *as, const uint8_t *b, con
 
 // A long K and too few tiles for the GPU: slices of K, each a share of the work-groups,
 // added up in a second launch.  256 work-groups measured best (128 and 512 a tenth to a
-// third slower), up to 8 slices: 64 x 512, K = 28672 47 us and 13; 256 x 256 31 and 13.5;
-// 500 x 700, K = 10000 19 and 14; 64 x 4096, K = 14336 27 and 15, K = 8192 17.6 and 14.  The
+// third slower), up to 8 slices, by the GPU's clock: 64 x 512, K = 28672 30 us and 12; 256 x
+// 256 30 and 12; 64 x 4096, K = 14336 18.5 and 13, K = 8192 11.2 and 10.8 (cold 17 and 14).  The
 // second launch and the scratch memory take the host 4 us: 128 x 1024, K = 8192 11.9 and
 // 13.7.  Against the kernel for few rows: 32 x 512, K = 28672 27 and 14; 32 x 4096,
 // K = 14336 15 and 15.5; 16 x 4096, K = 28672 19.5 and 18.8 at best.  Slices of 128 x 128

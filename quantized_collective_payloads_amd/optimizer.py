@@ -33,7 +33,7 @@ class AdamW:
     params   list of contiguous fp32 GPU tensors; their storage is updated in place
     copies   None, or one fp16 or bf16 tensor per parameter (all of one type),
              which receives the rounded parameter at every step
-    state    "e4m3" (8-bit moments) or "f32"
+    state    "e4m3" (8-bit moments, rounded at random: the default) or "f32"
     G        block size of the 8-bit moments (in both states a tensor's moments
              begin at a multiple of it)
     m, v, m_scales, v_scales   the moments of an earlier run; zeros by default.
