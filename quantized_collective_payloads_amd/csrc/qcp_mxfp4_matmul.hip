@@ -248,8 +248,8 @@ __global__ __launch_bounds__(kThreads) void k_mx_matmul(const uint8_t *__restric
 // ---------------------------------------------------------------------------
 // Bound: the matrix cores' clock and the waits between their instructions.  Normal values
 // multiplied in registers alone reach 6.5 PFLOP/s, zeros 9.7: the clock follows the energy
-// (here 1.3 to 1.7 GHz against 2.1).  8192 x 8192, K = 28672 takes 860 us and 710 (4.5 and
-// 5.4): in cycles the cores are busy 61 to 65% and 57%, and a wave waits at barriers and
+// (here 1.3 to 1.8 GHz against 2.1).  8192 x 8192, K = 28672 takes 860 us and 710 (4.5 and
+// 5.4): in cycles the cores are busy 59 to 65% and 57%, and a wave waits at barriers and
 // for memory 20% and 25% of the time.  Four waves, 2 x 2, hold 32*FM x 32*FN each.  At
 // 4 x 4 that is 256 x 256 per work-group and 256 accumulators, one wave per SIMD: a
 // phase is 32 instructions of 32 cycles on 16 KB of operands, a quarter of what LDS
@@ -780,7 +780,7 @@ hipError_t run_matmul(const uint8_t *a, const uint8_t *as, const uint8_t *b, con
         // 64 x 64 while they fit the GPU twice over (512 x 4096, K = 4096: 11.2 us
         // against 12.6 with 128 x 128); then 128 x 128, 512 at a time, or 256 x 256, 256
         // at a time, by what their rounds take: 1.35 us a stage and 3.5 more, or 2.05 and
-        // 11 (measured against the other: 8192 x 8192, K = 28672: 1116 us and 865;
+        // 11 (measured, 128 and 256: 8192 x 8192, K = 28672: 1116 us and 865;
         // 4096 x 4096, K = 4096: 47 and 42; 14336 x 4096, K = 2048: 89 and 107;
         // 2048 x 4096, K = 14336: 74 and 90; 2048 x 14336, K = 4096: 80 and 82)
         const int64_t stages = (granules + 1) / 2;
