@@ -315,6 +315,73 @@ int64_t qcp_mxfp4_matmul_work(int64_t M, int64_t N, int64_t K);
  * negative or above qcp_max_elements().  Host only. */
 int64_t qcp_mxfp4_padded(int64_t n);
 
+/*
+ * The INT8 payload of a matrix with one scale per row: a token of an activation, an
+ * output channel of a weight.  The rows of n codes are padded with zeros to
+ * P = qcp_mxfp4_padded(n) (whole 128s):
+ *   codes    rows x P bytes, two's complement
+ *   scales   one fp32 per row
+ * Quantize: as quantize_blockwise with the row as its block: s = absmax / 127 (IEEE; a
+ * row of zeros, or one whose quotient underflows, has s = +0 and codes 0), a code is
+ * the fp32 quotient x / s rounded half to even within [-127, 127].  A row with an
+ * infinity or a NaN has a NaN scale and codes 0.
+ *   x          rows x cols elements of type xt (aligned to them), rows ld elements
+ *              apart, ld >= cols; rows without elements get the scale 0
+ * Dequantize: y (rows x cols of type yt, rows ld apart) is the fp32 product code * s,
+ * rounded once to yt.
+ *   codes, scales   16-byte aligned; rows * P <= qcp_max_elements(), n <= 2^31
+ * Errors: QCP_EINVAL, QCP_EALIGN, QCP_EHIP.
+ */
+int int8_quantize(const void *x, int xt, int64_t rows, int64_t cols, int64_t ld, uint8_t *codes,
+                  float *scales, void *stream);
+int int8_dequantize(const uint8_t *codes, const float *scales, int64_t rows, int64_t cols, void *y, int yt,
+                    int64_t ld, void *stream);
+
+/*
+ * Product of two such payloads: c[m, n] = sa[m] * sb[n] * sum over k of qa[m, k] * qb[n, k],
+ * rounded to type ct (rows ldc elements apart).  The sum is exact (any codes of 8 bits,
+ * -128 too); the sum, the scales and their products are rounded to fp32.
+ *   a_codes, a_scales   the payload of A, M rows of K codes (tokens)
+ *   b_codes, b_scales   the payload of B, N rows of K codes (a weight, [out, in])
+ *   K <= 130944, within which no sum leaves 32 bits; K = 0 gives zeros (times the scales)
+ *   work     null, or scratch memory on the device of at least qcp_int8_matmul_work(M, N,
+ *            K) bytes, 16-byte aligned.  Where that is not 0 (few tiles of C and a long K)
+ *            slices of K are multiplied side by side and added up in a second launch.
+ *            The result is the same with and without.
+ */
+int int8_matmul(const uint8_t *a_codes, const float *a_scales, const uint8_t *b_codes, const float *b_scales,
+                int64_t M, int64_t N, int64_t K, void *c, int ct, int64_t ldc, void *work, int64_t work_bytes,
+                void *stream);
+
+/* Bytes of scratch memory for int8_matmul, at most 4 MB; -1 for a negative or too large
+ * size.  Host only. */
+int64_t qcp_int8_matmul_work(int64_t M, int64_t N, int64_t K);
+
+/*
+ * Product of a 16-bit matrix with an INT8 payload over whose rows is summed, as a
+ * backward pass has them: c[m, n] = sum over k of a[m, k] * x[k, n], where x[k, n] is
+ * what int8_dequantize gives for the payload in a's type.  Accumulated in fp32, rounded
+ * once to ct.
+ *   a          transpose 0: M x K elements of type at (QCP_F16 or QCP_BF16), rows lda
+ *              apart; 1: its transpose, K x M.  lda <= 2^23
+ *   codes, scales   the payload of X, K rows of N codes; N <= 2^24
+ *   c          M x N of type ct, which is QCP_F32 or at (else QCP_EUNSUPPORTED), rows
+ *              ldc apart; K = 0 gives zeros
+ *   work       null, or scratch memory on the device of at least qcp_int8_mixed_work(M, N,
+ *              K) bytes, 16-byte aligned: slices of a long K side by side, added up in a
+ *              fixed order in a second launch.  The order of the sums, and with it their
+ *              last bits, differs from the product without.
+ * dx = dy W: a = dy, the payload of W [out, in].  dW = dy^T x: a = dy with transpose, the
+ * payload of x [tokens, in], which is all that a layer keeps of its input.
+ */
+int int8_matmul_mixed(const void *a, int at, int64_t lda, int32_t transpose, const uint8_t *codes,
+                      const float *scales, int64_t M, int64_t N, int64_t K, void *c, int ct, int64_t ldc,
+                      void *work, int64_t work_bytes, void *stream);
+
+/* Bytes of scratch memory for int8_matmul_mixed; -1 for a negative or too large size.
+ * Host only. */
+int64_t qcp_int8_mixed_work(int64_t M, int64_t N, int64_t K);
+
 /* Payload bytes of n codes at `bits` bits with one fp32 scale per G elements:
  * ceil(n*bits/8) + 4*ceil(n/G); -1 for invalid arguments.  Host only. */
 int64_t qcp_payload_bytes(int64_t n, int32_t bits, int32_t G);

@@ -22,6 +22,11 @@ Functions (same names as the C entry points):
     mxfp4_dequantize(codes, scales, cols, dtype)       -> y
     mxfp4_matmul(a_codes, a_scales, b_codes, b_scales, dtype) -> A B^T
     mxfp4_linear(x, weight)                            -> y (differentiable)
+    int8_quantize(x)                                   -> (codes, scales), one scale per row
+    int8_dequantize(codes, scales, cols, dtype)        -> y
+    int8_matmul(a_codes, a_scales, b_codes, b_scales, dtype) -> A B^T
+    int8_matmul_mixed(a, codes, scales, cols, transpose, dtype) -> A X, A in 16 bits, summed over X's rows
+    int8_linear(x, weight)                             -> y (differentiable, its input kept in 8 bits)
     payload_bytes(n, bits, G)
 """
 from __future__ import annotations
@@ -34,7 +39,8 @@ import torch
 __all__ = ["quantize_blockwise", "dequantize_blockwise", "pack_subbyte", "unpack_subbyte",
            "dequant_reduce_requant", "fp8_accum_requant", "payload_bytes", "code_bytes",
            "n_blocks", "AdamW", "adamw_step", "mxfp4_quantize", "mxfp4_quantize_both", "mxfp4_dequantize",
-           "mxfp4_matmul", "mxfp4_linear", "mxfp4_padded", "QcpError", "library", "FORMATS", "DTYPES", "LIB_PATH"]
+           "mxfp4_matmul", "mxfp4_linear", "mxfp4_padded", "int8_quantize", "int8_dequantize", "int8_matmul",
+           "int8_matmul_mixed", "int8_linear", "QcpError", "library", "FORMATS", "DTYPES", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqcp.so")
 
@@ -81,6 +87,10 @@ def library():
             "mxfp4_dequantize": [p, p, i64, i64, p, ci, i64, p],
             "mxfp4_matmul": [p, p, p, p, i64, i64, i64, p, ci, i64, p],
             "mxfp4_matmul_sliced": [p, p, p, p, i64, i64, i64, p, ci, i64, p, i64, p],
+            "int8_quantize": [p, ci, i64, i64, i64, p, p, p],
+            "int8_dequantize": [p, p, i64, i64, p, ci, i64, p],
+            "int8_matmul": [p, p, p, p, i64, i64, i64, p, ci, i64, p, i64, p],
+            "int8_matmul_mixed": [p, ci, i64, i32, p, p, i64, i64, i64, p, ci, i64, p, i64, p],
             "qcp_aquavit_level": [i64, i64, ctypes.c_double, ctypes.c_double,
                                   ctypes.POINTER(i32), ctypes.POINTER(i32)],
         }
@@ -96,6 +106,9 @@ def library():
         lib.qcp_mxfp4_padded.restype = i64
         lib.qcp_mxfp4_matmul_work.argtypes = [i64, i64, i64]
         lib.qcp_mxfp4_matmul_work.restype = i64
+        for name in ("qcp_int8_matmul_work", "qcp_int8_mixed_work"):
+            getattr(lib, name).argtypes = [i64, i64, i64]
+            getattr(lib, name).restype = i64
         lib.qcp_strerror.argtypes = [ci]
         lib.qcp_strerror.restype = ctypes.c_char_p
         lib.qcp_version.argtypes = []
@@ -415,4 +428,5 @@ def fp8_accum_requant(state_codes: torch.Tensor, state_scales: torch.Tensor, gra
 # these modules use the helpers above
 from .mxfp4 import (mxfp4_dequantize, mxfp4_linear, mxfp4_matmul, mxfp4_padded,  # noqa: E402
                     mxfp4_quantize, mxfp4_quantize_both)
+from .int8 import (int8_dequantize, int8_linear, int8_matmul, int8_matmul_mixed, int8_quantize)  # noqa: E402
 from .optimizer import AdamW, adamw_step  # noqa: E402

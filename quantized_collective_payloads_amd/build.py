@@ -25,10 +25,11 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["qcp_api.hip", "qcp_codec.hip", "qcp_reduce.hip", "qcp_ops_api.hip", "qcp_adamw.hip",
-           "qcp_mxfp4.hip", "qcp_mxfp4_matmul.hip"]
+           "qcp_mxfp4.hip", "qcp_mxfp4_matmul.hip", "qcp_int8.hip", "qcp_int8_matmul.hip", "qcp_int8_mixed.hip"]
 
 NO_NANS = ["-fno-honor-nans", "-mno-amdgpu-ieee"]
-HONOR_NANS = {"qcp_ops_api.hip", "qcp_adamw.hip", "qcp_mxfp4.hip", "qcp_mxfp4_matmul.hip"}
+HONOR_NANS = {"qcp_ops_api.hip", "qcp_adamw.hip", "qcp_mxfp4.hip", "qcp_mxfp4_matmul.hip", "qcp_int8.hip",
+              "qcp_int8_matmul.hip", "qcp_int8_mixed.hip"}
 
 CXXFLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

@@ -1,0 +1,467 @@
+// qcp_int8_matmul.hip -- C = A B^T on INT8 payloads with one scale per row: A is [M, K], B
+// is [N, K], both with K along their rows, C [M, N] in fp32, bf16 or fp16.
+//
+// c = sa sb sum(qa qb): v_mfma_i32_32x32x32_i8 and _16x16x64_i8 add up the products of codes
+// in 32-bit integers, exactly (the entry point bounds K so that no sum leaves them), whatever
+// the order; only then come the two scales, in fp32, and one rounding to C's type.
+// Which 16 of K a lane brings is free as long as both operands agree.
+#include <algorithm>
+
+#include "qcp_matmul.h"
+#include "qcp_ops.h"
+
+namespace qcp {
+
+namespace {
+
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+
+// Scales whose product, and whose product with any sum, is a normal number or a true
+// overflow: 0, or 2^-62 to 2^62
+__device__ __forceinline__ bool tame(float s) { return s == 0.0f || (s >= 0x1p-62f && s <= 0x1p62f); }
+
+// sum * sa * sb.  Outside the tame range the mantissas are multiplied and the exponents
+// added, so that nothing overflows or underflows on the way to a result that does not.
+template <bool TAME>
+__device__ __forceinline__ float scaled(int sum, float sa, float sb) {
+    if constexpr (TAME) return (float)sum * (sa * sb);
+    const float m = __builtin_amdgcn_frexp_mantf(sa) * __builtin_amdgcn_frexp_mantf(sb);
+    return __builtin_amdgcn_ldexpf((float)sum * m, __builtin_amdgcn_frexp_expf(sa) + __builtin_amdgcn_frexp_expf(sb));
+}
+
+// ---------------------------------------------------------------------------
+// 64*FM x 64*FN of C per work-group, staged through LDS.
+// ---------------------------------------------------------------------------
+// Four waves, 2 x 2, hold 32*FM x 32*FN each.  A stage is 128 bytes of each operand row,
+// whole cache lines, copied from memory to LDS without registers into one of `slots`; the
+// lower half-wave takes the first 64 bytes of its rows, the upper one the others.  A stage is
+// two phases; while a phase's products issue, the fragments of the next one are read, and in
+// the second the copies of a later stage go into the slot that the barrier between the two
+// has freed.  The order written is kept (sched_barrier).
+//
+// LDS holds a row's 8 pieces of 16 bytes in the order piece ^ (row / 2 % 8): the copy
+// permutes its source addresses, so that a fragment read, 16 rows of 128 bytes at the same
+// piece a cycle, touches each of the 64 banks once.
+//
+// A work-group walks several tiles: the copies of the next one's first stages, and of its
+// scales, go out before the results of this one.  Rows past the end repeat the last row.
+template <int FM, int FN> struct igeom {
+    static constexpr int TM = 64 * FM, TN = 64 * FN;       // C per work-group
+    static constexpr int slots = FM * FN == 1 ? 4 : 2;     // stages in LDS
+    static constexpr int rows = TM + TN;
+    static constexpr int slot = rows * 128;                // codes of A and B, one stage
+    static constexpr int marks = rows * 4;                 // scales of A and B, one tile
+    static constexpr int lds = slots * slot + 2 * marks;   // 132 KB at 4 x 4, 66 KB at 2 x 2, 65 KB at 1 x 1
+    static constexpr int ops = 2 * FM * FN;                // products per phase and wave
+    static constexpr int reads = 2 * (FM + FN);            // fragment pieces per phase
+    static constexpr int copies = rows / 32;               // per stage and wave, 8 rows each
+    static constexpr int waves_per_simd = FM * FN <= 4 ? 2 : 1;
+    // 16-byte stores of a wave's whole results
+    template <int CT> static constexpr int stores() { return FM * FN * 16 * dtype_traits<CT>::bytes / 16; }
+    static constexpr int ahead = (slots - 2) * copies;     // copies of stages beyond the next
+};
+
+template <int FM, int FN> struct IntFragments {
+    i32x4_t a[FM][2], b[FN][2];
+};
+
+__device__ __forceinline__ i32x4_t lds_codes(uint32_t at) { return __builtin_bit_cast(i32x4_t, lds16(at)); }
+
+// as copy_to_lds, 4 bytes a lane
+__device__ __forceinline__ void copy4_to_lds(uint32_t lds, uint32_t voff, i32x4_t rsrc) {
+    asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+                 :
+                 : "v"(voff), "s"(rsrc), "{m0}"(__builtin_amdgcn_readfirstlane((int)lds))
+                 : "memory");
+}
+
+// SLICED: the tiles are those of `slices` parts of K, one part after the other; c is int32,
+// an M x N for each, and the scales are left to the join.
+template <int FM, int FN, int CT, bool SLICED>
+__global__ __launch_bounds__(kThreads, (igeom<FM, FN>::waves_per_simd)) void k_int8_matmul_tiled(
+    const uint8_t *__restrict__ a, const float *__restrict__ as, const uint8_t *__restrict__ b,
+    const float *__restrict__ bs, int64_t M, int64_t N, uint32_t row_stages, uint32_t slices, uint32_t m_tiles,
+    uint32_t n_tiles, uint32_t groups, void *__restrict__ c, int64_t ldc) {
+    using Gm = igeom<FM, FN>;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[Gm::lds];
+    const int tid = (int)__builtin_amdgcn_workitem_id_x();
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = lane_id();
+
+    const uint32_t tiles = m_tiles * n_tiles * (SLICED ? slices : 1);
+    const uint32_t row_bytes = row_stages * 128;
+    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
+    constexpr uint32_t kMarks = Gm::slots * Gm::slot;      // where the scales begin
+    uint32_t stages = row_stages, slice = 0;               // of the tile
+
+    // the tile that is being copied: a wave brings a quarter of each operand's rows, 8 rows
+    // at a time
+    int64_t m0, n0;
+    i32x4_t ra, rb;
+    uint32_t m_rows, n_rows;
+    auto set_tile = [&](uint32_t t) __attribute__((always_inline)) {
+        uint32_t skip = 0;                                   // stages before the slice
+        if constexpr (SLICED) {
+            slice = t / (m_tiles * n_tiles);
+            t -= slice * (m_tiles * n_tiles);
+            const uint32_t each = row_stages / slices, over = row_stages % slices;
+            skip = slice * each + min(slice, over);
+            stages = each + (slice < over ? 1 : 0);
+        }
+        const TilePlace at = tile_place(t, m_tiles, n_tiles);
+        m0 = (int64_t)at.m * Gm::TM;
+        n0 = (int64_t)at.n * Gm::TN;
+        m_rows = (uint32_t)min(M - m0, (int64_t)Gm::TM);
+        n_rows = (uint32_t)min(N - n0, (int64_t)Gm::TN);
+        ra = buffer_of(a + m0 * row_bytes + skip * 128, (uint64_t)m_rows * row_bytes - skip * 128);
+        rb = buffer_of(b + n0 * row_bytes + skip * 128, (uint64_t)n_rows * row_bytes - skip * 128);
+    };
+    // the tile's scales, 64 rows a wave
+    auto copy_marks = [&](uint32_t to) __attribute__((always_inline)) {
+        if constexpr (SLICED) return;
+        if (wave < FM)
+            copy4_to_lds(to + wave * 256, min((uint32_t)(wave * 64 + lane), m_rows - 1) * 4,
+                         buffer_of(as + m0, (uint64_t)m_rows * 4));
+        if (wave < FN)
+            copy4_to_lds(to + Gm::TM * 4 + wave * 256, min((uint32_t)(wave * 64 + lane), n_rows - 1) * 4,
+                         buffer_of(bs + n0, (uint64_t)n_rows * 4));
+    };
+
+    // the n-th copy of a stage into the slot at `to`, from byte k of the rows
+    const uint32_t copy_row = lane >> 3, copy_piece = ((lane & 7) ^ (lane >> 4)) * 16;
+    auto copy = [&](auto I, uint32_t to, uint32_t k) __attribute__((always_inline)) {
+        constexpr int n = I;
+        constexpr bool of_a = n < 2 * FM;
+        constexpr int i = of_a ? n : n - 2 * FM, rows = 16 * (of_a ? FM : FN);   // this wave's rows begin at wave * rows
+        // three operations a copy instead of a register each (the asm keeps them from
+        // being made once): row < 2^8, row_bytes < 2^24
+        uint32_t row = copy_row;
+        asm volatile("" : "+v"(row));
+        row = min(wave * rows + i * 8 + row, (of_a ? m_rows : n_rows) - 1);
+        const uint32_t at = (row & 0xffu) * (row_bytes & 0xffffffu) + (copy_piece ^ (i & 1 ? 64 : 0));
+        copy_to_lds(to + (of_a ? 0 : Gm::TM * 128) + wave * rows * 128 + i * 1024, at, of_a ? ra : rb, k);
+    };
+    auto slot_of = [&](uint32_t s) __attribute__((always_inline)) { return (s & (Gm::slots - 1)) * Gm::slot; };
+    auto copy_stage = [&](uint32_t s) __attribute__((always_inline)) {
+        static_for<Gm::copies>([&](auto I) __attribute__((always_inline)) { copy(I, base + slot_of(s), s * 128); });
+    };
+
+    // fragments: wave w computes rows 32*FM*(w&1) of A against rows 32*FN*(w>>1) of B
+    const int r = lane & 31, half = lane >> 5, x = (lane >> 1) & 7;
+    const uint32_t arow = (wave & 1) * 32 * FM + r, brow = Gm::TM + (wave >> 1) * 32 * FN + r;
+    // where piece 4 * half of the first fragment lies in slot 0; pieces p and q of a row
+    // differ by the bits of 16 * (p ^ q)
+    const uint32_t a_at = base + arow * 128 + ((4 * half) ^ x) * 16;
+    const uint32_t b_at = base + brow * 128 + ((4 * half) ^ x) * 16;
+    // the n-th of the fragments' pieces at la, lb and those at the piece beside, in the
+    // order the products use them
+    using Frag = IntFragments<FM, FN>;
+    auto read = [&](auto I, uint32_t la, uint32_t lb, Frag &f) __attribute__((always_inline)) {
+        constexpr int n = I, u = n / (FM + FN), q = n % (FM + FN);
+        if constexpr (q < FN) f.b[q][u] = lds_codes((lb ^ (16 * u)) + q * 4096);
+        else f.a[q - FN][u] = lds_codes((la ^ (16 * u)) + (q - FN) * 4096);
+    };
+    // pieces p and p ^ 1 beyond 4 * half of the slot of stage s
+    auto read_all = [&](uint32_t s, uint32_t p, Frag &f) __attribute__((always_inline)) {
+        const uint32_t la = (a_at ^ (16 * p)) + slot_of(s), lb = (b_at ^ (16 * p)) + slot_of(s);
+        static_for<Gm::reads>([&](auto I) __attribute__((always_inline)) { read(I, la, lb, f); });
+    };
+
+    i32x16_t acc[FM][FN];
+    Frag f, h;
+    // the n-th product of a phase.  B first: a lane then holds 4 consecutive n of one m per
+    // group of registers
+    auto product = [&](auto I, const Frag &v) __attribute__((always_inline)) {
+        constexpr int n = I, u = n / (FM * FN), i = n / FN % FM, j = n % FN;
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(v.b[j][u], v.a[i][u], acc[i][j], 0, 0, 0);
+    };
+    auto products = [&](const Frag &v) __attribute__((always_inline)) {
+        static_for<Gm::ops>([&](auto I) __attribute__((always_inline)) { product(I, v); });
+    };
+    // the products of phase P of a stage, in the order written: between them the reads of the
+    // next phase's fragments, from the slot at `from`, and with COPY the copies of stage
+    // `next`, so the matrix cores never wait for the rest to issue.
+    auto phase = [&](auto P, const Frag &now, Frag &then, uint32_t from, auto COPY, uint32_t next)
+        __attribute__((always_inline)) {
+        constexpr int S = Gm::ops;
+        const uint32_t to = base + slot_of(next), k = next * 128;
+        uint32_t la = a_at, lb = b_at;
+        asm volatile("" : "+v"(la), "+v"(lb));   // addresses made here, not kept for every phase
+        la = (la ^ (P ? 0 : 32)) + from;
+        lb = (lb ^ (P ? 0 : 32)) + from;
+        static_for<S>([&](auto I) __attribute__((always_inline)) {
+            constexpr int n = I;
+            product(I, now);
+            // reads in the first half of the phase, copies too
+            constexpr int r0 = n * 2 * Gm::reads / S, r1 = (n + 1) * 2 * Gm::reads / S;
+            static_for<r1 - r0>([&](auto Q) __attribute__((always_inline)) {
+                constexpr int q = r0 + Q;
+                if constexpr (q < Gm::reads) read(std::integral_constant<int, q>{}, la, lb, then);
+            });
+            if constexpr (COPY) {
+                constexpr int c0 = n * 2 * Gm::copies / S, c1 = (n + 1) * 2 * Gm::copies / S;
+                static_for<c1 - c0>([&](auto Q) __attribute__((always_inline)) {
+                    constexpr int q = c0 + Q;
+                    if constexpr (q < Gm::copies) copy(std::integral_constant<int, q>{}, to, k);
+                });
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    using no = std::integral_constant<int, 0>;
+    using yes = std::integral_constant<int, 1>;
+
+    uint32_t turn = 0;                                       // which of the scales' two places
+    auto copy_first = [&]() __attribute__((always_inline)) {
+        copy_marks(base + kMarks + turn * Gm::marks);
+        static_for<Gm::slots>([&](auto Q) __attribute__((always_inline)) {
+            if ((uint32_t)Q < stages) copy_stage((uint32_t)Q);
+        });
+    };
+    uint32_t tile = __builtin_amdgcn_workgroup_id_x();
+    set_tile(tile);
+    copy_first();
+    wait_and_meet<0>();
+    for (;;) {
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+            for (int j = 0; j < FN; j++) acc[i][j] = i32x16_t{};
+        if (stages) read_all(0, 0, f);
+        uint32_t s = 0;
+        for (; s + Gm::slots < stages; s++) {
+            phase(no{}, f, h, slot_of(s), no{}, 0);
+            wait_and_meet<Gm::ahead>();
+            phase(yes{}, h, f, slot_of(s + 1), yes{}, s + Gm::slots);
+        }
+        for (; s < stages; s++) {
+            read_all(s, 2, h);
+            products(f);
+            wait_and_meet<0>();
+            products(h);
+            if (s + 1 < stages) read_all(s + 1, 0, f);
+        }
+
+        // the next tile's first copies go out before this one's results
+        const int64_t m_done = m0 + (wave & 1) * 32 * FM + r, n_done = n0 + (wave >> 1) * 32 * FN;
+        const bool whole = m0 + Gm::TM <= M && n0 + Gm::TN <= N;
+        void *const to = SLICED ? (int *)c + slice * M * N : c;
+        const uint32_t marks = base + kMarks + turn * Gm::marks;
+        tile += groups;
+        const bool more = tile < tiles;
+        if (more) {
+            wait_lds_and_meet();                             // every wave is done with the slots
+            set_tile(tile);
+            turn ^= 1;
+            copy_first();
+        }
+        if constexpr (SLICED) {
+            static_for<FM * FN>([&](auto I) __attribute__((always_inline)) {
+                constexpr int i = I / FN, j = I % FN;
+                store_fragment<F32>(__builtin_bit_cast(f32x16_t, acc[i][j]), to, ldc, m_done + 32 * i, n_done + 32 * j,
+                                    half, M, N, whole);
+            });
+        } else {
+            const uint32_t at_a = marks + arow * 4, at_b = marks + (brow - r + 4 * half) * 4;
+            float sa[FM];
+            bool ok = true;
+#pragma unroll
+            for (int i = 0; i < FM; i++) {
+                sa[i] = __uint_as_float(lds4(at_a + i * 128));
+                ok = ok && tame(sa[i]);
+            }
+            static_for<FN>([&](auto J) __attribute__((always_inline)) {
+                constexpr int j = J;
+                float sb[16];
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    const u32x4_t w = lds16(at_b + j * 128 + q * 32);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        sb[4 * q + e] = __uint_as_float(w[e]);
+                        ok = ok && tame(sb[4 * q + e]);
+                    }
+                }
+                auto put = [&](auto T) __attribute__((always_inline)) {
+                    static_for<FM>([&](auto I) __attribute__((always_inline)) {
+                        constexpr int i = I;
+                        f32x16_t v;
+#pragma unroll
+                        for (int e = 0; e < 16; e++) v[e] = scaled<T>(acc[i][j][e], sa[i], sb[e]);
+                        store_fragment<CT>(v, to, ldc, m_done + 32 * i, n_done + 32 * j, half, M, N, whole);
+                    });
+                };
+                if (__all(ok)) put(yes{});
+                else put(no{});
+            });
+        }
+        if (!more) break;
+        // the copies are older than the stores, of which a whole tile has `stores` at least
+        constexpr int stores = SLICED ? Gm::template stores<F32>() : Gm::template stores<CT>();
+        if (whole) wait_and_meet<(stores < 63 ? stores : 63)>();
+        else wait_and_meet<0>();
+    }
+}
+
+template <int FM, int FN, int CT, bool SLICED = false>
+hipError_t run_tiled(const uint8_t *a, const float *as, const uint8_t *b, const float *bs, int64_t M, int64_t N,
+                     int64_t stages, void *c, int64_t ldc, hipStream_t st, int slices = 1) {
+    using Gm = igeom<FM, FN>;
+    const int64_t mt = (M + Gm::TM - 1) / Gm::TM, nt = (N + Gm::TN - 1) / Gm::TN;
+    // as many work-groups as the GPU holds walk the tiles (a multiple of 8, so that each
+    // stays on its XCD's tiles)
+    const unsigned groups = (unsigned)std::min<int64_t>(mt * nt * slices, kCUs * Gm::waves_per_simd);
+    hipLaunchKernelGGL((k_int8_matmul_tiled<FM, FN, CT, SLICED>), dim3(groups), dim3(kThreads), 0, st, a, as, b, bs, M,
+                       N, (uint32_t)stages, (uint32_t)slices, (uint32_t)mt, (uint32_t)nt, groups, c, ldc);
+    return hipGetLastError();
+}
+
+// The sum of the slices, and the scales: 4 columns a lane.
+template <int CT>
+__global__ __launch_bounds__(kThreads) void k_int8_matmul_join(const int *__restrict__ parts, int slices,
+                                                               const float *__restrict__ as,
+                                                               const float *__restrict__ bs, int64_t M, int64_t N,
+                                                               void *__restrict__ c, int64_t ldc) {
+    const int64_t m = group_y();
+    const int64_t n = ((int64_t)__builtin_amdgcn_workgroup_id_x() * kThreads + __builtin_amdgcn_workitem_id_x()) * 4;
+    if (n >= N) return;
+    const int count = N - n < 4 ? (int)(N - n) : 4;
+    const int *p = parts + m * N + n;
+    int sum[4] = {};
+    for (int s = 0; s < slices; s++, p += M * N) {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (j < count) sum[j] += p[j];
+    }
+    const float sa = as[m];
+    float v[4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        if (j < count) v[j] = scaled<false>(sum[j], sa, bs[n + j]);
+    store4<CT>(c, m * ldc + n, count, v);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows of A (a token, a small batch): 16*FA rows against 16*FB rows of B.
+// ---------------------------------------------------------------------------
+// Bound: reading B once.  N/16 work-groups; the WV waves of one deal out K in steps of 256
+// bytes and add their sums in LDS, so a few rows still fill the GPU, without a second
+// launch.  A quarter-wave takes 64 of a step's bytes of its rows, a lane 64 consecutive ones.
+// Operands go straight to registers, a whole step's loads at a time.
+template <int F> struct IntStep {
+    i32x4_t v[F][4];
+};
+
+template <int FA, int FB, int WV, int CT>
+__global__ __launch_bounds__(64 * WV) void k_int8_matmul_rows(
+    const uint8_t *__restrict__ a, const float *__restrict__ as, const uint8_t *__restrict__ b,
+    const float *__restrict__ bs, int64_t M, int64_t N, int64_t granules, void *__restrict__ c, int64_t ldc) {
+    __shared__ i32x4_t sums[WV][FA * FB][64];
+    const int wave = __builtin_amdgcn_readfirstlane((int)(__builtin_amdgcn_workitem_id_x() >> 6)), lane = lane_id();
+    const int row = lane & 15, quarter = lane >> 4;
+    const int64_t n0 = (int64_t)__builtin_amdgcn_workgroup_id_x() * (16 * FB), m0 = group_y() * (16 * FA);
+    const uint8_t *pa[FA], *pb[FB];
+#pragma unroll
+    for (int i = 0; i < FA; i++) pa[i] = a + (min(m0 + 16 * i + row, M - 1) * granules + quarter) * 64;
+#pragma unroll
+    for (int i = 0; i < FB; i++) pb[i] = b + (min(n0 + 16 * i + row, N - 1) * granules + quarter) * 64;
+    auto load = [&](int64_t g, auto &f, const uint8_t *const *p, auto F) __attribute__((always_inline)) {
+        static_for<F>([&](auto I) __attribute__((always_inline)) {
+            constexpr int i = I;
+            const bool inside = g + quarter < granules;
+#pragma unroll
+            for (int t = 0; t < 4; t++)
+                f.v[i][t] = inside ? *(const i32x4_t *)(p[i] + g * 64 + 16 * t) : i32x4_t{0, 0, 0, 0};
+        });
+    };
+    i32x4_t acc[FA][FB] = {};
+    for (int64_t g = 4 * wave; g < granules; g += 4 * WV) {
+        IntStep<FA> fa;
+        IntStep<FB> fb;
+        load(g, fb, pb, std::integral_constant<int, FB>{});
+        load(g, fa, pa, std::integral_constant<int, FA>{});
+#pragma unroll
+        for (int t = 0; t < 4; t++)
+#pragma unroll
+            for (int i = 0; i < FA; i++)
+#pragma unroll
+                for (int j = 0; j < FB; j++)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb.v[j][t], fa.v[i][t], acc[i][j], 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < FA; i++)
+#pragma unroll
+        for (int j = 0; j < FB; j++) sums[wave][i * FB + j][lane] = acc[i][j];
+    __syncthreads();
+    // a lane's 4 sums are consecutive n of one m
+    for (int k = wave; k < FA * FB; k += WV) {
+        i32x4_t v = sums[0][k][lane];
+#pragma unroll
+        for (int w = 1; w < WV; w++) v += sums[w][k][lane];
+        const int64_t m = m0 + 16 * (k / FB) + row, n = n0 + 16 * (k % FB) + 4 * quarter;
+        if (m >= M || n >= N) continue;
+        const int count = N - n < 4 ? (int)(N - n) : 4;
+        const float sa = as[m];
+        float r[4] = {};
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (j < count) r[j] = scaled<false>(v[j], sa, bs[n + j]);
+        store4<CT>(c, m * ldc + n, count, r);
+    }
+}
+
+template <int FA, int FB, int CT>
+hipError_t run_rows(const uint8_t *a, const float *as, const uint8_t *b, const float *bs, int64_t M, int64_t N,
+                    int64_t granules, void *c, int64_t ldc, hipStream_t st) {
+    const dim3 grid((unsigned)((N + 16 * FB - 1) / (16 * FB)), (unsigned)((M + 16 * FA - 1) / (16 * FA)));
+    if (granules <= 16)
+        hipLaunchKernelGGL((k_int8_matmul_rows<FA, FB, 4, CT>), grid, dim3(256), 0, st, a, as, b, bs, M, N, granules, c, ldc);
+    else
+        hipLaunchKernelGGL((k_int8_matmul_rows<FA, FB, 8, CT>), grid, dim3(512), 0, st, a, as, b, bs, M, N, granules, c, ldc);
+    return hipGetLastError();
+}
+
+template <int CT>
+hipError_t run_matmul(const uint8_t *a, const float *as, const uint8_t *b, const float *bs, int64_t M, int64_t N,
+                      int64_t stages, void *c, int64_t ldc, int *work, hipStream_t st) {
+    const int slices = work ? int8_matmul_slices(M, N, stages) : 1;
+    if (slices > 1) {
+        const hipError_t e = run_tiled<1, 1, F32, true>(a, as, b, bs, M, N, stages, work, N, st, slices);
+        if (e != hipSuccess) return e;
+        const dim3 grid((unsigned)((N + 4 * kThreads - 1) / (4 * kThreads)), (unsigned)M);
+        hipLaunchKernelGGL((k_int8_matmul_join<CT>), grid, dim3(kThreads), 0, st, work, slices, as, bs, M, N, c, ldc);
+        return hipGetLastError();
+    }
+    const auto tiles = [&](int64_t m, int64_t n) { return ((M + m - 1) / m) * ((N + n - 1) / n); };
+    const int64_t small = tiles(64, 64), middle = tiles(128, 128), large = tiles(256, 256), granules = 2 * stages;
+    const bool rows = (N + 15) / 16 <= kMaxGroups / 2;
+    if (rows && M <= 16) return run_rows<1, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
+    if (rows && M <= 32 && small < 128) return run_rows<2, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
+    if (rows && small <= 64 && granules <= 32) return run_rows<4, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
+    if (small <= 512) return run_tiled<1, 1, CT>(a, as, b, bs, M, N, stages, c, ldc, st);
+    if ((middle + 511) / 512 * (27 * stages + 70) < (large + 255) / 256 * (41 * stages + 220))
+        return run_tiled<2, 2, CT>(a, as, b, bs, M, N, stages, c, ldc, st);
+    return run_tiled<4, 4, CT>(a, as, b, bs, M, N, stages, c, ldc, st);
+}
+
+}  // namespace
+
+// A long K and too few tiles for the GPU: slices of K, each a share of the work-groups,
+// added up in a second launch.
+int int8_matmul_slices(int64_t M, int64_t N, int64_t stages) {
+    const int64_t rows = (M + 63) / 64, cols = (N + 63) / 64;
+    if (M <= 16 || N < 1 || rows > 128 || cols > 128 || rows * cols > 128) return 1;
+    if (stages < (M <= 32 ? 64 : rows * cols < 48 ? 48 : 32)) return 1;
+    return (int)std::min<int64_t>(8, 256 / (rows * cols));
+}
+
+hipError_t launch_int8_matmul(const uint8_t *a, const float *as, const uint8_t *b, const float *bs, int64_t M,
+                              int64_t N, int64_t stages, void *c, int ct, int64_t ldc, int *work, hipStream_t st) {
+    switch (ct) {
+    case F16: return run_matmul<F16>(a, as, b, bs, M, N, stages, c, ldc, work, st);
+    case BF16: return run_matmul<BF16>(a, as, b, bs, M, N, stages, c, ldc, work, st);
+    case F32: return run_matmul<F32>(a, as, b, bs, M, N, stages, c, ldc, work, st);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace qcp

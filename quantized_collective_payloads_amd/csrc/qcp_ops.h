@@ -1,4 +1,4 @@
-// qcp_ops.h -- internal launchers of the optimizer step and of the MXFP4 payload.
+// qcp_ops.h -- internal launchers of the optimizer step and of the MXFP4 and INT8 payloads.
 // As in qcp_launch.h, arguments are already validated by the caller (qcp_ops_api.hip).
 #pragma once
 
@@ -44,6 +44,25 @@ int mx_matmul_slices(int64_t M, int64_t N, int64_t granules);
 hipError_t launch_mx_matmul(const uint8_t *a, const uint8_t *as, const uint8_t *b, const uint8_t *bs,
                             int64_t M, int64_t N, int64_t granules, void *c, int ct, int64_t ldc,
                             float *work, hipStream_t st);
+
+// the INT8 payload of x with one scale per row, and back; see qcp_int8.hip
+hipError_t launch_int8_quantize(const void *x, int xt, int64_t rows, int64_t cols, int64_t ld, uint8_t *codes,
+                                float *scales, hipStream_t st);
+hipError_t launch_int8_dequantize(const uint8_t *codes, const float *scales, int64_t rows, int64_t cols, void *y,
+                                  int yt, int64_t ld, hipStream_t st);
+
+// C[M, N] = A B^T, rows of `stages` times 128 codes; see qcp_int8_matmul.hip.
+// work: null, or room for slices * M * N integers, slices of K as many as said here
+int int8_matmul_slices(int64_t M, int64_t N, int64_t stages);
+hipError_t launch_int8_matmul(const uint8_t *a, const float *as, const uint8_t *b, const float *bs, int64_t M,
+                              int64_t N, int64_t stages, void *c, int ct, int64_t ldc, int *work, hipStream_t st);
+
+// C[M, N] = A X for a 16-bit A (transpose: given as [K, M]) and the payload of X [K, N];
+// see qcp_int8_mixed.hip.  work: null, or room for slices * M * N floats
+int int8_mixed_slices(int64_t M, int64_t N, int64_t K);
+hipError_t launch_int8_mixed(const void *a, int at, int64_t lda, int transpose, const uint8_t *codes,
+                             const float *scales, int64_t M, int64_t N, int64_t K, void *c, int ct, int64_t ldc,
+                             float *work, hipStream_t st);
 
 // the counter hash of the stochastic rounding: an invertible scramble of 32 bits
 // (two rounds of xor-shift and an odd multiplier, the fractions of sqrt 2 and sqrt 3)

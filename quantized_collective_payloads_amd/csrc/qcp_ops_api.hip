@@ -1,9 +1,9 @@
 // qcp_ops_api.hip -- the extern "C" entry points of the optimizer step and of the
-// MXFP4 payload (include/qcp.h).
+// MXFP4 and INT8 payloads and their products (include/qcp.h).
 //
 // As in qcp_api.hip: each validates its arguments on the host (no HIP call is made for
 // a rejected call or one without work), enqueues on the caller's stream (one kernel;
-// adamw_step one per 64 tensors, the sliced product two) and maps a launch error to
+// adamw_step one per 64 tensors, a sliced product two) and maps a launch error to
 // QCP_EHIP.  Nothing is allocated on the device and no state is kept between calls.
 #include <math.h>
 #include <stdint.h>
@@ -71,6 +71,15 @@ bool mx_payload(int64_t lines, int64_t n, int64_t *pad) {
     *pad = (n + 127) / 128 * 128;
     return *pad == 0 || (n <= (int64_t)1 << 31 && lines <= kMaxElems / *pad);
 }
+
+// an INT8 payload of `lines` rows of n codes: the padded row length.  As above, positions
+// within a row are 32 bits.
+bool int8_payload(int64_t lines, int64_t n, int64_t *pad) { return mx_payload(lines, n, pad); }
+
+// sums of products of codes stay within 32 bits: 130944 * 128 * 128 < 2^31
+constexpr int64_t kInt8MaxK = 130944;
+// the mixed product: 128 rows of the payload and 256 of a, in bytes, are 32-bit offsets
+constexpr int64_t kMixedMaxN = (int64_t)1 << 24, kMixedMaxLd = (int64_t)1 << 23;
 
 // The arguments that adamw_step checks, by their names there
 struct AdamwArgs {
@@ -307,5 +316,99 @@ int64_t qcp_mxfp4_matmul_work(int64_t M, int64_t N, int64_t K) {
 }
 
 int64_t qcp_mxfp4_padded(int64_t n) { return n < 0 || n > kMaxElems ? -1 : (n + 127) / 128 * 128; }
+
+int int8_quantize(const void *x, int xt, int64_t rows, int64_t cols, int64_t ld, uint8_t *codes, float *scales,
+                  void *stream) {
+    int64_t xb, pad;
+    int rc = check_matrix(rows, cols, ld, xt, &xb);
+    if (rc != QCP_OK) return rc;
+    if (rows == 0) return QCP_OK;
+    if (!int8_payload(rows, cols, &pad)) return QCP_EINVAL;
+    if (!scales || (cols > 0 && (!x || !codes))) return QCP_EINVAL;
+    if ((uintptr_t)x % dtype_bytes(xt) || !aligned16(codes) || !aligned16(scales)) return QCP_EALIGN;
+    if (overlap(x, xb, codes, rows * pad) || overlap(x, xb, scales, rows * 4) ||
+        overlap(codes, rows * pad, scales, rows * 4))
+        return QCP_EINVAL;
+    return status_of(qcp::launch_int8_quantize(x, xt, rows, cols, ld, codes, scales, (hipStream_t)stream));
+}
+
+int int8_dequantize(const uint8_t *codes, const float *scales, int64_t rows, int64_t cols, void *y, int yt,
+                    int64_t ld, void *stream) {
+    int64_t yb, pad;
+    int rc = check_matrix(rows, cols, ld, yt, &yb);
+    if (rc != QCP_OK) return rc;
+    if (rows == 0 || cols == 0) return QCP_OK;
+    if (!int8_payload(rows, cols, &pad)) return QCP_EINVAL;
+    if (!codes || !scales || !y) return QCP_EINVAL;
+    if (!aligned16(codes) || !aligned16(scales) || (uintptr_t)y % dtype_bytes(yt)) return QCP_EALIGN;
+    if (overlap(y, yb, codes, rows * pad) || overlap(y, yb, scales, rows * 4)) return QCP_EINVAL;
+    return status_of(qcp::launch_int8_dequantize(codes, scales, rows, cols, y, yt, ld, (hipStream_t)stream));
+}
+
+int int8_matmul(const uint8_t *a_codes, const float *a_scales, const uint8_t *b_codes, const float *b_scales,
+                int64_t M, int64_t N, int64_t K, void *c, int ct, int64_t ldc, void *work, int64_t work_bytes,
+                void *stream) {
+    int64_t cb, pad;
+    int rc = check_matrix(M, N, ldc, ct, &cb);
+    if (rc != QCP_OK) return rc;
+    if (K < 0 || K > kInt8MaxK) return QCP_EINVAL;
+    if (M == 0 || N == 0) return QCP_OK;
+    if (!int8_payload(M, K, &pad) || !int8_payload(N, K, &pad)) return QCP_EINVAL;
+    if ((M + 127) / 128 > qcp::kMaxGroups / ((N + 127) / 128)) return QCP_EINVAL;   // tiles of C
+    if (!c || !a_scales || !b_scales || (K > 0 && (!a_codes || !b_codes))) return QCP_EINVAL;
+    const int64_t need = work ? qcp_int8_matmul_work(M, N, K) : 0;
+    if (work_bytes < need) return QCP_EINVAL;
+    if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(b_codes) || !aligned16(b_scales) ||
+        !aligned16(work) || (uintptr_t)c % dtype_bytes(ct))
+        return QCP_EALIGN;
+    const void *in[4] = {a_codes, a_scales, b_codes, b_scales};
+    const int64_t bytes[4] = {M * pad, M * 4, N * pad, N * 4};
+    if (overlap(c, cb, work, need)) return QCP_EINVAL;
+    for (int i = 0; i < 4; i++)
+        if (overlap(c, cb, in[i], bytes[i]) || overlap(work, need, in[i], bytes[i])) return QCP_EINVAL;
+    return status_of(qcp::launch_int8_matmul(a_codes, a_scales, b_codes, b_scales, M, N, pad / 128, c, ct, ldc,
+                                             need ? (int *)work : nullptr, (hipStream_t)stream));
+}
+
+int64_t qcp_int8_matmul_work(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0 || M > kMaxElems || N > kMaxElems || K > kInt8MaxK) return -1;
+    const int slices = qcp::int8_matmul_slices(M, N, (K + 127) / 128);
+    return slices > 1 ? 4 * slices * M * N : 0;
+}
+
+int int8_matmul_mixed(const void *a, int at, int64_t lda, int32_t transpose, const uint8_t *codes,
+                      const float *scales, int64_t M, int64_t N, int64_t K, void *c, int ct, int64_t ldc,
+                      void *work, int64_t work_bytes, void *stream) {
+    int64_t ab, cb, pad;
+    if (transpose != 0 && transpose != 1) return QCP_EINVAL;
+    if (at != QCP_F16 && at != QCP_BF16) return QCP_EINVAL;
+    if (valid_dtype(ct) && ct != QCP_F32 && ct != at) return QCP_EUNSUPPORTED;
+    int rc = transpose ? check_matrix(K, M, lda, at, &ab) : check_matrix(M, K, lda, at, &ab);
+    if (rc != QCP_OK) return rc;
+    rc = check_matrix(M, N, ldc, ct, &cb);
+    if (rc != QCP_OK) return rc;
+    if (M == 0 || N == 0) return QCP_OK;
+    if (N > kMixedMaxN || lda > kMixedMaxLd || !int8_payload(K, N, &pad)) return QCP_EINVAL;
+    if ((M + 255) / 256 > qcp::kMaxGroups / 2 / ((N + 255) / 256)) return QCP_EINVAL;   // tiles of C
+    if (!c || (K > 0 && (!a || !codes || !scales))) return QCP_EINVAL;
+    const int64_t need = work ? qcp_int8_mixed_work(M, N, K) : 0;
+    if (work_bytes < need) return QCP_EINVAL;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(work) || (uintptr_t)a % 2 ||
+        (uintptr_t)c % dtype_bytes(ct))
+        return QCP_EALIGN;
+    const void *in[3] = {a, codes, scales};
+    const int64_t bytes[3] = {ab, K * pad, K * 4};
+    if (overlap(c, cb, work, need)) return QCP_EINVAL;
+    for (int i = 0; i < 3; i++)
+        if (overlap(c, cb, in[i], bytes[i]) || overlap(work, need, in[i], bytes[i])) return QCP_EINVAL;
+    return status_of(qcp::launch_int8_mixed(a, at, lda, transpose, codes, scales, M, N, K, c, ct, ldc,
+                                            need ? (float *)work : nullptr, (hipStream_t)stream));
+}
+
+int64_t qcp_int8_mixed_work(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0 || M > kMaxElems || N > kMaxElems || K > kMaxElems) return -1;
+    const int slices = qcp::int8_mixed_slices(M, N, K);
+    return slices > 1 ? 4 * slices * M * N : 0;
+}
 
 }  // extern "C"

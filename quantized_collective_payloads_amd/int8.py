@@ -1,0 +1,284 @@
+"""The INT8 payload with one scale per row (a token, an output channel), its products
+on the matrix cores, and a linear layer that keeps its input in 8 bits for the
+backward pass (int8_* of include/qcp.h).
+
+A payload of `rows` rows of n values is a pair (codes, scales): uint8 [rows, P] in
+two's complement, with P = n rounded up to whole 128s, and float32 [rows].
+
+As in mxfp4.py, each function first asks what every valid call answers with yes and
+goes through the checks that name the fault only where the answer is no.
+"""
+from __future__ import annotations
+
+import torch
+from torch.autograd.forward_ad import unpack_dual
+
+from . import DTYPES, _dev, _enqueue, _F32, _need, _U8, library
+from .mxfp4 import _matrix, _pad, _result, _same_gpu
+
+_u8, _f32 = torch.uint8, torch.float32
+_HALF = (torch.float16, torch.bfloat16)
+
+
+def _payload(codes, scales, what: str):
+    """(rows, padded row length, GPU) of a payload after checking its two tensors;
+    the GPU is -1 for CPU tensors."""
+    try:
+        (rows, P), shape, index = codes.shape, scales.shape, codes.get_device()
+        if (codes.dtype is _u8 and scales.dtype is _f32 and P % 128 == 0 and shape == (rows,)
+                and index == scales.get_device() and codes.is_contiguous() and scales.is_contiguous()):
+            return rows, P, index
+    except (AttributeError, ValueError):
+        pass
+    _need(codes, f"{what}codes", _U8, 0)
+    _need(scales, f"{what}scales", _F32, 0)
+    if codes.dim() != 2:
+        raise ValueError(f"{what}codes: {codes.dim()} dimensions, expected 2")
+    if codes.shape[1] % 128:
+        raise ValueError(f"{what}codes: rows of {codes.shape[1]} bytes, expected a multiple of 128")
+    if tuple(scales.shape) != (codes.shape[0],):
+        raise ValueError(f"{what}scales: shape {tuple(scales.shape)} for codes of {tuple(codes.shape)}, "
+                         f"expected {(codes.shape[0],)}")
+    _dev(codes, scales)
+    raise ValueError(f"{what}codes: not a payload")
+
+
+def _columns(P: int, cols: int):
+    if cols < 0 or _pad(cols) != P:
+        raise ValueError(f"codes: rows of {P} values for {cols} columns")
+
+
+def _rows_of(x):
+    """x with its elements side by side along rows that do not overlap, and how far
+    apart they are."""
+    rows, cols = x.shape
+    if x.is_contiguous():
+        return x, cols
+    if x.stride(1) == 1 and (x.stride(0) >= cols or rows == 1):
+        return x, x.stride(0) if rows > 1 else cols
+    return x.contiguous(), cols
+
+
+def int8_quantize(x: torch.Tensor, codes=None, scales=None):
+    """The payload (codes, scales) of a 2-D fp16/bf16/fp32 GPU tensor.  Rows may lie any
+    distance apart; other strides are copied first.  Caller-supplied `codes` (uint8) and
+    `scales` (float32) must be contiguous and of the payload's shape."""
+    if type(x) is not torch.Tensor or x.dim() != 2 or x.dtype not in DTYPES:
+        _matrix(x, "x")
+    rows, cols = x.shape
+    x, ld = _rows_of(x)
+    P, index = _pad(cols), x.get_device()
+    for t, what, kinds, shape in ((codes, "codes", _U8, (rows, P)), (scales, "scales", _F32, (rows,))):
+        if t is not None:
+            _need(t, what, kinds, 0)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
+            _same_gpu(index, x, t)
+    if index < 0:
+        _dev(x)
+    if codes is None:
+        codes = x.new_empty((rows, P), dtype=_u8)
+    if scales is None:
+        scales = x.new_empty(rows, dtype=_f32)
+    _enqueue("int8_quantize", index, x.data_ptr(), DTYPES[x.dtype], rows, cols, ld, codes.data_ptr(),
+             scales.data_ptr())
+    return codes, scales
+
+
+def int8_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int, dtype=torch.bfloat16, out=None):
+    """The [rows, cols] values that a payload stands for, rounded once to `dtype`."""
+    rows, P, index = _payload(codes, scales, "")
+    _columns(P, cols)
+    y = _result(out, rows, cols, dtype, codes)
+    if index < 0 or out is not None:
+        _same_gpu(index, codes, y)
+    _enqueue("int8_dequantize", index, codes.data_ptr(), scales.data_ptr(), rows, cols, y.data_ptr(),
+             DTYPES[y.dtype], cols)
+    return y
+
+
+def int8_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor, b_scales: torch.Tensor,
+                dtype=torch.bfloat16, out=None):
+    """A B^T for the payloads of A [M, K] and B [N, K]: [M, N] in `dtype`.  The sums over K
+    (up to 130944) are exact."""
+    M, K, index = _payload(a_codes, a_scales, "a_")
+    N, Kb, other = _payload(b_codes, b_scales, "b_")
+    if K != Kb:
+        raise ValueError(f"b_codes: rows of {Kb} values, a_codes of {K}")
+    c = _result(out, M, N, dtype, a_codes)
+    if index < 0 or index != other or out is not None:
+        _same_gpu(index, a_codes, b_codes, c)
+    _multiply(index, a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(), M, N, K, c)
+    return c
+
+
+def _scratch(name: str, like, *sizes):
+    """(scratch memory or None, its address, its bytes) for a product."""
+    work = getattr(library(), name)(*sizes)
+    if work <= 0:
+        return None, None, 0
+    t = like.new_empty(work, dtype=_u8)
+    return t, t.data_ptr(), work
+
+
+def _multiply(index, a, sa, b, sb, M, N, K, c):
+    t, at, size = _scratch("qcp_int8_matmul_work", c, M, N, K)
+    _enqueue("int8_matmul", index, a, sa, b, sb, M, N, K, c.data_ptr(), DTYPES[c.dtype], N, at, size)
+
+
+def int8_matmul_mixed(a: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, cols: int,
+                      transpose: bool = False, dtype=None, out=None):
+    """A X for a 2-D fp16 or bf16 tensor A [M, K] (with `transpose`, `a` is [K, M] and A its
+    transpose) and the payload of X [K, cols], read in a's type: [M, cols] in `dtype`,
+    which is a's (the default) or float32, accumulated in fp32.  Rows of `a` may lie any
+    distance apart, and a transposed view is read where it is; other strides are copied."""
+    if type(a) is not torch.Tensor or a.dim() != 2 or a.dtype not in _HALF:
+        _matrix(a, "a")
+        if a.dtype not in _HALF:
+            raise ValueError(f"a: dtype {a.dtype}, expected {' or '.join(map(str, _HALF))}")
+    K, P, index = _payload(codes, scales, "")
+    _columns(P, cols)
+    M = a.shape[1 if transpose else 0]
+    if a.shape[0 if transpose else 1] != K:
+        raise ValueError(f"a: shape {tuple(a.shape)}{' (transposed)' if transpose else ''} for a payload of {K} rows")
+    dtype = (a.dtype if dtype is None else dtype) if out is None else out.dtype
+    if dtype not in (a.dtype, _f32):
+        raise ValueError(f"dtype {dtype}, expected {a.dtype} or {_f32}")
+    c = _result(out, M, cols, dtype, codes)
+    _same_gpu(index, codes, a, c)
+    _mixed(index, a, codes.data_ptr(), scales.data_ptr(), M, cols, K, transpose, c)
+    return c
+
+
+def _mixed(index, a, codes, scales, M, N, K, transpose, c):
+    if not a.is_contiguous() and a.stride(0) == 1 and a.stride(1) >= a.shape[0]:
+        a, transpose = a.t(), not transpose
+    a, lda = _rows_of(a)
+    t, at, size = _scratch("qcp_int8_mixed_work", c, M, N, K)
+    _enqueue("int8_matmul_mixed", index, a.data_ptr(), DTYPES[a.dtype], lda, 1 if transpose else 0, codes, scales,
+             M, N, K, c.data_ptr(), DTYPES[c.dtype], N, at, size)
+
+
+def _quantized(index, x):
+    """The payload of a contiguous matrix in one buffer: its codes, then its scales."""
+    rows, cols = x.shape
+    buffer = x.new_empty(rows * (_pad(cols) + 4), dtype=_u8)
+    _enqueue("int8_quantize", index, x.data_ptr(), DTYPES[x.dtype], rows, cols, cols, *_at(buffer, rows, cols))
+    return buffer
+
+
+def _at(buffer, rows, cols):
+    base = buffer.data_ptr()
+    return base, base + rows * _pad(cols)
+
+
+def _product(index, x, qx, w, O):
+    """The product of x's payload, held in qx, and that at the addresses w."""
+    T, I = x.shape
+    y = x.new_empty((T, O))
+    _multiply(index, *_at(qx, T, I), *w, T, O, _pad(I), y)
+    return y
+
+
+def _backward(index, dy, payload, rows, cols, transpose, dtype):
+    """dy times a payload, or its transpose times it, in `dtype`."""
+    M = dy.shape[1 if transpose else 0]
+    c = dy.new_empty((M, cols), dtype=dtype if dtype in (dy.dtype, _f32) else _f32)
+    _mixed(index, dy, *payload, M, cols, rows, transpose, c)
+    return c if c.dtype is dtype else c.to(dtype)
+
+
+class _Linear(torch.autograd.Function):
+    """y = Q(x) Q(w)^T.  The payload of x, which the forward product needs, is also all that
+    is kept of x: 8 bits a value.  The backward products read it and that of w as they
+    are: dx = dy Q(w), dw = dy^T Q(x), the gradients of the product with the rounding
+    passed straight through."""
+
+    @staticmethod
+    def forward(ctx, x, w):
+        index, (T, I), O = x.get_device(), x.shape, w.shape[0]
+        need_x, need_w = ctx.needs_input_grad
+        qx, qw = _quantized(index, x), _quantized(index, w)
+        y = _product(index, x, qx, _at(qw, O, I), O)
+        ctx.save_for_backward(qx if need_w else None, qw if need_x else None)
+        ctx.sizes, ctx.kinds = (T, I, O), (x.dtype, w.dtype)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        qx, qw = ctx.saved_tensors
+        T, I, O = ctx.sizes
+        index, dx, dw = dy.get_device(), None, None
+        if qw is not None:
+            dx = _backward(index, dy, _at(qw, O, I), O, I, False, ctx.kinds[0])
+        if qx is not None:
+            dw = _backward(index, dy, _at(qx, T, I), T, I, True, ctx.kinds[1])
+        return dx, dw
+
+
+class _FrozenLinear(torch.autograd.Function):
+    """The same on a weight that is a payload: a gradient for x alone, and nothing of x is kept."""
+
+    @staticmethod
+    def forward(ctx, x, codes, scales):
+        index, O = x.get_device(), codes.shape[0]
+        y = _product(index, x, _quantized(index, x), (codes.data_ptr(), scales.data_ptr()), O)
+        ctx.save_for_backward(codes, scales)
+        ctx.sizes = (x.shape[1], O)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        codes, scales = ctx.saved_tensors
+        I, O = ctx.sizes
+        dx = _backward(dy.get_device(), dy, (codes.data_ptr(), scales.data_ptr()), O, I, False, dy.dtype)
+        return dx, None, None
+
+
+def int8_linear(x: torch.Tensor, weight) -> torch.Tensor:
+    """x [..., in] (fp16 or bf16) times weight [out, in] transposed, in x's type, with x
+    rounded to INT8 by tokens and the weight by output channels.
+
+    weight   a 2-D fp16/bf16/fp32 tensor, quantized at every call; or a payload (codes,
+             scales) of int8_quantize, made once (serving, frozen weights)
+
+    Differentiable in x and in a weight tensor, backwards, with the rounding passed
+    straight through: of x only the 8-bit payload is kept, and the backward products read it
+    (and the weight's) in the gradient's type.  A forward-mode tangent raises
+    NotImplementedError."""
+    frozen = isinstance(weight, (tuple, list))
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x: expected a torch.Tensor with at least one dimension")
+    if frozen:
+        if len(weight) != 2:
+            raise ValueError("weight: expected a tensor or a payload (codes, scales)")
+        O, P, _ = _payload(*weight, "weight ")
+        if P != _pad(x.shape[-1]):
+            raise ValueError(f"x: last dimension {x.shape[-1]}, weight rows of {P} values")
+        parts = tuple(weight)
+    else:
+        _matrix(weight, "weight")
+        O = weight.shape[0]
+        if x.shape[-1] != weight.shape[1]:
+            raise ValueError(f"x: last dimension {x.shape[-1]}, weight's {weight.shape[1]}")
+        parts = (weight,)
+    # flatten, where reshape(-1, 0) would not know how many rows
+    x2 = x if x.dim() == 2 else x.flatten(0, -2) if x.dim() > 2 else x.unsqueeze(0)
+    if x2.dtype not in _HALF:
+        raise ValueError(f"x: dtype {x2.dtype}, expected {' or '.join(map(str, _HALF))}")
+    _same_gpu(x.get_device(), x, *parts)
+    x2 = x2.contiguous()
+    if not frozen:
+        parts = (weight.contiguous(),)
+    # a tangent of forward-mode differentiation, which the layer has no rule for, is for
+    # autograd to refuse in either mode
+    if torch.is_grad_enabled() or any(unpack_dual(t).tangent is not None for t in (x2, *parts)):
+        y = (_FrozenLinear if frozen else _Linear).apply(x2, *parts)
+    else:
+        index = x2.get_device()
+        qw = None if frozen else _quantized(index, parts[0])
+        w = tuple(t.data_ptr() for t in parts) if frozen else _at(qw, O, x2.shape[1])
+        y = _product(index, x2, _quantized(index, x2), w, O)
+    return y if x.dim() == 2 else y.view(*x.shape[:-1], O)
