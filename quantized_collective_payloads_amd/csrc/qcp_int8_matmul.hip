@@ -67,14 +67,6 @@ template <int FM, int FN> struct IntFragments {
 
 __device__ __forceinline__ i32x4_t lds_codes(uint32_t at) { return __builtin_bit_cast(i32x4_t, lds16(at)); }
 
-// as copy_to_lds, 4 bytes a lane
-__device__ __forceinline__ void copy4_to_lds(uint32_t lds, uint32_t voff, i32x4_t rsrc) {
-    asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
-                 :
-                 : "v"(voff), "s"(rsrc), "{m0}"(__builtin_amdgcn_readfirstlane((int)lds))
-                 : "memory");
-}
-
 // SLICED: the tiles are those of `slices` parts of K, one part after the other; c is int32,
 // an M x N for each, and the scales are left to the join.
 template <int FM, int FN, int CT, bool SLICED>
@@ -345,12 +337,8 @@ __global__ __launch_bounds__(kThreads) void k_int8_matmul_join(const int *__rest
 // ---------------------------------------------------------------------------
 // Bound: reading B once.  N/16 work-groups; the WV waves of one deal out K in steps of 256
 // bytes and add their sums in LDS, so a few rows still fill the GPU, without a second
-// launch.  A quarter-wave takes 64 of a step's bytes of its rows, a lane 64 consecutive ones.
+// launch.  A load takes 64 consecutive bytes of 16 rows, a quarter-wave 16 of them.
 // Operands go straight to registers, a whole step's loads at a time.
-template <int F> struct IntStep {
-    i32x4_t v[F][4];
-};
-
 template <int FA, int FB, int WV, int CT>
 __global__ __launch_bounds__(64 * WV) void k_int8_matmul_rows(
     const uint8_t *__restrict__ a, const float *__restrict__ as, const uint8_t *__restrict__ b,
@@ -359,33 +347,37 @@ __global__ __launch_bounds__(64 * WV) void k_int8_matmul_rows(
     const int wave = __builtin_amdgcn_readfirstlane((int)(__builtin_amdgcn_workitem_id_x() >> 6)), lane = lane_id();
     const int row = lane & 15, quarter = lane >> 4;
     const int64_t n0 = (int64_t)__builtin_amdgcn_workgroup_id_x() * (16 * FB), m0 = group_y() * (16 * FA);
+    // rows of A past the end are not read (their sums are not stored), those of B repeat the last
     const uint8_t *pa[FA], *pb[FB];
+    bool there[FA];
 #pragma unroll
-    for (int i = 0; i < FA; i++) pa[i] = a + (min(m0 + 16 * i + row, M - 1) * granules + quarter) * 64;
+    for (int i = 0; i < FA; i++) {
+        there[i] = m0 + 16 * i + row < M;
+        pa[i] = a + (m0 + 16 * i + row) * granules * 64 + 16 * quarter;
+    }
 #pragma unroll
-    for (int i = 0; i < FB; i++) pb[i] = b + (min(n0 + 16 * i + row, N - 1) * granules + quarter) * 64;
-    auto load = [&](int64_t g, auto &f, const uint8_t *const *p, auto F) __attribute__((always_inline)) {
-        static_for<F>([&](auto I) __attribute__((always_inline)) {
-            constexpr int i = I;
-            const bool inside = g + quarter < granules;
+    for (int i = 0; i < FB; i++) pb[i] = b + min(n0 + 16 * i + row, N - 1) * granules * 64 + 16 * quarter;
+    // granules are even, and so is where a step may end
+    auto load = [&](int64_t g, i32x4_t (&v)[4], const uint8_t *p) __attribute__((always_inline)) {
+        const bool all = g + 2 < granules;
 #pragma unroll
-            for (int t = 0; t < 4; t++)
-                f.v[i][t] = inside ? *(const i32x4_t *)(p[i] + g * 64 + 16 * t) : i32x4_t{0, 0, 0, 0};
-        });
+        for (int t = 0; t < 4; t++) v[t] = t < 2 || all ? *(const i32x4_t *)(p + (g + t) * 64) : i32x4_t{0, 0, 0, 0};
     };
     i32x4_t acc[FA][FB] = {};
     for (int64_t g = 4 * wave; g < granules; g += 4 * WV) {
-        IntStep<FA> fa;
-        IntStep<FB> fb;
-        load(g, fb, pb, std::integral_constant<int, FB>{});
-        load(g, fa, pa, std::integral_constant<int, FA>{});
+        i32x4_t fa[FA][4] = {}, fb[FB][4];
+#pragma unroll
+        for (int i = 0; i < FB; i++) load(g, fb[i], pb[i]);
+#pragma unroll
+        for (int i = 0; i < FA; i++)
+            if (there[i]) load(g, fa[i], pa[i]);
 #pragma unroll
         for (int t = 0; t < 4; t++)
 #pragma unroll
             for (int i = 0; i < FA; i++)
 #pragma unroll
                 for (int j = 0; j < FB; j++)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb.v[j][t], fa.v[i][t], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j][t], fa[i][t], acc[i][j], 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < FA; i++)
@@ -420,6 +412,13 @@ hipError_t run_rows(const uint8_t *a, const float *as, const uint8_t *b, const f
     return hipGetLastError();
 }
 
+// which form takes a product that is not one for few rows: the cheapest
+constexpr Form kForms[] = {
+    {64, 128, 512, 29, 44, 300},       // 512 x 4096, K = 4096: 18.7 us, tiles of 128 24.4
+    {128, 128, 512, 75, 103, 400},     // 2048 x 4096, K = 14336: 120 us, tiles of 64 201, of 256 152
+    {256, 128, 256, 125, 170, 1100},   // 4096 x 4096, K = 4096: 65 us, tiles of 128 76
+};
+
 template <int CT>
 hipError_t run_matmul(const uint8_t *a, const float *as, const uint8_t *b, const float *bs, int64_t M, int64_t N,
                       int64_t stages, void *c, int64_t ldc, int *work, hipStream_t st) {
@@ -431,26 +430,34 @@ hipError_t run_matmul(const uint8_t *a, const float *as, const uint8_t *b, const
         hipLaunchKernelGGL((k_int8_matmul_join<CT>), grid, dim3(kThreads), 0, st, work, slices, as, bs, M, N, c, ldc);
         return hipGetLastError();
     }
-    const auto tiles = [&](int64_t m, int64_t n) { return ((M + m - 1) / m) * ((N + n - 1) / n); };
-    const int64_t small = tiles(64, 64), middle = tiles(128, 128), large = tiles(256, 256), granules = 2 * stages;
+    // Few rows: one pass over B by as many work-groups as it has 16 rows, unless that many
+    // rows of A make it the slower (us warm and cold, and with tiles of 64: 1 x 14336, K = 4096
+    // 13.3 and 15.3, 12.2 and 17.9; 16 x 14336, K = 4096 17.4 and 19.9, 12.6 and 18.1; 16 x 4096,
+    // K = 4096 6.4 and 7.9, 10.5 and 12.9); also for more rows where the tiles would leave most
+    // of the GPU idle and K is short (77 x 1001, K = 1111: 4.2 and 4.7, 6.0 and 6.5; 48 x 4096,
+    // K = 4096: 12.7, 11.1 warm).
+    const int64_t small = kForms[0].tiles(M, N), granules = 2 * stages;
     const bool rows = (N + 15) / 16 <= kMaxGroups / 2;
-    if (rows && M <= 16) return run_rows<1, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
-    if (rows && M <= 32 && small < 128) return run_rows<2, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
-    if (rows && small <= 64 && granules <= 32) return run_rows<4, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
-    if (small <= 512) return run_tiled<1, 1, CT>(a, as, b, bs, M, N, stages, c, ldc, st);
-    if ((middle + 511) / 512 * (27 * stages + 70) < (large + 255) / 256 * (41 * stages + 220))
-        return run_tiled<2, 2, CT>(a, as, b, bs, M, N, stages, c, ldc, st);
+    if (rows && (M <= 8 || (M <= 16 && small < 160))) return run_rows<1, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
+    if (rows && ((M <= 32 && small < 160) || (small <= 64 && stages <= 16)))
+        return run_rows<2, 1, CT>(a, as, b, bs, M, N, granules, c, ldc, st);
+    const auto price = [&](int f) { return kForms[f].price(kForms[f].tiles(M, N), stages); };
+    const int64_t p64 = price(0), p128 = price(1), p256 = price(2);
+    if (p64 <= p128 && p64 <= p256) return run_tiled<1, 1, CT>(a, as, b, bs, M, N, stages, c, ldc, st);
+    if (p128 <= p256) return run_tiled<2, 2, CT>(a, as, b, bs, M, N, stages, c, ldc, st);
     return run_tiled<4, 4, CT>(a, as, b, bs, M, N, stages, c, ldc, st);
 }
 
 }  // namespace
 
 // A long K and too few tiles for the GPU: slices of K, each a share of the work-groups,
-// added up in a second launch.
+// added up in a second launch (us without and with: 64 x 4096, K = 14336 29 and 18.5; 128 x
+// 4096, K = 14336 29.5 and 23; 32 x 4096, K = 14336 22 and 17.5; 64 x 512, K = 28672 30 and 16.3;
+// 320 x 1000, K = 9000 20.4 and 16.7; but 64 x 4096, K = 4096 11 both; 256 x 4096, K = 14336 32
+// and 33).
 int int8_matmul_slices(int64_t M, int64_t N, int64_t stages) {
     const int64_t rows = (M + 63) / 64, cols = (N + 63) / 64;
-    if (M <= 16 || N < 1 || rows > 128 || cols > 128 || rows * cols > 128) return 1;
-    if (stages < (M <= 32 ? 64 : rows * cols < 48 ? 48 : 32)) return 1;
+    if (M <= 16 || N < 1 || rows > 128 || cols > 128 || rows * cols > 128 || stages < 64) return 1;
     return (int)std::min<int64_t>(8, 256 / (rows * cols));
 }
 

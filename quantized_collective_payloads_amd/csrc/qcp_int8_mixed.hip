@@ -53,7 +53,7 @@ template <int TM_, int TN_, int KS_, int WM_, int WN_> struct MixedTile {
 
 // The stages of one slice of k of one tile.  TRANS: a is given as [K, M].
 template <class G, int AT, bool TRANS, int CT, bool SLICED>
-__global__ __launch_bounds__(G::threads, (G::slot > 40960 ? 2 : 2)) void k_int8_mixed(
+__global__ __launch_bounds__(G::threads, 2) void k_int8_mixed(
     const uint16_t *__restrict__ a, int64_t lda, const uint8_t *__restrict__ codes, const float *__restrict__ scales,
     int64_t M, int64_t N, int64_t K, uint32_t pad, uint32_t slices, uint32_t m_tiles, uint32_t n_tiles,
     void *__restrict__ c, int64_t ldc) {
@@ -82,79 +82,69 @@ __global__ __launch_bounds__(G::threads, (G::slot > 40960 ? 2 : 2)) void k_int8_
     constexpr uint32_t groups = G::TN / 4;
     const uint32_t col = 4 * (tid % groups), octet = groups == 64 ? (uint32_t)wave : tid / groups;
     const uint32_t b_off = octet * 8 * pad + (uint32_t)min(n0 + col, (int64_t)pad - 4);
-    const uint32_t at_off = TRANS ? octet * 8 * (uint32_t)lda + col : 0;   // in elements
-    const bool m_whole = m_rows == G::TM;
-    // ... or 8 of k of 4 rows of a
+    // ... (columns past the end repeat the last four that begin within), or 8 of k of 4 rows of a
+    const uint32_t a_col = min(col, (m_rows - 1) & ~3u);
+    const uint32_t t_off = octet * 8 * (uint32_t)lda + a_col;              // in elements
     constexpr uint32_t row_step = G::threads / G::octets;
     const uint32_t a_row = tid / G::octets, a_oct = tid % G::octets;
+    uint32_t s_off[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) s_off[i] = min(a_row + i * row_step, m_rows - 1) * (uint32_t)lda + a_oct * 8;
 
     uint32_t wb[8];
     float sb[8];
     u32x2_t wt[8];
     u32x4_t wa[4];
+    // A stage all of whose rows exist.  4 columns of a transposed a may reach 3 elements past
+    // its row: 3 more rows have to follow.
+    constexpr int beyond = TRANS ? 3 : 0;
     auto load = [&](int64_t s) __attribute__((always_inline)) {
         const int64_t k0 = s * KS;
         const uint8_t *const pb = codes + k0 * pad;
         const float *const ps = scales + k0 + octet * 8;
-        const bool k_whole = k0 + KS <= K;
-        if (k_whole) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                wb[j] = *(const uint32_t *)(pb + (int64_t)j * pad + b_off);
-                sb[j] = ps[j];
-            }
-        } else {
-            const int left = (int)(K - k0) - (int)octet * 8;
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                wb[j] = 0;
-                sb[j] = 0;
-                if (j < left) {
-                    wb[j] = *(const uint32_t *)(pb + (int64_t)j * pad + b_off);
-                    sb[j] = ps[j];
-                }
-            }
+        for (int j = 0; j < 8; j++) {
+            wb[j] = *(const uint32_t *)(pb + (int64_t)j * pad + b_off);
+            sb[j] = ps[j];
         }
         if constexpr (TRANS) {
             const uint16_t *const pa = a + k0 * lda + m0;
-            if (k_whole && m_whole) {
 #pragma unroll
-                for (int j = 0; j < 8; j++) wt[j] = *(const u32x2_any *)(pa + (int64_t)j * lda + at_off);
-            } else {
-                const int left = (int)min(K - k0, (int64_t)KS) - (int)octet * 8, width = (int)m_rows - (int)col;
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    wt[j] = u32x2_t{0, 0};
-                    if (j >= left) continue;
-                    const uint16_t *const p = pa + (int64_t)j * lda + at_off;
-                    if (width >= 4) {
-                        wt[j] = *(const u32x2_any *)p;
-                    } else {
-                        if (width > 0) wt[j].x = p[0];
-                        if (width > 1) wt[j].x |= (uint32_t)p[1] << 16;
-                        if (width > 2) wt[j].y = p[2];
-                    }
-                }
-            }
+            for (int j = 0; j < 8; j++) wt[j] = *(const u32x2_any *)(pa + (int64_t)j * lda + t_off);
         } else {
             const uint16_t *const pa = a + m0 * lda + k0;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const uint32_t r = min(a_row + i * row_step, m_rows - 1);
-                const uint16_t *const p = pa + (r * (uint32_t)lda + a_oct * 8);
-                if (k_whole) {
-                    wa[i] = *(const u32x4_any *)p;
-                } else {
-                    const int left = (int)(K - k0) - (int)a_oct * 8;
-                    wa[i] = u32x4_t{0, 0, 0, 0};
-                    if (left >= 8) {
-                        wa[i] = *(const u32x4_any *)p;
-                    } else {
+            for (int i = 0; i < 4; i++) wa[i] = *(const u32x4_any *)(pa + s_off[i]);
+        }
+    };
+    // the last ones, element by element where need be; rows past the end are zeros
+    auto load_last = [&](int64_t s) __attribute__((always_inline)) {
+        const int64_t k0 = s * KS;
+        const int left = (int)min(K - k0, (int64_t)KS);
 #pragma unroll
-                        for (int e = 0; e < 8; e++)
-                            if (e < left) wa[i][e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
-                    }
-                }
+        for (int j = 0; j < 8; j++) {
+            const bool in = (int)octet * 8 + j < left;
+            wb[j] = in ? *(const uint32_t *)(codes + (k0 + j) * pad + b_off) : 0;
+            sb[j] = in ? scales[k0 + octet * 8 + j] : 0;
+            if constexpr (TRANS) {
+                const uint16_t *const p = a + (k0 + j) * lda + m0 + t_off;
+                wt[j] = u32x2_t{0, 0};
+                const int width = in ? (int)(m_rows - a_col) : 0;
+                if (width > 0) wt[j].x = p[0];
+                if (width > 1) wt[j].x |= (uint32_t)p[1] << 16;
+                if (width > 2) wt[j].y = p[2];
+                if (width > 3) wt[j].y |= (uint32_t)p[3] << 16;
+            }
+        }
+        if constexpr (!TRANS) {
+            const int width = left - (int)a_oct * 8;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint16_t *const p = a + m0 * lda + k0 + s_off[i];
+                wa[i] = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    if (e < width) wa[i][e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
             }
         }
     };
@@ -192,33 +182,54 @@ __global__ __launch_bounds__(G::threads, (G::slot > 40960 ? 2 : 2)) void k_int8_
     f32x16_t acc[FM][FN] = {};
     auto multiply = [&](uint32_t slot) __attribute__((always_inline)) {
         const lds_byte *const from = base + slot * G::slot;
+        u32x4_t fa[2][FM], fb[2][FN];
+        auto read = [&](int q) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < FN; j++) fb[q & 1][j] = *(const lds_piece *)(from + G::TM * G::row + G::at(brow + 32 * j, 2 * q + half));
+#pragma unroll
+            for (int i = 0; i < FM; i++) fa[q & 1][i] = *(const lds_piece *)(from + G::at(arow + 32 * i, 2 * q + half));
+        };
+        read(0);
 #pragma unroll
         for (int q = 0; q < KS / 16; q++) {
-            u32x4_t fa[FM], fb[FN];
-#pragma unroll
-            for (int j = 0; j < FN; j++) fb[j] = *(const lds_piece *)(from + G::TM * G::row + G::at(brow + 32 * j, 2 * q + half));
-#pragma unroll
-            for (int i = 0; i < FM; i++) fa[i] = *(const lds_piece *)(from + G::at(arow + 32 * i, 2 * q + half));
+            if (q + 1 < KS / 16) read(q + 1);
             // B first: a lane then holds 4 consecutive n of one m per group of registers
 #pragma unroll
             for (int i = 0; i < FM; i++)
 #pragma unroll
-                for (int j = 0; j < FN; j++) acc[i][j] = mma16bit<AT>(fb[j], fa[i], acc[i][j]);
+                for (int j = 0; j < FN; j++) acc[i][j] = mma16bit<AT>(fb[q & 1][j], fa[q & 1][i], acc[i][j]);
         }
     };
 
+    // the stages of `load`, and then those of load_last
+    const int64_t whole_k = min(max((K - beyond) / KS, first), last);
+    auto stages = [&](int64_t from, int64_t to, auto body) __attribute__((always_inline)) {
+        // body(s, how to load the stage after the next: 0 not at all, 1 load, 2 load_last)
+        int64_t s = from;
+        for (; s + 2 < whole_k; s++) body(s, std::integral_constant<int, 1>{});
+        for (; s + 2 < to; s++) body(s, std::integral_constant<int, 2>{});
+        for (; s < to; s++) body(s, std::integral_constant<int, 0>{});
+    };
+    auto fill = [&](int64_t s) __attribute__((always_inline)) {
+        if (s < whole_k) load(s);
+        else load_last(s);
+    };
     if (first < last) {
-        load(first);
+        fill(first);
         write(0);
-        if (first + 1 < last) load(first + 1);
+        if (first + 1 < last) fill(first + 1);
         wait_lds_and_meet();
-        for (int64_t s = first; s < last; s++) {
+        auto next = [&](int64_t s, uint32_t slot, auto how) __attribute__((always_inline)) {
+            if (how != 0 || s + 1 < last) write(slot ^ 1);
+            if constexpr (how == 1) load(s + 2);
+            if constexpr (how == 2) load_last(s + 2);
+        };
+        stages(first, last, [&](int64_t s, auto how) __attribute__((always_inline)) {
             const uint32_t slot = (uint32_t)(s - first) & 1;
-            if (s + 1 < last) write(slot ^ 1);
-            if (s + 2 < last) load(s + 2);
+            next(s, slot, how);
             multiply(slot);
             wait_lds_and_meet();
-        }
+        });
     }
     const bool whole = m0 + G::TM <= M && n0 + G::TN <= N;
     void *const to = SLICED ? (float *)c + slice * M * N : c;
@@ -227,6 +238,272 @@ __global__ __launch_bounds__(G::threads, (G::slot > 40960 ? 2 : 2)) void k_int8_
         store_fragment<CT>(acc[i][j], to, ldc, m0 + arow + 32 * i, n0 + (brow - r) + 32 * j, half, M, N, whole);
     });
 }
+
+// ---------------------------------------------------------------------------
+// 256 x 256 of C per work-group, operands copied to LDS as they lie in memory.
+// ---------------------------------------------------------------------------
+// For an a whose rows are aligned to 16 bytes.  Eight waves hold 256 x 32 each, so that a
+// column of the payload is decoded once in a work-group; a's fragments are read by all of
+// them.  A stage is 64 of k: 32 KB of a, 16 KB of codes and 64 scales, in one of three
+// slots, so that copies have two stages to arrive.  LDS gives 8 k of a column to a lane:
+// ds_read_b64_tr_b8 turns 8 rows x 16 bytes for 16 lanes, _tr_b16 4 rows x 16 values of a
+// transposed a.  A register holds the scales of two steps of 16, each row of 16 lanes its own
+// 16, and the products with them take one lane's for all (row_newbcast).
+//
+// A step is 8 products; between them, in the order written, the fragment just used is read
+// for the next step, and that step's codes are read and decoded.  In a stage's last step,
+// whose fragments were read before, the barrier says that the slot of the stage before is
+// free, and the copies of the stage three on go there.
+//
+// Pieces of 16 bytes lie in LDS in an order that spreads what a read touches in a cycle over all
+// banks: of a row by row, piece ^ (row / 2 % 8); of a transposed, piece ^ 4 (row % 4); of the
+// payload, piece ^ 2 (row % 8).  What is read past the end of a buffer counts for nothing: results
+// past the end are not stored, and in the last stage of a K that is no multiple of 64 the values
+// of a and the scales past the end are made zeros in LDS.
+namespace direct {
+
+constexpr int kSide = 256, kStage = 64, kThreads8 = 512, kSlots = 3, FM = 8;
+constexpr uint32_t kCodesAt = kSide * kStage * 2, kScalesAt = kCodesAt + kSide * kStage, kSlot = kScalesAt + 256;
+constexpr int kCopies = 7;                                   // of a wave and stage
+constexpr int64_t kMaxLd = (int64_t)1 << 22;                 // 256 rows of a are within 32 bits
+
+typedef __attribute__((address_space(3))) uint8_t lds_byte;
+
+__device__ __forceinline__ u32x2_t read_tr8(uint32_t at) {
+    typedef int i32x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2_t *)at));
+}
+__device__ __forceinline__ u32x2_t read_tr16(uint32_t at) {
+    typedef short i16x4_t __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t *)at));
+}
+// lane J of each row of 16 lanes, to all of the row
+template <int J>
+__device__ __forceinline__ float of_lane(float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x150 + J, 0xf, 0xf, true));
+}
+template <int AT, bool TRANS, int CT, bool SLICED>
+__global__ __launch_bounds__(kThreads8, 2) void k_int8_mixed_direct(
+    const uint16_t *__restrict__ a, int64_t lda, const uint8_t *__restrict__ codes, const float *__restrict__ scales,
+    int64_t M, int64_t N, int64_t K, uint32_t pad, uint32_t slices, uint32_t m_tiles, uint32_t n_tiles, uint32_t groups,
+    void *__restrict__ c, int64_t ldc) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * kSlot];
+    const int tid = (int)__builtin_amdgcn_workitem_id_x();
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t lane = (uint32_t)lane_id(), r = lane & 31, half = lane >> 5, t16 = lane & 15, side = (lane >> 4) & 1;
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_byte *)lds;
+    const uint32_t tiles = m_tiles * n_tiles * (SLICED ? slices : 1);
+
+    // the tile that is being copied, and the next of its stages to be
+    int64_t m0, n0, k_next, k_end;
+    uint32_t m_rows, stages, slice = 0, b_voff[2], to_slot;
+    auto set_tile = [&](uint32_t t) __attribute__((always_inline)) {
+        const int64_t all = (K + kStage - 1) / kStage;
+        int64_t first = 0, count = all;
+        if constexpr (SLICED) {
+            slice = t / (m_tiles * n_tiles);
+            t -= slice * (m_tiles * n_tiles);
+            const int64_t each = all / slices, over = all % slices;
+            first = slice * each + min((int64_t)slice, over);
+            count = each + (slice < over ? 1 : 0);
+        }
+        stages = (uint32_t)count;
+        const TilePlace at = tile_place(t, m_tiles, n_tiles);
+        m0 = (int64_t)at.m * kSide;
+        n0 = (int64_t)at.n * kSide;
+        m_rows = (uint32_t)min(M - m0, (int64_t)kSide);
+        k_next = first * kStage;
+        k_end = min((first + count) * kStage, K);
+        to_slot = 0;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const uint32_t row = 8 * wave + 4 * i + (lane >> 4), piece = (lane & 15) ^ (2 * (row & 7));
+            b_voff[i] = row * pad + (uint32_t)min(n0 + 16 * piece, (int64_t)pad - 16);
+        }
+    };
+    // the n-th copy of the next stage, the scales first
+    auto copy = [&](auto I) __attribute__((always_inline)) {
+        constexpr int n = I;
+        const uint32_t to = base + to_slot;
+        if constexpr (n == 0) {
+            copy4_to_lds(to + kScalesAt, lane * 4, buffer_of(scales + k_next, (uint64_t)(K - k_next) * 4));
+        } else if constexpr (n <= 2) {
+            copy_to_lds(to + kCodesAt + wave * 2048 + (n - 1) * 1024, b_voff[n - 1],
+                        buffer_of(codes + k_next * pad, (uint64_t)(K - k_next) * pad), 0);
+        } else if constexpr (TRANS) {
+            constexpr int i = n - 3;
+            const uint32_t row = 8 * wave + 2 * i + half, piece = r ^ (4 * (2 * (i & 1) + half));
+            copy_to_lds(to + wave * 4096 + i * 1024, row * (uint32_t)lda * 2 + piece * 16,
+                        buffer_of(a + k_next * lda + m0, (uint64_t)((K - 1 - k_next) * lda + (M - m0)) * 2), 0);
+        } else {
+            constexpr int i = n - 3;
+            const uint32_t row = min(32 * wave + 8 * i + (lane >> 3), m_rows - 1);
+            const uint32_t piece = (lane & 7) ^ (lane >> 4) ^ (4 * (i & 1));
+            copy_to_lds(to + wave * 4096 + i * 1024, row * (uint32_t)lda * 2 + piece * 16,
+                        buffer_of(a + m0 * lda, (uint64_t)((m_rows - 1) * lda + K) * 2), (uint32_t)k_next * 2);
+        }
+    };
+    auto copied = [&]() __attribute__((always_inline)) {
+        k_next += kStage;
+        to_slot = to_slot == (kSlots - 1) * kSlot ? 0 : to_slot + kSlot;
+    };
+
+    // where this lane reads in slot 0
+    const uint32_t a_at = base + (TRANS ? (8 * half + (t16 >> 2)) * 512 + ((4 * (t16 >> 2) + 2 * side + ((t16 & 3) >> 1)) * 16) + 8 * (t16 & 1)
+                                        : r * 128 + ((half ^ ((r >> 1) & 7)) * 16));
+    const uint32_t b_at = base + kCodesAt + (8 * half + (t16 >> 1)) * 256 + ((2 * (wave ^ (t16 >> 1)) + side) * 16) + 8 * (t16 & 1);
+    const uint32_t s_at = base + kScalesAt + 4 * (16 * (t16 >> 3) + 8 * half + (t16 & 7));
+
+    f32x16_t acc[FM];
+    u32x4_t fa[FM], fb;
+    u32x2_t raw;
+    float mark[2];
+    uint32_t from = 0;                                       // the slot that is being read
+    auto read_a = [&](auto I, auto Q) __attribute__((always_inline)) {
+        constexpr int i = I, q = Q;
+        if constexpr (TRANS) {
+            const uint32_t at = (a_at ^ (64 * (i & 3))) + from;
+            const u32x2_t lo = read_tr16(at + 256 * (i >> 2) + 8192 * q), hi = read_tr16(at + 256 * (i >> 2) + 8192 * q + 2048);
+            fa[i] = u32x4_t{lo.x, lo.y, hi.x, hi.y};
+        } else {
+            fa[i] = lds16((a_at ^ (32 * q)) + from + 4096 * i);
+        }
+    };
+    auto read_codes = [&](auto Q) __attribute__((always_inline)) { raw = read_tr8(b_at + from + 4096 * Q); };
+    auto read_marks = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) mark[i] = __uint_as_float(lds4(s_at + from + 128 * i));
+    };
+    // values 2J and 2J + 1 of step Q
+    auto decode = [&](auto J, auto Q, u32x4_t &to) __attribute__((always_inline)) {
+        constexpr int j = J, q = Q, l = 8 * (q & 1) + 2 * j;
+        const uint32_t w = j < 2 ? raw.x : raw.y;
+        to[j] = narrow2<AT>(cvt_sbyte<2 * (j & 1)>(w) * of_lane<l>(mark[q >> 1]),
+                            cvt_sbyte<2 * (j & 1) + 1>(w) * of_lane<l + 1>(mark[q >> 1]));
+    };
+    using std::integral_constant;
+    using zero = integral_constant<int, 0>;
+    // what lies past the end of K in the slot at `at`, `left` of whose rows exist, becomes zeros:
+    // a's values (of a row by row, `left` is a multiple of 8) and the scales
+    auto clear = [&](uint32_t at, uint32_t left) __attribute__((always_inline)) {
+        typedef __attribute__((address_space(3))) u32x4_t lds_piece;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t n = i * kThreads8 + tid;
+            const uint32_t k = TRANS ? n / 32 : n % 8 * 8;
+            const uint32_t to = TRANS ? n * 16 : n / 8 * 128 + ((n ^ (n / 16)) & 7) * 16;
+            if (k >= left) *(lds_piece *)(at + to) = u32x4_t{0, 0, 0, 0};
+        }
+        if (tid < kStage && (uint32_t)tid >= left) *(__attribute__((address_space(3))) float *)(at + kScalesAt + tid * 4) = 0;
+        wait_lds_and_meet();
+    };
+    // a stage.  COPY: the next stage is copied beside it.  LAST: nothing follows.  meet: before the
+    // next stage's slot, which it is given, is read.
+    auto stage = [&](auto COPY, auto LAST, auto meet) __attribute__((always_inline)) {
+        static_for<4>([&](auto Q) __attribute__((always_inline)) {
+            constexpr int q = Q, then = (q + 1) % 4;
+            constexpr bool more = q < 3 || !LAST;
+            u32x4_t fn;
+            if constexpr (q == 3 && !LAST) {
+                from = from == (kSlots - 1) * kSlot ? 0 : from + kSlot;
+                meet(from);
+            }
+            static_for<FM>([&](auto I) __attribute__((always_inline)) {
+                constexpr int i = I;
+                // B first: a lane then holds 4 consecutive n of one m per group of registers
+                acc[i] = mma16bit<AT>(fb, fa[i], acc[i]);
+                if constexpr (more) {
+                    if constexpr (i == 0) {
+                        read_codes(integral_constant<int, then>{});
+                        if constexpr (then == 0) read_marks();
+                    }
+                    read_a(I, integral_constant<int, then>{});
+                    if constexpr (i >= 4) decode(integral_constant<int, i - 4>{}, integral_constant<int, then>{}, fn);
+                }
+                if constexpr (COPY && q == 3) {
+                    if constexpr (i >= 1) copy(integral_constant<int, i - 1>{});
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            if constexpr (more) fb = fn;
+            if constexpr (COPY && q == 3) copied();
+        });
+    };
+    auto begin = [&]() __attribute__((always_inline)) {
+        from = 0;
+        read_codes(zero{});
+        read_marks();
+        static_for<FM>([&](auto I) __attribute__((always_inline)) { read_a(I, zero{}); });
+        static_for<4>([&](auto J) __attribute__((always_inline)) { decode(J, zero{}, fb); });
+    };
+    auto copy_first = [&]() __attribute__((always_inline)) {
+        for (uint32_t s = 0; s < min(stages, (uint32_t)kSlots); s++) {
+            static_for<kCopies>(copy);
+            copied();
+        }
+    };
+    using no = integral_constant<int, 0>;
+    using yes = integral_constant<int, 1>;
+    // 16-byte stores of a wave's whole results
+    constexpr int stores = FM * 16 * dtype_traits<CT>::bytes / 16;
+
+    uint32_t tile = __builtin_amdgcn_workgroup_id_x();
+    set_tile(tile);
+    copy_first();
+    wait_and_meet<0>();
+    int behind = 0;                                          // stages whose copies are older than the last tile's stores
+    for (;;) {
+#pragma unroll
+        for (int i = 0; i < FM; i++) acc[i] = f32x16_t{};
+        if (stages) {
+            const uint32_t tail = (uint32_t)(k_end - (k_end - 1) / kStage * kStage);   // rows of the last stage
+            if (stages == 1 && tail < kStage) clear(base, tail);
+            begin();
+            uint32_t s = 0;
+            for (; s + kSlots < stages; s++)
+                stage(yes{}, no{}, [&](uint32_t) __attribute__((always_inline)) {
+                    if (behind > 0) {
+                        behind--;
+                        wait_and_meet<kCopies + stores>();
+                    } else {
+                        wait_and_meet<kCopies>();
+                    }
+                });
+            for (; s + 1 < stages; s++)
+                stage(no{}, no{}, [&](uint32_t slot) __attribute__((always_inline)) {
+                    wait_and_meet<0>();
+                    if (s + 2 == stages && tail < kStage) clear(base + slot, tail);
+                });
+            stage(no{}, yes{}, [](uint32_t) __attribute__((always_inline)) {});
+        }
+
+        // the next tile's first copies go out before this one's results
+        const int64_t m_done = m0 + r, n_done = n0 + 32 * wave;
+        const bool whole = m0 + kSide <= M && n0 + kSide <= N;
+        void *const to = SLICED ? (float *)c + slice * M * N : c;
+        tile += groups;
+        const bool more = tile < tiles;
+        if (more) {
+            wait_lds_and_meet();                             // every wave is done with the slots
+            set_tile(tile);
+            copy_first();
+        }
+        static_for<FM>([&](auto I) __attribute__((always_inline)) {
+            constexpr int i = I;
+            store_fragment<CT>(acc[i], to, ldc, m_done + 32 * i, n_done, (int)half, M, N, whole);
+        });
+        if (!more) break;
+        if (whole && stages >= kSlots) {
+            wait_and_meet<(2 * kCopies + stores < 63 ? 2 * kCopies + stores : 63)>();
+            behind = 2;
+        } else {
+            wait_and_meet<0>();
+            behind = 0;
+        }
+    }
+}
+
+}  // namespace direct
 
 // The sum of the slices, in their order, rounded once: 4 columns a lane.
 template <int CT>
@@ -272,24 +549,77 @@ hipError_t run(const MixedArgs &p, int slices = 1) {
     return hipGetLastError();
 }
 
+template <int AT, bool TRANS, int CT, bool SLICED = false>
+hipError_t run_direct(const MixedArgs &p, int slices = 1) {
+    const int64_t mt = (p.M + direct::kSide - 1) / direct::kSide, nt = (p.N + direct::kSide - 1) / direct::kSide;
+    const uint32_t pad = (uint32_t)((p.N + 127) / 128 * 128);
+    const unsigned groups = (unsigned)std::min<int64_t>(mt * nt * slices, kCUs);
+    hipLaunchKernelGGL((direct::k_int8_mixed_direct<AT, TRANS, CT, SLICED>), dim3(groups), dim3(direct::kThreads8), 0, p.st,
+                       p.a, p.lda, p.codes, p.scales, p.M, p.N, p.K, pad, (uint32_t)slices, (uint32_t)mt, (uint32_t)nt,
+                       groups, p.c, p.ldc);
+    return hipGetLastError();
+}
+
+// which form takes a product: the cheapest
+constexpr Form kForms[] = {
+    {64, 128, 512, 90, 140, 300},      // 1024 x 1024, K = 1024: 10.2 us, tiles of 128 18.5
+    {128, 64, 512, 100, 145, 400},     // 2048 x 2048, K = 2048: 37 us, tiles of 64 46, of 256 47
+    {256, 64, 256, 175, 205, 1000},    // 4096 x 4096, K = 4096: 138 us, tiles of 128 183
+    {256, 64, 256, 120, 180, 800},     // the same, aligned: 124 us
+};
+constexpr int kDirect = 3;
+
+struct Choice {
+    int form, slices;
+};
+// Slices of K (up to 16, each of at least 256) fill the GPU where there are few tiles: 512 x
+// 4096, K = 14336 96 us with 4, 275 without; 2048 x 4096, K = 14336 239 with 2, 283 without.
+// They cost a second launch, and the sums a trip to memory and back.
+Choice choose(int64_t M, int64_t N, int64_t K, bool aligned, bool slicing) {
+    Choice best = {0, 1};
+    int64_t least = INT64_MAX;
+    for (int f = 0; f < 4; f++) {
+        if (f == (aligned ? 2 : kDirect)) continue;
+        const Form &m = kForms[f];
+        const int64_t tiles = m.tiles(M, N), stages = (K + m.stage - 1) / m.stage;
+        if (tiles > kMaxGroups / 2) continue;
+        for (int s = 1; s <= (slicing ? 16 : 1); s *= 2) {
+            if (s > 1 && (K / s < 256 || tiles * s > m.resident + m.resident / 4)) break;
+            int64_t price = m.price(tiles * s, (stages + s - 1) / s);
+            if (s > 1) price += 400 + (2 * s + 1) * M * N / 10000;             // 4 TB/s
+            if (price < least) {
+                least = price;
+                best = {f, s};
+            }
+        }
+    }
+    return best;
+}
+
+template <int AT, bool TRANS, int CT, bool SLICED>
+hipError_t run_form(const MixedArgs &p, Choice which) {
+    switch (which.form) {
+    case 0: return run<Tile64, AT, TRANS, CT, SLICED>(p, which.slices);
+    case 1: return run<Tile128, AT, TRANS, CT, SLICED>(p, which.slices);
+    case 2: return run<Tile256, AT, TRANS, CT, SLICED>(p, which.slices);
+    default: return run_direct<AT, TRANS, CT, SLICED>(p, which.slices);
+    }
+}
+
 template <int AT, bool TRANS, int CT>
 hipError_t run_mixed(const MixedArgs &p, float *work) {
-    const int slices = work ? int8_mixed_slices(p.M, p.N, p.K) : 1;
-    if (slices > 1) {
-        MixedArgs q = p;
-        q.c = work;
-        q.ldc = p.N;
-        const hipError_t e = run<Tile64, AT, TRANS, F32, true>(q, slices);
-        if (e != hipSuccess) return e;
-        const int64_t total = p.M * ((p.N + 3) / 4);
-        hipLaunchKernelGGL((k_int8_mixed_join<CT>), dim3((unsigned)((total + kThreads - 1) / kThreads)), dim3(kThreads), 0,
-                           p.st, work, slices, p.M, p.N, p.c, p.ldc);
-        return hipGetLastError();
-    }
-    const auto tiles = [&](int64_t side) { return ((p.M + side - 1) / side) * ((p.N + side - 1) / side); };
-    if (tiles(64) <= 512) return run<Tile64, AT, TRANS, CT>(p);
-    if (tiles(256) < 192) return run<Tile128, AT, TRANS, CT>(p);
-    return run<Tile256, AT, TRANS, CT>(p);
+    const bool aligned = (uintptr_t)p.a % 16 == 0 && p.lda % 8 == 0 && (TRANS ? p.M : p.K) % 8 == 0 && p.lda <= direct::kMaxLd;
+    const Choice which = choose(p.M, p.N, p.K, aligned, work != nullptr);
+    if (which.slices == 1) return run_form<AT, TRANS, CT, false>(p, which);
+    MixedArgs q = p;
+    q.c = work;
+    q.ldc = p.N;
+    const hipError_t e = run_form<AT, TRANS, F32, true>(q, which);
+    if (e != hipSuccess) return e;
+    const int64_t total = p.M * ((p.N + 3) / 4);
+    hipLaunchKernelGGL((k_int8_mixed_join<CT>), dim3((unsigned)((total + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+                       p.st, work, which.slices, p.M, p.N, p.c, p.ldc);
+    return hipGetLastError();
 }
 
 template <int AT, bool TRANS>
@@ -299,10 +629,10 @@ hipError_t by_result(const MixedArgs &p, int ct, float *work) {
 
 }  // namespace
 
+// the more of an aligned and of another a
 int int8_mixed_slices(int64_t M, int64_t N, int64_t K) {
-    const int64_t stages = (K + 127) / 128, rows = (M + 63) / 64, cols = (N + 63) / 64;
-    if (M < 1 || N < 1 || rows > 128 || cols > 128 || rows * cols > 128 || stages < 8) return 1;
-    return (int)std::min<int64_t>(std::min<int64_t>(8, stages / 4), 256 / (rows * cols));
+    if (M < 1 || N < 1 || K < 1) return 1;
+    return std::max(choose(M, N, K, false, true).slices, choose(M, N, K, true, true).slices);
 }
 
 hipError_t launch_int8_mixed(const void *a, int at, int64_t lda, int transpose, const uint8_t *codes,

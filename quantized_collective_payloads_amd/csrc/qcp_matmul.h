@@ -2,6 +2,8 @@
 // to the XCDs, copies from memory to LDS, and the stores of a fragment of C.
 #pragma once
 
+#include <algorithm>
+
 #include "qcp_device.h"
 #include "qcp_launch.h"
 
@@ -34,6 +36,20 @@ __device__ __forceinline__ void store4(void *c, int64_t at, int count, const flo
                 if (j < count) p[j] = (uint16_t)((j < 2 ? lo : hi) >> (16 * (j & 1)));
     }
 }
+
+// What a product takes in a kernel of square tiles, in units of 10 ns, from measured parts: a
+// stage while the GPU is half full and when it is full (where the clock gives way to the power
+// that the matrix cores draw, and the caches are shared), and a round beside its stages.
+struct Form {
+    int side, stage, resident;   // of its tiles, bytes or values of K in a stage, work-groups that the GPU holds
+    int half, full, beside;
+    int64_t tiles(int64_t M, int64_t N) const { return ((M + side - 1) / side) * ((N + side - 1) / side); }
+    int64_t price(int64_t groups, int64_t stages) const {
+        const int64_t last = groups % resident, over = std::max<int64_t>(0, 2 * last - resident);
+        const int64_t step = half + (full - half) * over / resident;
+        return groups / resident * (stages * full + beside) + (last ? stages * step + beside : 0);
+    }
+};
 
 // Which tile of C work-group t takes.  Work-groups are dealt round-robin to the 8 XCDs:
 // each gets a contiguous run of tiles and walks it 4 tiles of M by N, so that the tiles
@@ -117,6 +133,14 @@ __device__ __forceinline__ i32x4_t buffer_of(const void *p, uint64_t bytes) {
     return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)at),
                    __builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32)),
                    __builtin_amdgcn_readfirstlane((int)n), 0x00020000};
+}
+
+// as copy_to_lds, 4 bytes a lane
+__device__ __forceinline__ void copy4_to_lds(uint32_t lds, uint32_t voff, i32x4_t rsrc) {
+    asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+                 :
+                 : "v"(voff), "s"(rsrc), "{m0}"(__builtin_amdgcn_readfirstlane((int)lds))
+                 : "memory");
 }
 
 // 16 bytes and 4 bytes of LDS at a byte address
