@@ -6,7 +6,7 @@
 // a NaN has a NaN scale and codes 0.  Rows of codes are padded with zeros to whole 128s, so
 // that every row begins on a cache line and the products never see a short one.
 //
-// The scale has to be known before the first code, so a team of lanes (a wave, or a
+// The scale has to be known before the first code, so a team of lanes (16, a wave, or a
 // work-group) keeps a whole row in registers: x is read once.  A piece is 16 bytes of x:
 // 8 values of 16 bits or 4 of 32, whose codes are 8 or 4 consecutive bytes.
 #include <algorithm>
@@ -109,7 +109,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void k_int8_quantize(
     const void *__restrict__ x, int64_t rows, int64_t cols, int64_t ld, uint32_t pieces, uint32_t groups,
     uint8_t *__restrict__ codes, float *__restrict__ scales) {
     constexpr int U = unit<XT>(), B = dtype_traits<XT>::bytes, ROWS = LANES < 256 ? 256 / LANES : 1;
-    __shared__ uint32_t maxima[2][LANES / 64];
+    __shared__ uint32_t maxima[2][(LANES + 63) / 64];
     const uint32_t tid = __builtin_amdgcn_workitem_id_x(), team = tid / LANES, t = tid % LANES;
     uint32_t turn = 0;
     for (int64_t row = (int64_t)__builtin_amdgcn_workgroup_id_x() * ROWS + team; row < rows;
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void k_int8_quantize(
 #pragma unroll
             for (int k = 0; k < V; k++) m = largest<XT>(m, v[k]);
         }
-        m = group_max_u32<64>(as_f32_bits<XT>(m));
+        m = group_max_u32<(LANES < 64 ? LANES : 64)>(as_f32_bits<XT>(m));
         if constexpr (LANES > 64) {
             if ((tid & 63) == 0) maxima[turn][tid / 64] = m;
             __syncthreads();
@@ -173,11 +173,19 @@ template <int XT>
 hipError_t quantize_rows(const void *x, int64_t rows, int64_t cols, int64_t ld, uint8_t *codes, float *scales,
                          hipStream_t st) {
     const int64_t pieces = (cols + 127) / 128 * 128 / unit<XT>();
+    // The fewest lanes that hold a row in 2 to 8 pieces each.  us of bf16 (fp32), read past the
+    // caches: 8192 x 28672 512 x 8 114, 256 x 16 119, 1024 x 4 135; 28672 x 8192 256 x 4 107
+    // (512 x 4 179), 512 x 4 123 (256 x 8 185); 4096 x 14336 512 x 4 31, 256 x 8 32; 14336 x 4096
+    // 256 x 2 30 (256 x 4 48), 64 x 8 31.5; 5000 x 520 64 x 2 4.8, 256 x 2 7.3.  Few long rows do
+    // not fill the GPU, and more lanes a row make each quicker: 1 x 28672 1024 x 4 4.0, 512 x 8 4.8.
+    if (pieces <= 16 * 2) return run_quantize<XT, 16, 2>(x, rows, cols, ld, pieces, codes, scales, st);
     if (pieces <= 64 * 2) return run_quantize<XT, 64, 2>(x, rows, cols, ld, pieces, codes, scales, st);
-    if (pieces <= 256 * 2 && rows < 1024) return run_quantize<XT, 256, 2>(x, rows, cols, ld, pieces, codes, scales, st);
-    if (pieces <= 64 * 8) return run_quantize<XT, 64, 8>(x, rows, cols, ld, pieces, codes, scales, st);
-    if (pieces <= 1024 * 2 && rows < 256) return run_quantize<XT, 1024, 2>(x, rows, cols, ld, pieces, codes, scales, st);
-    if (pieces <= 256 * 8) return run_quantize<XT, 256, 8>(x, rows, cols, ld, pieces, codes, scales, st);
+    if (pieces <= 64 * 4) return run_quantize<XT, 64, 4>(x, rows, cols, ld, pieces, codes, scales, st);
+    if (pieces <= 256 * 2) return run_quantize<XT, 256, 2>(x, rows, cols, ld, pieces, codes, scales, st);
+    if (pieces <= 256 * 4) return run_quantize<XT, 256, 4>(x, rows, cols, ld, pieces, codes, scales, st);
+    if (pieces <= 512 * 4) return run_quantize<XT, 512, 4>(x, rows, cols, ld, pieces, codes, scales, st);
+    if (pieces <= 1024 * 4 && rows < 256) return run_quantize<XT, 1024, 4>(x, rows, cols, ld, pieces, codes, scales, st);
+    if (pieces <= 512 * 8) return run_quantize<XT, 512, 8>(x, rows, cols, ld, pieces, codes, scales, st);
     if (pieces <= 1024 * 8) return run_quantize<XT, 1024, 8>(x, rows, cols, ld, pieces, codes, scales, st);
     return run_quantize<XT, 1024, 8, true>(x, rows, cols, ld, pieces, codes, scales, st);
 }

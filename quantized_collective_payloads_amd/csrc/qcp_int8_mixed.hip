@@ -32,9 +32,11 @@ __device__ __forceinline__ f32x16_t mma16bit(u32x4_t a, u32x4_t b, f32x16_t c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 
-// TM x TN of C per work-group, KS of k per stage, WM x WN waves
-template <int TM_, int TN_, int KS_, int WM_, int WN_> struct MixedTile {
-    static constexpr int TM = TM_, TN = TN_, KS = KS_, WM = WM_, WN = WN_;
+// TM x TN of C per work-group, KS of k per stage, WM x WN waves; the loads of AHEAD stages are in
+// flight beside the one that is multiplied.  TEAMS of so many waves take the stages in turn, and
+// their sums are added in LDS at the end.
+template <int TM_, int TN_, int KS_, int WM_, int WN_, int AHEAD_, int TEAMS_> struct MixedTile {
+    static constexpr int TM = TM_, TN = TN_, KS = KS_, WM = WM_, WN = WN_, AHEAD = AHEAD_, TEAMS = TEAMS_;
     static constexpr int threads = 64 * WM * WN;
     static constexpr int FM = TM / WM / 32, FN = TN / WN / 32;   // fragments of a wave
     static constexpr int row = 2 * KS;                           // bytes of a row in LDS
@@ -53,13 +55,15 @@ template <int TM_, int TN_, int KS_, int WM_, int WN_> struct MixedTile {
 
 // The stages of one slice of k of one tile.  TRANS: a is given as [K, M].
 template <class G, int AT, bool TRANS, int CT, bool SLICED>
-__global__ __launch_bounds__(G::threads, 2) void k_int8_mixed(
+__global__ __launch_bounds__(G::threads * G::TEAMS, 2) void k_int8_mixed(
     const uint16_t *__restrict__ a, int64_t lda, const uint8_t *__restrict__ codes, const float *__restrict__ scales,
     int64_t M, int64_t N, int64_t K, uint32_t pad, uint32_t slices, uint32_t m_tiles, uint32_t n_tiles,
     void *__restrict__ c, int64_t ldc) {
     constexpr int KS = G::KS, FM = G::FM, FN = G::FN;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * G::slot];
-    const uint32_t tid = __builtin_amdgcn_workitem_id_x();
+    constexpr int TEAMS = G::TEAMS;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[TEAMS * 2 * G::slot];
+    const uint32_t tid = __builtin_amdgcn_workitem_id_x() % G::threads;
+    const int team = TEAMS == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)(__builtin_amdgcn_workitem_id_x() / G::threads));
     const int wave = __builtin_amdgcn_readfirstlane((int)(tid >> 6)), lane = lane_id();
     uint32_t t = __builtin_amdgcn_workgroup_id_x(), slice = 0;
     if constexpr (SLICED) {
@@ -91,89 +95,110 @@ __global__ __launch_bounds__(G::threads, 2) void k_int8_mixed(
 #pragma unroll
     for (int i = 0; i < 4; i++) s_off[i] = min(a_row + i * row_step, m_rows - 1) * (uint32_t)lda + a_oct * 8;
 
-    uint32_t wb[8];
-    float sb[8];
-    u32x2_t wt[8];
-    u32x4_t wa[4];
-    // A stage all of whose rows exist.  4 columns of a transposed a may reach 3 elements past
-    // its row: 3 more rows have to follow.
-    constexpr int beyond = TRANS ? 3 : 0;
-    auto load = [&](int64_t s) __attribute__((always_inline)) {
+    struct Loaded {
+        uint32_t b[8];
+        float s[8];
+        u32x2_t t[8];
+        u32x4_t a[4];
+    };
+    Loaded regs[G::AHEAD];
+    // A stage all of whose rows exist.  Where M is no multiple of 4, 4 columns of a transposed a may
+    // reach 3 elements past its row: 3 more rows have to follow.
+    const bool fours = TRANS ? M % 4 == 0 : true;
+    const int beyond = fours ? 0 : 3;
+    auto load = [&](int64_t s, Loaded &w) __attribute__((always_inline)) {
         const int64_t k0 = s * KS;
         const uint8_t *const pb = codes + k0 * pad;
         const float *const ps = scales + k0 + octet * 8;
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            wb[j] = *(const uint32_t *)(pb + (int64_t)j * pad + b_off);
-            sb[j] = ps[j];
+            w.b[j] = *(const uint32_t *)(pb + (int64_t)j * pad + b_off);
+            w.s[j] = ps[j];
         }
         if constexpr (TRANS) {
             const uint16_t *const pa = a + k0 * lda + m0;
 #pragma unroll
-            for (int j = 0; j < 8; j++) wt[j] = *(const u32x2_any *)(pa + (int64_t)j * lda + t_off);
+            for (int j = 0; j < 8; j++) w.t[j] = *(const u32x2_any *)(pa + (int64_t)j * lda + t_off);
         } else {
             const uint16_t *const pa = a + m0 * lda + k0;
 #pragma unroll
-            for (int i = 0; i < 4; i++) wa[i] = *(const u32x4_any *)(pa + s_off[i]);
+            for (int i = 0; i < 4; i++) w.a[i] = *(const u32x4_any *)(pa + s_off[i]);
         }
     };
-    // the last ones, element by element where need be; rows past the end are zeros
-    auto load_last = [&](int64_t s) __attribute__((always_inline)) {
-        const int64_t k0 = s * KS;
-        const int left = (int)min(K - k0, (int64_t)KS);
+    // the last ones: rows past the end repeat the last one and become zeros.  No branch that
+    // differs between lanes, so that the loads are in flight together.
+    auto load_last = [&](int64_t s, Loaded &w) __attribute__((always_inline)) {
+        const int64_t k0 = s * KS, last_k = K - 1;
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            const bool in = (int)octet * 8 + j < left;
-            wb[j] = in ? *(const uint32_t *)(codes + (k0 + j) * pad + b_off) : 0;
-            sb[j] = in ? scales[k0 + octet * 8 + j] : 0;
-            if constexpr (TRANS) {
-                const uint16_t *const p = a + (k0 + j) * lda + m0 + t_off;
-                wt[j] = u32x2_t{0, 0};
-                const int width = in ? (int)(m_rows - a_col) : 0;
-                if (width > 0) wt[j].x = p[0];
-                if (width > 1) wt[j].x |= (uint32_t)p[1] << 16;
-                if (width > 2) wt[j].y = p[2];
-                if (width > 3) wt[j].y |= (uint32_t)p[3] << 16;
-            }
+            const int64_t k = k0 + octet * 8 + j, row = min(k, last_k);
+            w.b[j] = *(const uint32_t *)(codes + row * pad + (b_off - octet * 8 * pad));
+            const float mark = scales[row];
+            w.s[j] = k <= last_k ? mark : 0.0f;
         }
-        if constexpr (!TRANS) {
-            const int width = left - (int)a_oct * 8;
+        if constexpr (TRANS) {
+            const uint16_t *const pa = a + m0;
+            if (fours) {
+#pragma unroll
+                for (int j = 0; j < 8; j++) w.t[j] = *(const u32x2_any *)(pa + min(k0 + octet * 8 + j, last_k) * lda + a_col);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const uint16_t *const p = pa + min(k0 + octet * 8 + j, last_k) * lda;
+                    uint32_t h[4];
+#pragma unroll
+                    for (uint32_t e = 0; e < 4; e++) h[e] = p[min(a_col + e, m_rows - 1)];
+                    w.t[j] = u32x2_t{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                if (k0 + octet * 8 + j > last_k) w.t[j] = u32x2_t{0, 0};
+        } else {
+            const int64_t k = k0 + a_oct * 8;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                const uint16_t *const p = a + m0 * lda + k0 + s_off[i];
-                wa[i] = u32x4_t{0, 0, 0, 0};
+                const uint16_t *const p = a + m0 * lda + (s_off[i] - a_oct * 8);
+                if (K % 8 == 0) {
+                    w.a[i] = *(const u32x4_any *)(p + min(k, K - 8));
+                    if (k > last_k) w.a[i] = u32x4_t{0, 0, 0, 0};
+                } else {
+                    w.a[i] = u32x4_t{0, 0, 0, 0};
 #pragma unroll
-                for (int e = 0; e < 8; e++)
-                    if (e < width) wa[i][e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+                    for (int e = 0; e < 8; e++) {
+                        const uint32_t h = p[min(k + e, last_k)];
+                        w.a[i][e / 2] |= k + e <= last_k ? h << (16 * (e & 1)) : 0;
+                    }
+                }
             }
         }
     };
     typedef __attribute__((address_space(3))) uint8_t lds_byte;
-    lds_byte *const base = (lds_byte *)lds;
+    lds_byte *const base = (lds_byte *)lds + team * 2 * G::slot;
     typedef __attribute__((address_space(3))) u32x4_t lds_piece;
-    auto write = [&](uint32_t slot) __attribute__((always_inline)) {
+    auto write = [&](uint32_t slot, const Loaded &w) __attribute__((always_inline)) {
         lds_byte *const to = base + slot * G::slot;
         if constexpr (TRANS) {
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                u32x4_t w;
+                u32x4_t v;
 #pragma unroll
                 for (int j = 0; j < 4; j++)
-                    w[j] = __builtin_amdgcn_perm(e < 2 ? wt[2 * j + 1].x : wt[2 * j + 1].y, e < 2 ? wt[2 * j].x : wt[2 * j].y,
+                    v[j] = __builtin_amdgcn_perm(e < 2 ? w.t[2 * j + 1].x : w.t[2 * j + 1].y, e < 2 ? w.t[2 * j].x : w.t[2 * j].y,
                                                  e & 1 ? 0x07060302u : 0x05040100u);
-                *(lds_piece *)(to + G::at(col + e, octet)) = w;
+                *(lds_piece *)(to + G::at(col + e, octet)) = v;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; i++) *(lds_piece *)(to + G::at(a_row + i * row_step, a_oct)) = wa[i];
+            for (int i = 0; i < 4; i++) *(lds_piece *)(to + G::at(a_row + i * row_step, a_oct)) = w.a[i];
         }
         static_for<4>([&](auto E) __attribute__((always_inline)) {
             constexpr int e = E;
-            u32x4_t w;
+            u32x4_t v;
 #pragma unroll
             for (int j = 0; j < 4; j++)
-                w[j] = narrow2<AT>(cvt_sbyte<e>(wb[2 * j]) * sb[2 * j], cvt_sbyte<e>(wb[2 * j + 1]) * sb[2 * j + 1]);
-            *(lds_piece *)(to + G::TM * G::row + G::at(col + e, octet)) = w;
+                v[j] = narrow2<AT>(cvt_sbyte<e>(w.b[2 * j]) * w.s[2 * j], cvt_sbyte<e>(w.b[2 * j + 1]) * w.s[2 * j + 1]);
+            *(lds_piece *)(to + G::TM * G::row + G::at(col + e, octet)) = v;
         });
     };
 
@@ -201,34 +226,62 @@ __global__ __launch_bounds__(G::threads, 2) void k_int8_mixed(
         }
     };
 
-    // the stages of `load`, and then those of load_last
-    const int64_t whole_k = min(max((K - beyond) / KS, first), last);
-    auto stages = [&](int64_t from, int64_t to, auto body) __attribute__((always_inline)) {
-        // body(s, how to load the stage after the next: 0 not at all, 1 load, 2 load_last)
-        int64_t s = from;
-        for (; s + 2 < whole_k; s++) body(s, std::integral_constant<int, 1>{});
-        for (; s + 2 < to; s++) body(s, std::integral_constant<int, 2>{});
-        for (; s < to; s++) body(s, std::integral_constant<int, 0>{});
+    // the team's turns: stage first + TEAMS i + team.  Those of `load` come first, then those of
+    // load_last.
+    constexpr int D = G::AHEAD;
+    const int64_t mine = first + team, whole_k = min((K - beyond) / KS, last);
+    auto fill = [&](int64_t s, Loaded &w) __attribute__((always_inline)) {
+        if (s < whole_k) load(s, w);
+        else if (s < last) load_last(s, w);
     };
-    auto fill = [&](int64_t s) __attribute__((always_inline)) {
-        if (s < whole_k) load(s);
-        else load_last(s);
+    // stage s, in slot P: the next one is written, the one D turns after it loaded
+    auto stage = [&](int64_t s, auto P, auto MAIN) __attribute__((always_inline)) {
+        Loaded &w = regs[(D - 1) & (P ^ 1)];
+        if (MAIN || s + TEAMS < last) write(P ^ 1, w);
+        if constexpr (MAIN) load(s + TEAMS * (1 + D), w);
+        else fill(s + TEAMS * (1 + D), w);
+        if (MAIN || s < last) multiply(P);
+        wait_lds_and_meet();
     };
     if (first < last) {
-        fill(first);
-        write(0);
-        if (first + 1 < last) fill(first + 1);
+        fill(mine, regs[0]);
+        if (mine < last) write(0, regs[0]);
+        static_for<D>([&](auto I) __attribute__((always_inline)) { fill(mine + TEAMS * (1 + I), regs[(1 + I) % D]); });
         wait_lds_and_meet();
-        auto next = [&](int64_t s, uint32_t slot, auto how) __attribute__((always_inline)) {
-            if (how != 0 || s + 1 < last) write(slot ^ 1);
-            if constexpr (how == 1) load(s + 2);
-            if constexpr (how == 2) load_last(s + 2);
-        };
-        stages(first, last, [&](int64_t s, auto how) __attribute__((always_inline)) {
-            const uint32_t slot = (uint32_t)(s - first) & 1;
-            next(s, slot, how);
-            multiply(slot);
-            wait_lds_and_meet();
+        int64_t s = first;                                   // of team 0, the longest
+        if constexpr (D == 1) {
+            uint32_t slot = 0;
+            for (; s + TEAMS * 3 <= whole_k; s += TEAMS, slot ^= 1) stage(s + team, slot, std::true_type{});
+            for (; s < last; s += TEAMS, slot ^= 1) stage(s + team, slot, std::false_type{});
+        } else {
+            using even = std::integral_constant<uint32_t, 0>;
+            using odd = std::integral_constant<uint32_t, 1>;
+            for (; s + TEAMS * (3 + D) <= whole_k; s += 2 * TEAMS) {
+                stage(s + team, even{}, std::true_type{});
+                stage(s + team + TEAMS, odd{}, std::true_type{});
+            }
+            for (; s < last; s += 2 * TEAMS) {
+                stage(s + team, even{}, std::false_type{});
+                if (s + TEAMS < last) stage(s + team + TEAMS, odd{}, std::false_type{});
+            }
+        }
+    }
+    if constexpr (TEAMS == 2) {
+        // the second team's sums to LDS; the first adds and stores them
+        typedef __attribute__((address_space(3))) f32x4_t lds_sums;
+        lds_byte *const at = (lds_byte *)lds + tid * 16;
+        static_for<FM * FN * 4>([&](auto I) __attribute__((always_inline)) {
+            constexpr int f = I / 4, q = I % 4;
+            const f32x16_t &v = acc[f / FN][f % FN];
+            if (team == 1) *(lds_sums *)(at + I * G::threads * 16) = f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        });
+        wait_lds_and_meet();
+        if (team == 1) return;
+        static_for<FM * FN * 4>([&](auto I) __attribute__((always_inline)) {
+            constexpr int f = I / 4, q = I % 4;
+            const f32x4_t v = *(const lds_sums *)(at + I * G::threads * 16);
+#pragma unroll
+            for (int e = 0; e < 4; e++) acc[f / FN][f % FN][4 * q + e] += v[e];
         });
     }
     const bool whole = m0 + G::TM <= M && n0 + G::TN <= N;
@@ -524,9 +577,10 @@ __global__ __launch_bounds__(kThreads) void k_int8_mixed_join(const float *__res
     store4<CT>(c, m * ldc + n, count, v);
 }
 
-using Tile256 = MixedTile<256, 256, 64, 2, 4>;
-using Tile128 = MixedTile<128, 128, 64, 2, 2>;
-using Tile64 = MixedTile<64, 64, 128, 2, 2>;
+using Tile256 = MixedTile<256, 256, 64, 2, 4, 1, 1>;
+using Tile128 = MixedTile<128, 128, 64, 2, 2, 2, 1>;
+using Tile64 = MixedTile<64, 64, 128, 2, 2, 1, 1>;
+using Tile64x2 = MixedTile<64, 64, 128, 2, 2, 1, 2>;
 
 struct MixedArgs {
     const uint16_t *a;
@@ -543,7 +597,7 @@ template <class G, int AT, bool TRANS, int CT, bool SLICED = false>
 hipError_t run(const MixedArgs &p, int slices = 1) {
     const int64_t mt = (p.M + G::TM - 1) / G::TM, nt = (p.N + G::TN - 1) / G::TN;
     const uint32_t pad = (uint32_t)((p.N + 127) / 128 * 128);
-    hipLaunchKernelGGL((k_int8_mixed<G, AT, TRANS, CT, SLICED>), dim3((unsigned)(mt * nt * slices)), dim3(G::threads), 0,
+    hipLaunchKernelGGL((k_int8_mixed<G, AT, TRANS, CT, SLICED>), dim3((unsigned)(mt * nt * slices)), dim3(G::threads * G::TEAMS), 0,
                        p.st, p.a, p.lda, p.codes, p.scales, p.M, p.N, p.K, pad, (uint32_t)slices, (uint32_t)mt,
                        (uint32_t)nt, p.c, p.ldc);
     return hipGetLastError();
@@ -562,12 +616,13 @@ hipError_t run_direct(const MixedArgs &p, int slices = 1) {
 
 // which form takes a product: the cheapest
 constexpr Form kForms[] = {
-    {64, 128, 512, 90, 140, 300},      // 1024 x 1024, K = 1024: 10.2 us, tiles of 128 18.5
-    {128, 64, 512, 100, 145, 400},     // 2048 x 2048, K = 2048: 37 us, tiles of 64 46, of 256 47
-    {256, 64, 256, 175, 205, 1000},    // 4096 x 4096, K = 4096: 138 us, tiles of 128 183
-    {256, 64, 256, 120, 180, 800},     // the same, aligned: 124 us
+    {64, 256, 256, 110, 130, 380},     // two teams; 512 x 512, K = 512: 6.1 us, one team 6.7
+    {64, 128, 512, 85, 130, 330},      // 1000 x 1500, K = 1000: 15 us, two teams 18.6, tiles of 128 18.8
+    {128, 64, 512, 85, 134, 400},      // 2048 x 2048, K = 2048: 33 us, tiles of 64 44, of 256 46
+    {256, 64, 256, 200, 215, 1000},    // 4000 x 4000, K = 300: 24 us, tiles of 128 29
+    {256, 64, 256, 120, 180, 800},     // an aligned a: 4096 x 4096, K = 4096 116 us, the form above 138
 };
-constexpr int kDirect = 3;
+constexpr int kPlain256 = 3, kDirect = 4;
 
 struct Choice {
     int form, slices;
@@ -578,15 +633,15 @@ struct Choice {
 Choice choose(int64_t M, int64_t N, int64_t K, bool aligned, bool slicing) {
     Choice best = {0, 1};
     int64_t least = INT64_MAX;
-    for (int f = 0; f < 4; f++) {
-        if (f == (aligned ? 2 : kDirect)) continue;
+    for (int f = 0; f < 5; f++) {
+        if (f == (aligned ? kPlain256 : kDirect)) continue;
         const Form &m = kForms[f];
         const int64_t tiles = m.tiles(M, N), stages = (K + m.stage - 1) / m.stage;
         if (tiles > kMaxGroups / 2) continue;
         for (int s = 1; s <= (slicing ? 16 : 1); s *= 2) {
             if (s > 1 && (K / s < 256 || tiles * s > m.resident + m.resident / 4)) break;
             int64_t price = m.price(tiles * s, (stages + s - 1) / s);
-            if (s > 1) price += 400 + (2 * s + 1) * M * N / 10000;             // 4 TB/s
+            if (s > 1) price += 550 + (2 * s + 1) * M * N / 10000;             // 4 TB/s
             if (price < least) {
                 least = price;
                 best = {f, s};
@@ -599,9 +654,10 @@ Choice choose(int64_t M, int64_t N, int64_t K, bool aligned, bool slicing) {
 template <int AT, bool TRANS, int CT, bool SLICED>
 hipError_t run_form(const MixedArgs &p, Choice which) {
     switch (which.form) {
-    case 0: return run<Tile64, AT, TRANS, CT, SLICED>(p, which.slices);
-    case 1: return run<Tile128, AT, TRANS, CT, SLICED>(p, which.slices);
-    case 2: return run<Tile256, AT, TRANS, CT, SLICED>(p, which.slices);
+    case 0: return run<Tile64x2, AT, TRANS, CT, SLICED>(p, which.slices);
+    case 1: return run<Tile64, AT, TRANS, CT, SLICED>(p, which.slices);
+    case 2: return run<Tile128, AT, TRANS, CT, SLICED>(p, which.slices);
+    case kPlain256: return run<Tile256, AT, TRANS, CT, SLICED>(p, which.slices);
     default: return run_direct<AT, TRANS, CT, SLICED>(p, which.slices);
     }
 }

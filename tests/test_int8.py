@@ -409,7 +409,7 @@ def test_streams_and_graph(gpu):
     x, w = values(300, 1000, "bf16", 1), values(520, 1000, "bf16", 2)
     long = values(64, 9000, "bf16", 3)
     dy = values(300, 520, "bf16", 4)
-    tall = torch.randn(1500, 64, device="cuda").to(torch.bfloat16)
+    tall = torch.randn(6000, 64, device="cuda").to(torch.bfloat16)
 
     def chain():
         a, b, c = qcp.int8_quantize(x), qcp.int8_quantize(w), qcp.int8_quantize(long)
@@ -420,7 +420,7 @@ def test_streams_and_graph(gpu):
                 qcp.int8_matmul_mixed(tall, *t, 64, transpose=True), qcp.int8_linear(x, w), qcp.int8_linear(x, b)]
     same = lambda p, q: torch.equal(p.view(torch.uint8), q.view(torch.uint8))  # noqa: E731
     lib = qcp.library()
-    assert lib.qcp_int8_matmul_work(64, 64, 9000) > 0 and lib.qcp_int8_mixed_work(64, 64, 1500) > 0
+    assert lib.qcp_int8_matmul_work(64, 64, 9000) > 0 and lib.qcp_int8_mixed_work(64, 64, 6000) > 0
     want = [t.clone() for t in chain()]
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -449,7 +449,7 @@ def test_streams_and_graph(gpu):
 def test_two_calls_at_once(gpu):
     """On two streams, each with its own scratch memory."""
     a, b = random_payload(64, 9000, 1), random_payload(128, 9000, 2)
-    dy, t = torch.randn(1500, 64, device="cuda").to(torch.bfloat16), random_payload(1500, 128, 3)
+    dy, t = torch.randn(6000, 64, device="cuda").to(torch.bfloat16), random_payload(6000, 128, 3)
     want = qcp.int8_matmul(*a, *b), qcp.int8_matmul_mixed(dy, *t, 128, transpose=True)
     torch.cuda.synchronize()
     streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
