@@ -315,10 +315,20 @@ __global__ __launch_bounds__(G::threads * G::TEAMS, 2) void k_int8_mixed(
 // of a and the scales past the end are made zeros in LDS.
 namespace direct {
 
-constexpr int kSide = 256, kStage = 64, kThreads8 = 512, kSlots = 3, FM = 8;
-constexpr uint32_t kCodesAt = kSide * kStage * 2, kScalesAt = kCodesAt + kSide * kStage, kSlot = kScalesAt + 256;
+constexpr int kStage = 64, kSlots = 3;
 constexpr int kCopies = 7;                                   // of a wave and stage
 constexpr int64_t kMaxLd = (int64_t)1 << 22;                 // 256 rows of a are within 32 bits
+
+// 32*FM x 32*NW of C per work-group of NW waves
+template <int FM_, int NW_> struct Tile {
+    static constexpr int FM = FM_, NW = NW_, TM = 32 * FM, TN = 32 * NW, threads = 64 * NW;
+    static constexpr uint32_t codes_at = TM * kStage * 2, scales_at = codes_at + TN * kStage, slot = scales_at + 256;
+    static constexpr uint32_t t_row = 2 * TM, t_pieces = TM / 8; // of a row of a transposed a, in LDS
+    static constexpr uint32_t b_row = TN, b_pieces = TN / 16;    // of a row of codes
+    static_assert(FM == NW && (NW == 8 || NW == 4), "7 copies a wave; the order of the pieces");
+    // what a piece of the payload's row k is moved by
+    __device__ static __forceinline__ uint32_t turn(uint32_t k) { return NW == 8 ? 2 * (k & 7) : k & 6; }
+};
 
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
@@ -335,11 +345,13 @@ template <int J>
 __device__ __forceinline__ float of_lane(float v) {
     return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x150 + J, 0xf, 0xf, true));
 }
-template <int AT, bool TRANS, int CT, bool SLICED>
-__global__ __launch_bounds__(kThreads8, 2) void k_int8_mixed_direct(
+template <class G, int AT, bool TRANS, int CT, bool SLICED>
+__global__ __launch_bounds__(G::threads, 2) void k_int8_mixed_direct(
     const uint16_t *__restrict__ a, int64_t lda, const uint8_t *__restrict__ codes, const float *__restrict__ scales,
     int64_t M, int64_t N, int64_t K, uint32_t pad, uint32_t slices, uint32_t m_tiles, uint32_t n_tiles, uint32_t groups,
     void *__restrict__ c, int64_t ldc) {
+    constexpr int FM = G::FM;
+    constexpr uint32_t kSlot = G::slot, kCodesAt = G::codes_at, kScalesAt = G::scales_at;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * kSlot];
     const int tid = (int)__builtin_amdgcn_workitem_id_x();
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane(tid >> 6);
@@ -362,15 +374,16 @@ __global__ __launch_bounds__(kThreads8, 2) void k_int8_mixed_direct(
         }
         stages = (uint32_t)count;
         const TilePlace at = tile_place(t, m_tiles, n_tiles);
-        m0 = (int64_t)at.m * kSide;
-        n0 = (int64_t)at.n * kSide;
-        m_rows = (uint32_t)min(M - m0, (int64_t)kSide);
+        m0 = (int64_t)at.m * G::TM;
+        n0 = (int64_t)at.n * G::TN;
+        m_rows = (uint32_t)min(M - m0, (int64_t)G::TM);
         k_next = first * kStage;
         k_end = min((first + count) * kStage, K);
         to_slot = 0;
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-            const uint32_t row = 8 * wave + 4 * i + (lane >> 4), piece = (lane & 15) ^ (2 * (row & 7));
+            const uint32_t row = kStage / G::NW * wave + (kStage / G::NW / 2) * i + lane / G::b_pieces;
+            const uint32_t piece = lane % G::b_pieces ^ G::turn(row);
             b_voff[i] = row * pad + (uint32_t)min(n0 + 16 * piece, (int64_t)pad - 16);
         }
     };
@@ -385,7 +398,8 @@ __global__ __launch_bounds__(kThreads8, 2) void k_int8_mixed_direct(
                         buffer_of(codes + k_next * pad, (uint64_t)(K - k_next) * pad), 0);
         } else if constexpr (TRANS) {
             constexpr int i = n - 3;
-            const uint32_t row = 8 * wave + 2 * i + half, piece = r ^ (4 * (2 * (i & 1) + half));
+            const uint32_t row = kStage / G::NW * wave + (kStage / G::NW / 4) * i + lane / G::t_pieces;
+            const uint32_t piece = lane % G::t_pieces ^ (4 * (row & 3));
             copy_to_lds(to + wave * 4096 + i * 1024, row * (uint32_t)lda * 2 + piece * 16,
                         buffer_of(a + k_next * lda + m0, (uint64_t)((K - 1 - k_next) * lda + (M - m0)) * 2), 0);
         } else {
@@ -402,9 +416,9 @@ __global__ __launch_bounds__(kThreads8, 2) void k_int8_mixed_direct(
     };
 
     // where this lane reads in slot 0
-    const uint32_t a_at = base + (TRANS ? (8 * half + (t16 >> 2)) * 512 + ((4 * (t16 >> 2) + 2 * side + ((t16 & 3) >> 1)) * 16) + 8 * (t16 & 1)
+    const uint32_t a_at = base + (TRANS ? (8 * half + (t16 >> 2)) * G::t_row + ((4 * (t16 >> 2) + 2 * side + ((t16 & 3) >> 1)) * 16) + 8 * (t16 & 1)
                                         : r * 128 + ((half ^ ((r >> 1) & 7)) * 16));
-    const uint32_t b_at = base + kCodesAt + (8 * half + (t16 >> 1)) * 256 + ((2 * (wave ^ (t16 >> 1)) + side) * 16) + 8 * (t16 & 1);
+    const uint32_t b_at = base + kCodesAt + (8 * half + (t16 >> 1)) * G::b_row + (((2 * wave + side) ^ G::turn(t16 >> 1)) * 16) + 8 * (t16 & 1);
     const uint32_t s_at = base + kScalesAt + 4 * (16 * (t16 >> 3) + 8 * half + (t16 & 7));
 
     f32x16_t acc[FM];
@@ -416,13 +430,13 @@ __global__ __launch_bounds__(kThreads8, 2) void k_int8_mixed_direct(
         constexpr int i = I, q = Q;
         if constexpr (TRANS) {
             const uint32_t at = (a_at ^ (64 * (i & 3))) + from;
-            const u32x2_t lo = read_tr16(at + 256 * (i >> 2) + 8192 * q), hi = read_tr16(at + 256 * (i >> 2) + 8192 * q + 2048);
+            const u32x2_t lo = read_tr16(at + 256 * (i >> 2) + 16 * G::t_row * q), hi = read_tr16(at + 256 * (i >> 2) + 16 * G::t_row * q + 4 * G::t_row);
             fa[i] = u32x4_t{lo.x, lo.y, hi.x, hi.y};
         } else {
             fa[i] = lds16((a_at ^ (32 * q)) + from + 4096 * i);
         }
     };
-    auto read_codes = [&](auto Q) __attribute__((always_inline)) { raw = read_tr8(b_at + from + 4096 * Q); };
+    auto read_codes = [&](auto Q) __attribute__((always_inline)) { raw = read_tr8(b_at + from + 16 * G::b_row * Q); };
     auto read_marks = [&]() __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < 2; i++) mark[i] = __uint_as_float(lds4(s_at + from + 128 * i));
@@ -442,8 +456,8 @@ __global__ __launch_bounds__(kThreads8, 2) void k_int8_mixed_direct(
         typedef __attribute__((address_space(3))) u32x4_t lds_piece;
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const uint32_t n = i * kThreads8 + tid;
-            const uint32_t k = TRANS ? n / 32 : n % 8 * 8;
+            const uint32_t n = i * G::threads + tid;
+            const uint32_t k = TRANS ? n / G::t_pieces : n % 8 * 8;
             const uint32_t to = TRANS ? n * 16 : n / 8 * 128 + ((n ^ (n / 16)) & 7) * 16;
             if (k >= left) *(lds_piece *)(at + to) = u32x4_t{0, 0, 0, 0};
         }
@@ -471,11 +485,16 @@ __global__ __launch_bounds__(kThreads8, 2) void k_int8_mixed_direct(
                         if constexpr (then == 0) read_marks();
                     }
                     read_a(I, integral_constant<int, then>{});
-                    if constexpr (i >= 4) decode(integral_constant<int, i - 4>{}, integral_constant<int, then>{}, fn);
+                    if constexpr (i >= FM / 2)
+                        static_for<8 / FM>([&](auto J) __attribute__((always_inline)) {
+                            decode(integral_constant<int, (i - FM / 2) * (8 / FM) + J>{}, integral_constant<int, then>{}, fn);
+                        });
                 }
-                if constexpr (COPY && q == 3) {
-                    if constexpr (i >= 1) copy(integral_constant<int, i - 1>{});
-                }
+                if constexpr (COPY && q == 3)
+                    static_for<8 / FM>([&](auto J) __attribute__((always_inline)) {
+                        constexpr int n = i * (8 / FM) + J - 1;
+                        if constexpr (n >= 0) copy(integral_constant<int, n>{});
+                    });
                 __builtin_amdgcn_sched_barrier(0);
             });
             if constexpr (more) fb = fn;
@@ -532,7 +551,7 @@ __global__ __launch_bounds__(kThreads8, 2) void k_int8_mixed_direct(
 
         // the next tile's first copies go out before this one's results
         const int64_t m_done = m0 + r, n_done = n0 + 32 * wave;
-        const bool whole = m0 + kSide <= M && n0 + kSide <= N;
+        const bool whole = m0 + G::TM <= M && n0 + G::TN <= N;
         void *const to = SLICED ? (float *)c + slice * M * N : c;
         tile += groups;
         const bool more = tile < tiles;
@@ -603,12 +622,12 @@ hipError_t run(const MixedArgs &p, int slices = 1) {
     return hipGetLastError();
 }
 
-template <int AT, bool TRANS, int CT, bool SLICED = false>
-hipError_t run_direct(const MixedArgs &p, int slices = 1) {
-    const int64_t mt = (p.M + direct::kSide - 1) / direct::kSide, nt = (p.N + direct::kSide - 1) / direct::kSide;
+template <class G, int AT, bool TRANS, int CT, bool SLICED>
+hipError_t run_direct(const MixedArgs &p, int slices, int resident) {
+    const int64_t mt = (p.M + G::TM - 1) / G::TM, nt = (p.N + G::TN - 1) / G::TN;
     const uint32_t pad = (uint32_t)((p.N + 127) / 128 * 128);
-    const unsigned groups = (unsigned)std::min<int64_t>(mt * nt * slices, kCUs);
-    hipLaunchKernelGGL((direct::k_int8_mixed_direct<AT, TRANS, CT, SLICED>), dim3(groups), dim3(direct::kThreads8), 0, p.st,
+    const unsigned groups = (unsigned)std::min<int64_t>(mt * nt * slices, resident);
+    hipLaunchKernelGGL((direct::k_int8_mixed_direct<G, AT, TRANS, CT, SLICED>), dim3(groups), dim3(G::threads), 0, p.st,
                        p.a, p.lda, p.codes, p.scales, p.M, p.N, p.K, pad, (uint32_t)slices, (uint32_t)mt, (uint32_t)nt,
                        groups, p.c, p.ldc);
     return hipGetLastError();
@@ -620,9 +639,10 @@ constexpr Form kForms[] = {
     {64, 128, 512, 85, 130, 330},      // 1000 x 1500, K = 1000: 15 us, two teams 18.6, tiles of 128 18.8
     {128, 64, 512, 85, 134, 400},      // 2048 x 2048, K = 2048: 33 us, tiles of 64 44, of 256 46
     {256, 64, 256, 200, 215, 1000},    // 4000 x 4000, K = 300: 24 us, tiles of 128 29
-    {256, 64, 256, 120, 180, 800},     // an aligned a: 4096 x 4096, K = 4096 116 us, the form above 138
+    {128, 64, 512, 66, 112, 400},      // an aligned a: 2048 x 2048, K = 2048 26 us, without copies to LDS 30
+    {256, 64, 256, 120, 170, 800},     // the same: 4096 x 4096, K = 4096 119 us, the form above 146, tiles of 128 168
 };
-constexpr int kPlain256 = 3, kDirect = 4;
+constexpr int kPlain256 = 3, kDirect128 = 4, kDirect256 = 5;
 
 struct Choice {
     int form, slices;
@@ -633,15 +653,15 @@ struct Choice {
 Choice choose(int64_t M, int64_t N, int64_t K, bool aligned, bool slicing) {
     Choice best = {0, 1};
     int64_t least = INT64_MAX;
-    for (int f = 0; f < 5; f++) {
-        if (f == (aligned ? kPlain256 : kDirect)) continue;
+    for (int f = 0; f <= kDirect256; f++) {
+        if (aligned ? f == kPlain256 : f >= kDirect128) continue;
         const Form &m = kForms[f];
         const int64_t tiles = m.tiles(M, N), stages = (K + m.stage - 1) / m.stage;
         if (tiles > kMaxGroups / 2) continue;
         for (int s = 1; s <= (slicing ? 16 : 1); s *= 2) {
             if (s > 1 && (K / s < 256 || tiles * s > m.resident + m.resident / 4)) break;
             int64_t price = m.price(tiles * s, (stages + s - 1) / s);
-            if (s > 1) price += 550 + (2 * s + 1) * M * N / 10000;             // 4 TB/s
+            if (s > 1) price += 550 + (2 * s + 1) * M * N / 12000;             // 4.8 TB/s
             if (price < least) {
                 least = price;
                 best = {f, s};
@@ -658,7 +678,8 @@ hipError_t run_form(const MixedArgs &p, Choice which) {
     case 1: return run<Tile64, AT, TRANS, CT, SLICED>(p, which.slices);
     case 2: return run<Tile128, AT, TRANS, CT, SLICED>(p, which.slices);
     case kPlain256: return run<Tile256, AT, TRANS, CT, SLICED>(p, which.slices);
-    default: return run_direct<AT, TRANS, CT, SLICED>(p, which.slices);
+    case kDirect128: return run_direct<direct::Tile<4, 4>, AT, TRANS, CT, SLICED>(p, which.slices, kForms[kDirect128].resident);
+    default: return run_direct<direct::Tile<8, 8>, AT, TRANS, CT, SLICED>(p, which.slices, kForms[kDirect256].resident);
     }
 }
 

@@ -18,6 +18,7 @@ from .mxfp4 import _matrix, _pad, _result, _same_gpu
 
 _u8, _f32 = torch.uint8, torch.float32
 _HALF = (torch.float16, torch.bfloat16)
+_UNSLICED = 63 * 128              # slices of K begin at 64 stages of 128
 
 
 def _payload(codes, scales, what: str):
@@ -68,12 +69,13 @@ def int8_quantize(x: torch.Tensor, codes=None, scales=None):
     rows, cols = x.shape
     x, ld = _rows_of(x)
     P, index = _pad(cols), x.get_device()
-    for t, what, kinds, shape in ((codes, "codes", _U8, (rows, P)), (scales, "scales", _F32, (rows,))):
-        if t is not None:
-            _need(t, what, kinds, 0)
-            if tuple(t.shape) != shape:
-                raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
-            _same_gpu(index, x, t)
+    if codes is not None or scales is not None:
+        for t, what, kinds, shape in ((codes, "codes", _U8, (rows, P)), (scales, "scales", _F32, (rows,))):
+            if t is not None:
+                _need(t, what, kinds, 0)
+                if tuple(t.shape) != shape:
+                    raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
+                _same_gpu(index, x, t)
     if index < 0:
         _dev(x)
     if codes is None:
@@ -122,7 +124,9 @@ def _scratch(name: str, like, *sizes):
 
 
 def _multiply(index, a, sa, b, sb, M, N, K, c):
-    t, at, size = _scratch("qcp_int8_matmul_work", c, M, N, K)
+    """The product into c; scratch memory is asked for only where the library may have a use
+    for it, which it never has for rows of up to _UNSLICED codes."""
+    t, at, size = _scratch("qcp_int8_matmul_work", c, M, N, K) if K > _UNSLICED else (None, None, 0)
     _enqueue("int8_matmul", index, a, sa, b, sb, M, N, K, c.data_ptr(), DTYPES[c.dtype], N, at, size)
 
 
@@ -145,7 +149,8 @@ def int8_matmul_mixed(a: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
     if dtype not in (a.dtype, _f32):
         raise ValueError(f"dtype {dtype}, expected {a.dtype} or {_f32}")
     c = _result(out, M, cols, dtype, codes)
-    _same_gpu(index, codes, a, c)
+    if index < 0 or a.get_device() != index or out is not None:
+        _same_gpu(index, codes, a, c)
     _mixed(index, a, codes.data_ptr(), scales.data_ptr(), M, cols, K, transpose, c)
     return c
 

@@ -716,6 +716,15 @@ def test_c_entry_of_the_product_refuses(lib):
         assert mul(**bad) == EALIGN, bad
 
 
+def test_rows_below_the_bound_have_no_slices(lib):
+    """The binding asks for scratch memory only above this length."""
+    from quantized_collective_payloads_amd.int8 import _UNSLICED
+    work = lib.qcp_int8_matmul_work
+    shapes = [(M, N) for M in (17, 32, 33, 64, 128, 200, 500, 2048, 8192) for N in (1, 16, 64, 500, 700, 2048, 4096, 8192)]
+    assert not any(work(M, N, K) for M, N in shapes for K in (128, 1000, 4096, _UNSLICED - 127, _UNSLICED))
+    assert work(64, 64, _UNSLICED + 1) > 0
+
+
 def test_c_entry_of_the_mixed_product_refuses(lib):
     work = lib.qcp_int8_mixed_work
     need = work(64, 64, 9000)
