@@ -358,6 +358,19 @@ int int8_matmul(const uint8_t *a_codes, const float *a_scales, const uint8_t *b_
 int64_t qcp_int8_matmul_work(int64_t M, int64_t N, int64_t K);
 
 /*
+ * A linear layer for few rows (the tokens of a decoding step) in one launch: y = Q(x) W^T,
+ * what int8_quantize of x and int8_matmul give.
+ *   x          M x K elements of type xt (QCP_F16 or QCP_BF16), rows ldx apart
+ *   w_codes, w_scales   the payload of W, N rows of K codes
+ *   y          M x N of type xt, rows ldy apart
+ * Where qcp_int8_linear_rows_fit(M, N, K) is 0 (more than 8 rows, rows too long for a
+ * work-group to hold, or a product that is as quick in two launches), QCP_EUNSUPPORTED.
+ */
+int int8_linear_rows(const void *x, int xt, int64_t M, int64_t K, int64_t ldx, const uint8_t *w_codes,
+                     const float *w_scales, int64_t N, void *y, int64_t ldy, void *stream);
+int qcp_int8_linear_rows_fit(int64_t M, int64_t N, int64_t K);
+
+/*
  * Product of a 16-bit matrix with an INT8 payload over whose rows is summed, as a
  * backward pass has them: c[m, n] = sum over k of a[m, k] * x[k, n], where x[k, n] is
  * what int8_dequantize gives for the payload in a's type.  Accumulated in fp32, rounded

@@ -90,6 +90,8 @@ def library():
             "int8_quantize": [p, ci, i64, i64, i64, p, p, p],
             "int8_dequantize": [p, p, i64, i64, p, ci, i64, p],
             "int8_matmul": [p, p, p, p, i64, i64, i64, p, ci, i64, p, i64, p],
+            "int8_linear_rows": [p, ci, i64, i64, i64, p, p, i64, p, i64, p],
+            "qcp_int8_linear_rows_fit": [i64, i64, i64],
             "int8_matmul_mixed": [p, ci, i64, i32, p, p, i64, i64, i64, p, ci, i64, p, i64, p],
             "qcp_aquavit_level": [i64, i64, ctypes.c_double, ctypes.c_double,
                                   ctypes.POINTER(i32), ctypes.POINTER(i32)],

@@ -7,6 +7,7 @@
 // Which 16 of K a lane brings is free as long as both operands agree.
 #include <algorithm>
 
+#include "qcp_int8.h"
 #include "qcp_matmul.h"
 #include "qcp_ops.h"
 
@@ -412,6 +413,126 @@ hipError_t run_rows(const uint8_t *a, const float *as, const uint8_t *b, const f
     return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// The layer for few rows, in one launch: y = Q(x) W^T, up to 8 rows of x in 16 bits.
+// ---------------------------------------------------------------------------
+// Bound: reading W once; what a launch of its own for Q(x) takes, 2.6 us of the GPU and 6 of the
+// host, is as much as a small product.  Every work-group makes Q(x) for itself, in LDS: a team
+// of its lanes keeps a row in registers, V pieces a lane, as the quantize does and with its
+// results.  Its first loads of W go out before.
+//
+// LDS holds a row's pieces of 16 bytes in the order piece ^ (row % 8), so that the reads of a
+// piece of 8 rows touch different banks.
+constexpr int kFewWaves = 8, kFewThreads = 64 * kFewWaves, kFewBytes = 48 << 10;
+
+template <int XT, int V>
+__global__ __launch_bounds__(kFewThreads) void k_int8_linear_rows(const void *__restrict__ x, int64_t ldx, int M, int64_t K,
+                                                                  const uint8_t *__restrict__ b,
+                                                                  const float *__restrict__ bs, int64_t N,
+                                                                  uint32_t granules, void *__restrict__ y, int64_t ldy) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t codes[];          // M rows of 64 * granules bytes
+    __shared__ i32x4_t sums[kFewWaves][64];
+    __shared__ uint32_t maxima[kFewWaves];
+    __shared__ float marks[8];
+    const uint32_t tid = __builtin_amdgcn_workitem_id_x(), P = granules * 64;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(tid >> 6)), lane = lane_id();
+    const int row = lane & 15, quarter = lane >> 4;
+    const int64_t n0 = (int64_t)__builtin_amdgcn_workgroup_id_x() * 16;
+    const uint8_t *const pb = b + min(n0 + row, N - 1) * P + 16 * quarter;
+    auto load = [&](uint32_t g, i32x4_t (&v)[4]) __attribute__((always_inline)) {
+#pragma unroll
+        for (uint32_t t = 0; t < 4; t++)
+            v[t] = g + t < granules ? *(const i32x4_t *)(pb + (uint64_t)(g + t) * 64) : i32x4_t{0, 0, 0, 0};
+    };
+    i32x4_t fb[4];
+    load(4 * wave, fb);
+
+    // 1, 2, 4 or 8 teams of at least a wave, a row each
+    const uint32_t teams = M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : 8, lanes = kFewThreads / teams;
+    const uint32_t m = tid / lanes, t = tid % lanes, pieces = P / 8;
+    const bool mine = m < (uint32_t)M;
+    const uint8_t *const from = (const uint8_t *)x + (mine ? m : 0) * ldx * 2;
+    u32x4_t v[V];
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < V; k++) {
+        const int64_t p = k * lanes + t, left = mine ? K - p * 8 : 0;
+        v[k] = u32x4_t{0, 0, 0, 0};
+        if (left > 0) v[k] = load_piece<XT>(from + p * 16, left > 8 ? 8 : (int)left);
+    }
+#pragma unroll
+    for (int k = 0; k < V; k++) top = largest<XT>(top, v[k]);
+    top = group_max_u32<64>(as_f32_bits<XT>(top));
+    if (lane == 0) maxima[wave] = top;
+    __syncthreads();
+    const uint32_t first = wave & ~(lanes / 64 - 1);
+    for (uint32_t w = 0; w < lanes / 64; w++) top = max(top, maxima[first + w]);
+    BlockScale<INT8> s;
+    const bool finite = row_scale(top, s);
+    const RecipBracket rb = recip_bracket(s.r);
+#pragma unroll
+    for (int k = 0; k < V; k++) {
+        const uint32_t p = k * lanes + t;
+        if (!mine || p >= pieces) continue;
+        u32x2_t c = {0, 0};
+        if (finite) c = encode<XT>(v[k], s, rb);
+        *(u32x2_t *)(codes + m * P + ((p / 2) ^ (m & 7)) * 16 + 8 * (p & 1)) = c;
+    }
+    if (mine && t == 0) marks[m] = scale_value(finite, s);
+    __syncthreads();
+
+    // rows past the end repeat the last one and are not stored
+    const uint32_t ra = min(row, M - 1);
+    const uint8_t *const pa = codes + ra * P;
+    i32x4_t acc = {};
+    for (uint32_t g = 4 * wave; g < granules; g += 4 * kFewWaves) {
+        i32x4_t next[4];
+        load(g + 4 * kFewWaves, next);
+#pragma unroll
+        for (uint32_t t4 = 0; t4 < 4; t4++) {
+            // past the end of the row fb is zeros
+            const uint32_t piece = 4 * min(g + t4, granules - 1) + quarter;
+            const i32x4_t fa = *(const i32x4_t *)(pa + (piece ^ (ra & 7)) * 16);
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[t4], fa, acc, 0, 0, 0);
+        }
+#pragma unroll
+        for (int t4 = 0; t4 < 4; t4++) fb[t4] = next[t4];
+    }
+    sums[wave][lane] = acc;
+    __syncthreads();
+    if (wave != 0) return;
+    // a lane's 4 sums are consecutive n of one m
+#pragma unroll
+    for (int w = 1; w < kFewWaves; w++) acc += sums[w][lane];
+    const int64_t n = n0 + 4 * quarter;
+    if (row >= M || n >= N) return;
+    const int count = N - n < 4 ? (int)(N - n) : 4;
+    float r[4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        if (j < count) r[j] = scaled<false>(acc[j], marks[row], bs[n + j]);
+    store4<XT>(y, row * ldy + n, count, r);
+}
+
+template <int XT, int V>
+hipError_t run_few(const void *x, int64_t ldx, int64_t M, int64_t K, const uint8_t *b, const float *bs, int64_t N,
+                   int64_t granules, void *y, int64_t ldy, hipStream_t st) {
+    hipLaunchKernelGGL((k_int8_linear_rows<XT, V>), dim3((unsigned)((N + 15) / 16)), dim3(kFewThreads),
+                       (unsigned)(M * granules * 64), st, x, ldx, (int)M, K, b, bs, N, (uint32_t)granules, y, ldy);
+    return hipGetLastError();
+}
+
+template <int XT>
+hipError_t few_rows(const void *x, int64_t ldx, int64_t M, int64_t K, const uint8_t *b, const float *bs, int64_t N,
+                    int64_t stages, void *y, int64_t ldy, hipStream_t st) {
+    const int64_t granules = 2 * stages, teams = M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : 8;
+    const int64_t each = (granules * 8 + kFewThreads / teams - 1) / (kFewThreads / teams);   // pieces a lane
+    if (each <= 1) return run_few<XT, 1>(x, ldx, M, K, b, bs, N, granules, y, ldy, st);
+    if (each <= 4) return run_few<XT, 4>(x, ldx, M, K, b, bs, N, granules, y, ldy, st);
+    if (each <= 16) return run_few<XT, 16>(x, ldx, M, K, b, bs, N, granules, y, ldy, st);
+    return hipErrorInvalidValue;
+}
+
 // which form takes a product that is not one for few rows: the cheapest
 constexpr Form kForms[] = {
     {64, 128, 512, 29, 44, 300},       // 512 x 4096, K = 4096: 18.7 us, tiles of 128 24.4
@@ -459,6 +580,23 @@ int int8_matmul_slices(int64_t M, int64_t N, int64_t stages) {
     const int64_t rows = (M + 63) / 64, cols = (N + 63) / 64;
     if (M <= 16 || N < 1 || rows > 128 || cols > 128 || rows * cols > 128 || stages < 64) return 1;
     return (int)std::min<int64_t>(8, 256 / (rows * cols));
+}
+
+// Up to 8 rows that fit LDS, where the work that every work-group repeats takes no more than the
+// launch that it saves (us of the GPU in one launch and in two, warm: 1 x 14336, K = 4096 15.5
+// and 16.2; 1 x 4096, K = 4096 6.6 and 7.6; 8 x 4096, K = 4096 9.1 and 8.5, but 6 us less of the
+// host; 8 x 14336, K = 4096 24.7 and 18.3).
+bool int8_linear_few(int64_t M, int64_t N, int64_t stages) {
+    const int64_t teams = M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : 8, P = stages * 128;
+    if (M < 1 || M > 8 || stages < 1 || teams * P > kFewBytes || (N + 15) / 16 > kMaxGroups / 2) return false;
+    return M == 1 || N <= ((int64_t)1 << 27) / (M * P);
+}
+
+hipError_t launch_int8_linear_rows(const void *x, int xt, int64_t ldx, int64_t M, int64_t K, const uint8_t *b,
+                                   const float *bs, int64_t N, int64_t stages, void *y, int64_t ldy, hipStream_t st) {
+    if (xt == BF16) return few_rows<BF16>(x, ldx, M, K, b, bs, N, stages, y, ldy, st);
+    if (xt == F16) return few_rows<F16>(x, ldx, M, K, b, bs, N, stages, y, ldy, st);
+    return hipErrorInvalidValue;
 }
 
 hipError_t launch_int8_matmul(const uint8_t *a, const float *as, const uint8_t *b, const float *bs, int64_t M,

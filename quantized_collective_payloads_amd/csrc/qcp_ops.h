@@ -57,6 +57,11 @@ int int8_matmul_slices(int64_t M, int64_t N, int64_t stages);
 hipError_t launch_int8_matmul(const uint8_t *a, const float *as, const uint8_t *b, const float *bs, int64_t M,
                               int64_t N, int64_t stages, void *c, int ct, int64_t ldc, int *work, hipStream_t st);
 
+// Y[M, N] = Q(x) B^T for few rows of 16 bits, in one launch; `few`: whether they are
+bool int8_linear_few(int64_t M, int64_t N, int64_t stages);
+hipError_t launch_int8_linear_rows(const void *x, int xt, int64_t ldx, int64_t M, int64_t K, const uint8_t *b,
+                                   const float *bs, int64_t N, int64_t stages, void *y, int64_t ldy, hipStream_t st);
+
 // C[M, N] = A X for a 16-bit A (transpose: given as [K, M]) and the payload of X [K, N];
 // see qcp_int8_mixed.hip.  work: null, or room for slices * M * N floats
 int int8_mixed_slices(int64_t M, int64_t N, int64_t K);

@@ -376,6 +376,30 @@ int64_t qcp_int8_matmul_work(int64_t M, int64_t N, int64_t K) {
     return slices > 1 ? 4 * slices * M * N : 0;
 }
 
+int int8_linear_rows(const void *x, int xt, int64_t M, int64_t K, int64_t ldx, const uint8_t *w_codes,
+                     const float *w_scales, int64_t N, void *y, int64_t ldy, void *stream) {
+    int64_t xb, yb, pad;
+    if (xt != QCP_F16 && xt != QCP_BF16) return QCP_EINVAL;
+    int rc = check_matrix(M, K, ldx, xt, &xb);
+    if (rc != QCP_OK) return rc;
+    rc = check_matrix(M, N, ldy, xt, &yb);
+    if (rc != QCP_OK) return rc;
+    if (K > kInt8MaxK) return QCP_EINVAL;
+    if (M == 0 || N == 0) return QCP_OK;
+    if (!int8_payload(N, K, &pad)) return QCP_EINVAL;
+    if (!qcp_int8_linear_rows_fit(M, N, K)) return QCP_EUNSUPPORTED;
+    if (!x || !y || !w_codes || !w_scales) return QCP_EINVAL;
+    if (!aligned16(w_codes) || !aligned16(w_scales) || (uintptr_t)x % 2 || (uintptr_t)y % 2) return QCP_EALIGN;
+    if (overlap(y, yb, x, xb) || overlap(y, yb, w_codes, N * pad) || overlap(y, yb, w_scales, N * 4)) return QCP_EINVAL;
+    return status_of(qcp::launch_int8_linear_rows(x, xt, ldx, M, K, w_codes, w_scales, N, pad / 128, y, ldy,
+                                                  (hipStream_t)stream));
+}
+
+int qcp_int8_linear_rows_fit(int64_t M, int64_t N, int64_t K) {
+    if (M < 1 || N < 1 || K < 1 || N > kMaxElems || K > kInt8MaxK) return 0;
+    return qcp::int8_linear_few(M, N, (K + 127) / 128) ? 1 : 0;
+}
+
 int int8_matmul_mixed(const void *a, int at, int64_t lda, int32_t transpose, const uint8_t *codes,
                       const float *scales, int64_t M, int64_t N, int64_t K, void *c, int ct, int64_t ldc,
                       void *work, int64_t work_bytes, void *stream) {

@@ -185,6 +185,17 @@ def _product(index, x, qx, w, O):
     return y
 
 
+def _frozen_product(index, x, codes, scales):
+    """The product of x's payload and a given one; for few rows in one launch."""
+    (T, I), O = x.shape, codes.shape[0]
+    if T <= 8 and library().qcp_int8_linear_rows_fit(T, O, I):
+        y = x.new_empty((T, O))
+        _enqueue("int8_linear_rows", index, x.data_ptr(), DTYPES[x.dtype], T, I, I, codes.data_ptr(), scales.data_ptr(),
+                 O, y.data_ptr(), O)
+        return y
+    return _product(index, x, _quantized(index, x), (codes.data_ptr(), scales.data_ptr()), O)
+
+
 def _backward(index, dy, payload, rows, cols, transpose, dtype):
     """dy times a payload, or its transpose times it, in `dtype`."""
     M = dy.shape[1 if transpose else 0]
@@ -227,10 +238,9 @@ class _FrozenLinear(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, codes, scales):
-        index, O = x.get_device(), codes.shape[0]
-        y = _product(index, x, _quantized(index, x), (codes.data_ptr(), scales.data_ptr()), O)
+        y = _frozen_product(x.get_device(), x, codes, scales)
         ctx.save_for_backward(codes, scales)
-        ctx.sizes = (x.shape[1], O)
+        ctx.sizes = (x.shape[1], codes.shape[0])
         return y
 
     @staticmethod
@@ -283,7 +293,9 @@ def int8_linear(x: torch.Tensor, weight) -> torch.Tensor:
         y = (_FrozenLinear if frozen else _Linear).apply(x2, *parts)
     else:
         index = x2.get_device()
-        qw = None if frozen else _quantized(index, parts[0])
-        w = tuple(t.data_ptr() for t in parts) if frozen else _at(qw, O, x2.shape[1])
-        y = _product(index, x2, _quantized(index, x2), w, O)
+        if frozen:
+            y = _frozen_product(index, x2, *parts)
+        else:
+            qw = _quantized(index, parts[0])
+            y = _product(index, x2, _quantized(index, x2), _at(qw, O, x2.shape[1]), O)
     return y if x.dim() == 2 else y.view(*x.shape[:-1], O)

@@ -503,6 +503,38 @@ def test_linear_and_its_gradients_match_the_formula(gpu, T, I, O, dt, kind):
 
 
 @GPU
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("I", [1, 100, 128, 1000, 4096, 6144, 6145, 12000, 20001, 49152, 49153])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 9])
+def test_linear_of_few_rows_is_the_quantize_and_the_product(gpu, T, I, dt):
+    """Up to 8 rows of a frozen layer take one launch where they fit, with the same bytes; rows of
+    zeros, with NaN and of any size among them."""
+    x = values(T, I, dt, T * I)
+    if T > 3:
+        x[3, I // 2] = float("nan")
+    for O in (1, 16, 70, 1001):
+        w = random_payload(O, I, O)
+        with torch.no_grad():
+            y = qcp.int8_linear(x, w)
+        want = qcp.int8_matmul(*qcp.int8_quantize(x), *w, dtype=DT[dt])
+        assert torch.equal(y.view(torch.int16), want.view(torch.int16)), (O, qcp.library().qcp_int8_linear_rows_fit(T, O, I))
+
+
+@GPU
+def test_c_entry_for_few_rows_takes_strides(gpu):
+    """Rows of x and y apart; what lies between them is neither read into the sums nor written."""
+    big = torch.full((5, 700), float("nan"), device="cuda").to(torch.bfloat16)
+    x = values(5, 300, "bf16", 1)
+    big[:, 3:303] = x
+    w = random_payload(90, 300, 2)
+    y = torch.full((5, 100), 7.0, device="cuda", dtype=torch.bfloat16)
+    rc = qcp.library().int8_linear_rows(big[:, 3:].data_ptr(), 2, 5, 300, 700, w[0].data_ptr(), w[1].data_ptr(), 90, y.data_ptr(), 100,
+                                        torch.cuda.current_stream().cuda_stream)
+    want = qcp.int8_matmul(*qcp.int8_quantize(x), *w)
+    assert rc == 0 and torch.equal(y[:, :90], want) and (y[:, 90:] == 7).all()
+
+
+@GPU
 def test_linear_gradients_match_differences(gpu):
     """On rows whose largest value is 127 and whose values are integers the payload is the
     matrix itself, so the layer is the plain linear map, and differences of a whole step equal
@@ -716,6 +748,24 @@ def test_c_entry_of_the_product_refuses(lib):
         assert mul(**bad) == EALIGN, bad
 
 
+def test_c_entry_for_few_rows_refuses(lib):
+    fit = lib.qcp_int8_linear_rows_fit
+    assert fit(1, 14336, 4096) == fit(1, 28672, 8192) == fit(8, 4096, 4096) == fit(8, 1000, 6144) == fit(1, 1, 49152) == 1
+    assert fit(8, 14336, 4096) == fit(4, 14336, 4096) == 0                  # as quick in two launches
+    assert fit(9, 64, 64) == fit(8, 1000, 6145) == fit(1, 1, 49153) == fit(0, 4, 4) == fit(4, 0, 4) == fit(4, 4, 0) == fit(1, 4, 1 << 40) == 0
+
+    def call(x=A, xt=2, M=4, K=256, ldx=256, w=A + S, s=A + 2 * S, N=64, y=A + 3 * S, ldy=64):
+        return lib.int8_linear_rows(x, xt, M, K, ldx, w, s, N, y, ldy, None)
+    assert call(M=0) == OK and call(N=0, ldy=0) == OK
+    for bad in (dict(M=-1), dict(N=-1), dict(K=-1), dict(xt=3), dict(xt=0), dict(ldx=255), dict(ldy=63), dict(x=0), dict(w=0), dict(s=0),
+                dict(y=0), dict(y=A), dict(y=A + S), dict(y=A + 2 * S), dict(K=130945, ldx=130945), dict(N=1 << 30, ldy=1 << 30)):
+        assert call(**bad) == EINVAL, bad
+    for bad in (dict(M=9), dict(K=0, ldx=0), dict(K=50000, ldx=50000), dict(M=8, N=14336, ldy=14336, K=4096, ldx=4096)):
+        assert call(**bad) == EUNSUP, bad
+    for bad in (dict(x=A + 1), dict(y=A + 3 * S + 1), dict(w=A + S + 8), dict(s=A + 2 * S + 4)):
+        assert call(**bad) == EALIGN, bad
+
+
 def test_rows_below_the_bound_have_no_slices(lib):
     """The binding asks for scratch memory only above this length."""
     from quantized_collective_payloads_amd.int8 import _UNSLICED
@@ -801,6 +851,7 @@ def layer_on_cpu(monkeypatch):
     monkeypatch.setattr(int8, "_same_gpu", lambda index, *ts: None)
     monkeypatch.setattr(int8, "_quantized", lambda index, x: x.new_empty(x.shape[0] * (R.padded(x.shape[1]) + 4), dtype=torch.uint8))
     monkeypatch.setattr(int8, "_multiply", lambda index, a, sa, b, sb, M, N, K, c: c.zero_())
+    monkeypatch.setattr(int8, "_frozen_product", lambda index, x, codes, scales: x.new_zeros((x.shape[0], codes.shape[0])))
     monkeypatch.setattr(int8, "_mixed", lambda index, a, codes, scales, M, N, K, transpose, c: c.zero_())
 
 
