@@ -108,9 +108,12 @@ __device__ __forceinline__ void store_fragment(const f32x16_t &v, void *c, int64
 // 64 lanes x 16 bytes from rsrc[voff + soff] to LDS at `lds` + 16 * lane.  The
 // caller waits for it with wait_and_meet; no vector register is written.  The
 // instruction takes the LDS address from m0, which is an operand here, so that the
-// compiler knows what it holds; s_nop is the wait state between the two.
+// compiler knows what it holds.  The compiler does not count wait states into an asm
+// statement: the s_nop holds the five that a scalar register needs between a vector
+// instruction that writes it (v_readlane, which restores a spilled one) and a memory
+// instruction that reads it, and the one that m0 needs.
 __device__ __forceinline__ void copy_to_lds(uint32_t lds, uint32_t voff, i32x4_t rsrc, uint32_t soff) {
-    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                  :
                  : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane((int)soff)),
                    "{m0}"(__builtin_amdgcn_readfirstlane((int)lds))
@@ -137,7 +140,7 @@ __device__ __forceinline__ i32x4_t buffer_of(const void *p, uint64_t bytes) {
 
 // as copy_to_lds, 4 bytes a lane
 __device__ __forceinline__ void copy4_to_lds(uint32_t lds, uint32_t voff, i32x4_t rsrc) {
-    asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+    asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, 0 offen lds"
                  :
                  : "v"(voff), "s"(rsrc), "{m0}"(__builtin_amdgcn_readfirstlane((int)lds))
                  : "memory");
