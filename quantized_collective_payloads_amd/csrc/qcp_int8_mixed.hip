@@ -293,29 +293,37 @@ __global__ __launch_bounds__(G::threads * G::TEAMS, 2) void k_int8_mixed(
 }
 
 // ---------------------------------------------------------------------------
-// 256 x 256 of C per work-group, operands copied to LDS as they lie in memory.
+// 256 x 256 or 128 x 128 of C per work-group, operands copied to LDS as they lie in memory.
 // ---------------------------------------------------------------------------
-// For an a whose rows are aligned to 16 bytes.  Eight waves hold 256 x 32 each, so that a
-// column of the payload is decoded once in a work-group; a's fragments are read by all of
-// them.  A stage is 64 of k: 32 KB of a, 16 KB of codes and 64 scales, in one of three
-// slots, so that copies have two stages to arrive.  LDS gives 8 k of a column to a lane:
-// ds_read_b64_tr_b8 turns 8 rows x 16 bytes for 16 lanes, _tr_b16 4 rows x 16 values of a
-// transposed a.  A register holds the scales of two steps of 16, each row of 16 lanes its own
-// 16, and the products with them take one lane's for all (row_newbcast).
+// For an a whose rows are aligned to 16 bytes.  Eight waves hold 256 x 32 each (four 128 x 32), so
+// that a column of the payload is decoded once in a work-group; a's fragments are read by all of
+// them.  A stage is 64 of k: 32 KB of a, 16 KB of codes and 64 scales, in one of three slots.
+// LDS gives 8 k of a column to a lane: ds_read_b64_tr_b8 turns 8 rows x 16 bytes for 16 lanes,
+// _tr_b16 4 rows x 16 values of a transposed a.  A register holds the scales of two steps of 16,
+// each row of 16 lanes its own 16, and the products with them take one lane's for all
+// (row_newbcast).
 //
 // A step is 8 products; between them, in the order written, the fragment just used is read
-// for the next step, and that step's codes are read and decoded.  In a stage's last step,
-// whose fragments were read before, the barrier says that the slot of the stage before is
-// free, and the copies of the stage three on go there.
+// for the next step, and that step's codes are read and decoded.  Before a stage's last step,
+// whose fragments were read by then, the waves meet: the next stage has arrived, and the one
+// before this was multiplied by all, so the copies of the stage after the next go into its slot.
+// (Another stage ahead, into the slot just read, the waves had to wait for those reads as well:
+// 1% slower.)
+//
+// Bound: the power that the matrix cores draw on normal values: 8192 x 8192, K = 4096 takes 460 us
+// (1.2 PFLOP/s, the clock at 1.8 GHz) and on zeros 320 (1.7 PFLOP/s, 2.4 GHz); in cycles the cores are
+// busy 63% of the time, LDS 35%.  4096 x 4096, K = 4096 119 us; 14336 x 4096, K = 2048 to fp32 245;
+// 2048 x 2048, K = 2048 in tiles of 128 26.
 //
 // Pieces of 16 bytes lie in LDS in an order that spreads what a read touches in a cycle over all
 // banks: of a row by row, piece ^ (row / 2 % 8); of a transposed, piece ^ 4 (row % 4); of the
-// payload, piece ^ 2 (row % 8).  What is read past the end of a buffer counts for nothing: results
-// past the end are not stored, and in the last stage of a K that is no multiple of 64 the values
-// of a and the scales past the end are made zeros in LDS.
+// payload, piece ^ 2 (row % 8), or where its rows are 128 bytes 2 (row / 2 % 4).  What is read past
+// the end of a buffer counts for nothing: results past the end are not stored, and in the last stage
+// of a K that is no multiple of 64 the values of a and the scales past the end are made zeros in LDS.
 namespace direct {
 
 constexpr int kStage = 64, kSlots = 3;
+constexpr uint32_t kAhead = 2;                               // stages copied before the first is multiplied
 constexpr int kCopies = 7;                                   // of a wave and stage
 constexpr int64_t kMaxLd = (int64_t)1 << 22;                 // 256 rows of a are within 32 bits
 
@@ -345,6 +353,13 @@ template <int J>
 __device__ __forceinline__ float of_lane(float v) {
     return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x150 + J, 0xf, 0xf, true));
 }
+// until at most N of this wave's copies and stores are in flight, reads of LDS not counted; then
+// with the other waves
+template <int N>
+__device__ __forceinline__ void wait_copies_and_meet() {
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
 template <class G, int AT, bool TRANS, int CT, bool SLICED>
 __global__ __launch_bounds__(G::threads, 2) void k_int8_mixed_direct(
     const uint16_t *__restrict__ a, int64_t lda, const uint8_t *__restrict__ codes, const float *__restrict__ scales,
@@ -509,7 +524,7 @@ __global__ __launch_bounds__(G::threads, 2) void k_int8_mixed_direct(
         static_for<4>([&](auto J) __attribute__((always_inline)) { decode(J, zero{}, fb); });
     };
     auto copy_first = [&]() __attribute__((always_inline)) {
-        for (uint32_t s = 0; s < min(stages, (uint32_t)kSlots); s++) {
+        for (uint32_t s = 0; s < min(stages, kAhead); s++) {
             static_for<kCopies>(copy);
             copied();
         }
@@ -523,7 +538,7 @@ __global__ __launch_bounds__(G::threads, 2) void k_int8_mixed_direct(
     set_tile(tile);
     copy_first();
     wait_and_meet<0>();
-    int behind = 0;                                          // stages whose copies are older than the last tile's stores
+    bool behind = false;                                     // the second stage's copies are older than the last tile's stores
     for (;;) {
 #pragma unroll
         for (int i = 0; i < FM; i++) acc[i] = f32x16_t{};
@@ -532,13 +547,13 @@ __global__ __launch_bounds__(G::threads, 2) void k_int8_mixed_direct(
             if (stages == 1 && tail < kStage) clear(base, tail);
             begin();
             uint32_t s = 0;
-            for (; s + kSlots < stages; s++)
+            for (; s + kAhead < stages; s++)
                 stage(yes{}, no{}, [&](uint32_t) __attribute__((always_inline)) {
-                    if (behind > 0) {
-                        behind--;
-                        wait_and_meet<kCopies + stores>();
+                    if (behind) {
+                        behind = false;
+                        wait_copies_and_meet<stores>();
                     } else {
-                        wait_and_meet<kCopies>();
+                        wait_copies_and_meet<0>();
                     }
                 });
             for (; s + 1 < stages; s++)
@@ -565,13 +580,9 @@ __global__ __launch_bounds__(G::threads, 2) void k_int8_mixed_direct(
             store_fragment<CT>(acc[i], to, ldc, m_done + 32 * i, n_done, (int)half, M, N, whole);
         });
         if (!more) break;
-        if (whole && stages >= kSlots) {
-            wait_and_meet<(2 * kCopies + stores < 63 ? 2 * kCopies + stores : 63)>();
-            behind = 2;
-        } else {
-            wait_and_meet<0>();
-            behind = 0;
-        }
+        behind = whole && stages >= kAhead;
+        if (behind) wait_and_meet<kCopies + stores>();
+        else wait_and_meet<0>();
     }
 }
 
