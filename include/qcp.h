@@ -380,10 +380,11 @@ int qcp_int8_linear_rows_fit(int64_t M, int64_t N, int64_t K);
  *   codes, scales   the payload of X, K rows of N codes; N <= 2^24
  *   c          M x N of type ct, which is QCP_F32 or at (else QCP_EUNSUPPORTED), rows
  *              ldc apart; K = 0 gives zeros
- *   work       null, or scratch memory on the device of at least qcp_int8_mixed_work(M, N,
- *              K) bytes, 16-byte aligned: slices of a long K side by side, added up in a
- *              fixed order in a second launch.  The order of the sums, and with it their
- *              last bits, differs from the product without.
+ *   work       null, or scratch memory on the device of at least qcp_int8_mixed_work(...)
+ *              bytes, 16-byte aligned: for slices of a long K side by side, added up in a
+ *              fixed order in a second launch, and for a copy of a large a whose rows are
+ *              not aligned to 16 bytes (at most 256 MB).  The order of the sums, and with
+ *              it their last bits, differs from the product without.
  * dx = dy W: a = dy, the payload of W [out, in].  dW = dy^T x: a = dy with transpose, the
  * payload of x [tokens, in], which is all that a layer keeps of its input.
  */
@@ -391,9 +392,10 @@ int int8_matmul_mixed(const void *a, int at, int64_t lda, int32_t transpose, con
                       const float *scales, int64_t M, int64_t N, int64_t K, void *c, int ct, int64_t ldc,
                       void *work, int64_t work_bytes, void *stream);
 
-/* Bytes of scratch memory for int8_matmul_mixed; -1 for a negative or too large size.
- * Host only. */
-int64_t qcp_int8_mixed_work(int64_t M, int64_t N, int64_t K);
+/* Bytes of scratch memory for int8_matmul_mixed; `aligned` is 1 for an a that is 16-byte
+ * aligned with lda a multiple of 8 and at most 2^22, else 0.  -1 for a negative or too
+ * large size.  Host only. */
+int64_t qcp_int8_mixed_work(int64_t M, int64_t N, int64_t K, int32_t transpose, int32_t aligned);
 
 /* Payload bytes of n codes at `bits` bits with one fp32 scale per G elements:
  * ceil(n*bits/8) + 4*ceil(n/G); -1 for invalid arguments.  Host only. */

@@ -108,9 +108,10 @@ def library():
         lib.qcp_mxfp4_padded.restype = i64
         lib.qcp_mxfp4_matmul_work.argtypes = [i64, i64, i64]
         lib.qcp_mxfp4_matmul_work.restype = i64
-        for name in ("qcp_int8_matmul_work", "qcp_int8_mixed_work"):
-            getattr(lib, name).argtypes = [i64, i64, i64]
-            getattr(lib, name).restype = i64
+        lib.qcp_int8_matmul_work.argtypes = [i64, i64, i64]
+        lib.qcp_int8_matmul_work.restype = i64
+        lib.qcp_int8_mixed_work.argtypes = [i64, i64, i64, i32, i32]
+        lib.qcp_int8_mixed_work.restype = i64
         lib.qcp_strerror.argtypes = [ci]
         lib.qcp_strerror.restype = ctypes.c_char_p
         lib.qcp_version.argtypes = []

@@ -305,12 +305,13 @@ __global__ __launch_bounds__(G::threads * G::TEAMS, 2) void k_int8_mixed(
 // each row of 16 lanes its own 16, and the products with them take one lane's for all
 // (row_newbcast).
 //
-// A step is 8 products; between them, in the order written, the fragment just used is read
-// for the next step, and that step's codes are read and decoded.  Before a stage's last step,
-// whose fragments were read by then, the waves meet: the next stage has arrived, and the one
-// before this was multiplied by all, so the copies of the stage after the next go into its slot.
-// (Another stage ahead, into the slot just read, the waves had to wait for those reads as well:
-// 1% slower.)
+// A step is 8 products (4 in tiles of 128); between them, in the order written, the fragment just
+// used is read for the next step, and that step's codes are read and decoded.  Before a stage's
+// last step, whose fragments were read by then, the waves meet: the next stage has arrived, and the
+// one before this was multiplied by all, so the copies of the stage after the next go into its slot.
+// In tiles of 128, whose stages are half as long, copies go a stage further ahead, into the slot
+// just read, and the waves wait for those reads as well (1024 x 4096, K = 4096 46 us and 52; in
+// tiles of 256 that is 1% the slower).
 //
 // Bound: the power that the matrix cores draw on normal values: 8192 x 8192, K = 4096 takes 460 us
 // (1.2 PFLOP/s, the clock at 1.8 GHz) and on zeros 320 (1.7 PFLOP/s, 2.4 GHz); in cycles the cores are
@@ -325,13 +326,13 @@ __global__ __launch_bounds__(G::threads * G::TEAMS, 2) void k_int8_mixed(
 namespace direct {
 
 constexpr int kStage = 64, kSlots = 3;
-constexpr uint32_t kAhead = 2;                               // stages copied before the first is multiplied
 constexpr int kCopies = 7;                                   // of a wave and stage
 constexpr int64_t kMaxLd = (int64_t)1 << 22;                 // 256 rows of a are within 32 bits
 
 // 32*FM x 32*NW of C per work-group of NW waves
 template <int FM_, int NW_> struct Tile {
     static constexpr int FM = FM_, NW = NW_, TM = 32 * FM, TN = 32 * NW, threads = 64 * NW;
+    static constexpr uint32_t ahead = NW == 8 ? 2 : 3;           // stages copied before the first is multiplied
     static constexpr uint32_t codes_at = TM * kStage * 2, scales_at = codes_at + TN * kStage, slot = scales_at + 256;
     static constexpr uint32_t t_row = 2 * TM, t_pieces = TM / 8; // of a row of a transposed a, in LDS
     static constexpr uint32_t b_row = TN, b_pieces = TN / 16;    // of a row of codes
@@ -362,11 +363,12 @@ __device__ __forceinline__ void wait_copies_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// width: elements of a row of a as it is given, a multiple of 8
 template <class G, int AT, bool TRANS, int CT, bool SLICED>
 __global__ __launch_bounds__(G::threads, 2) void k_int8_mixed_direct(
     const uint16_t *__restrict__ a, int64_t lda, const uint8_t *__restrict__ codes, const float *__restrict__ scales,
-    int64_t M, int64_t N, int64_t K, uint32_t pad, uint32_t slices, uint32_t m_tiles, uint32_t n_tiles, uint32_t groups,
-    void *__restrict__ c, int64_t ldc) {
+    int64_t M, int64_t N, int64_t K, int64_t width, uint32_t pad, uint32_t slices, uint32_t m_tiles, uint32_t n_tiles,
+    uint32_t groups, void *__restrict__ c, int64_t ldc) {
     constexpr int FM = G::FM;
     constexpr uint32_t kSlot = G::slot, kCodesAt = G::codes_at, kScalesAt = G::scales_at;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * kSlot];
@@ -418,13 +420,13 @@ __global__ __launch_bounds__(G::threads, 2) void k_int8_mixed_direct(
             const uint32_t row = kStage / G::NW * wave + (kStage / G::NW / 4) * i + lane / G::t_pieces;
             const uint32_t piece = lane % G::t_pieces ^ (4 * (row & 3));
             copy_to_lds(to + wave * 4096 + i * 1024, row * (uint32_t)lda * 2 + piece * 16,
-                        buffer_of(a + k_next * lda + m0, (uint64_t)((K - 1 - k_next) * lda + (M - m0)) * 2), 0);
+                        buffer_of(a + k_next * lda + m0, (uint64_t)((K - 1 - k_next) * lda + (width - m0)) * 2), 0);
         } else {
             constexpr int i = n - 3;
             const uint32_t row = min(32 * wave + 8 * i + (lane >> 3), m_rows - 1);
             const uint32_t piece = (lane & 7) ^ (lane >> 4) ^ (4 * (i & 1));
             copy_to_lds(to + wave * 4096 + i * 1024, row * (uint32_t)lda * 2 + piece * 16,
-                        buffer_of(a + m0 * lda, (uint64_t)((m_rows - 1) * lda + K) * 2), (uint32_t)k_next * 2);
+                        buffer_of(a + m0 * lda, (uint64_t)((m_rows - 1) * lda + width) * 2), (uint32_t)k_next * 2);
         }
     };
     auto copied = [&]() __attribute__((always_inline)) {
@@ -526,7 +528,7 @@ __global__ __launch_bounds__(G::threads, 2) void k_int8_mixed_direct(
         static_for<4>([&](auto J) __attribute__((always_inline)) { decode(J, zero{}, fb); });
     };
     auto copy_first = [&]() __attribute__((always_inline)) {
-        for (uint32_t s = 0; s < min(stages, kAhead); s++) {
+        for (uint32_t s = 0; s < min(stages, G::ahead); s++) {
             static_for<kCopies>(copy);
             copied();
         }
@@ -540,7 +542,12 @@ __global__ __launch_bounds__(G::threads, 2) void k_int8_mixed_direct(
     set_tile(tile);
     copy_first();
     wait_and_meet<0>();
-    bool behind = false;                                     // the second stage's copies are older than the last tile's stores
+    int behind = 0;                                          // stages whose copies are older than the last tile's stores
+    constexpr int later = (G::ahead - 2) * kCopies;          // copies of stages beyond the next, in flight where the waves meet
+    auto arrive = [&](auto N) __attribute__((always_inline)) {
+        if constexpr (G::ahead == kSlots) wait_and_meet<N>();
+        else wait_copies_and_meet<N>();
+    };
     for (;;) {
 #pragma unroll
         for (int i = 0; i < FM; i++) acc[i] = f32x16_t{};
@@ -549,13 +556,13 @@ __global__ __launch_bounds__(G::threads, 2) void k_int8_mixed_direct(
             if (stages == 1 && tail < kStage) clear(base, tail);
             begin();
             uint32_t s = 0;
-            for (; s + kAhead < stages; s++)
+            for (; s + G::ahead < stages; s++)
                 stage(yes{}, no{}, [&](uint32_t) __attribute__((always_inline)) {
-                    if (behind) {
-                        behind = false;
-                        wait_copies_and_meet<stores>();
+                    if (behind > 0) {
+                        behind--;
+                        arrive(integral_constant<int, later + stores>{});
                     } else {
-                        wait_copies_and_meet<0>();
+                        arrive(integral_constant<int, later>{});
                     }
                 });
             for (; s + 1 < stages; s++)
@@ -582,8 +589,8 @@ __global__ __launch_bounds__(G::threads, 2) void k_int8_mixed_direct(
             store_fragment<CT>(acc[i], to, ldc, m_done + 32 * i, n_done, (int)half, M, N, whole);
         });
         if (!more) break;
-        behind = whole && stages >= kAhead;
-        if (behind) wait_and_meet<kCopies + stores>();
+        behind = whole && stages >= G::ahead ? (int)G::ahead - 1 : 0;
+        if (behind) wait_and_meet<later + kCopies + stores>();
         else wait_and_meet<0>();
     }
 }
@@ -604,9 +611,16 @@ __global__ __launch_bounds__(kThreads) void k_int8_mixed_join(const float *__res
         const float *p = parts + m * N + n;
         float v[4] = {};
         if (count == 4) {
-            for (int s = 0; s < slices; s++, p += part) {
-                const f32x4_any x = *(const f32x4_any *)p;
-                v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+            // 2, 4, 8 or 16 slices: several loads in flight
+#pragma unroll 4
+            for (int s = 0; s < slices; s += 2) {
+                f32x4_any x[2];
+#pragma unroll
+                for (int k = 0; k < 2; k++, p += part) x[k] = *(const f32x4_any *)p;
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    v[0] += x[k].x; v[1] += x[k].y; v[2] += x[k].z; v[3] += x[k].w;
+                }
             }
         } else {
             for (int s = 0; s < slices; s++, p += part)
@@ -618,6 +632,27 @@ __global__ __launch_bounds__(kThreads) void k_int8_mixed_join(const float *__res
     }
 }
 
+// a with rows of whole 16 bytes, the rest of a row's last 16 zeros: what the kernel above can copy.
+// A row of work-groups for each row.
+__global__ __launch_bounds__(kThreads) void k_int8_mixed_align(const uint16_t *__restrict__ a, int64_t lda, int64_t rows,
+                                                               int64_t width, uint16_t *__restrict__ to) {
+    const int64_t at = ((int64_t)__builtin_amdgcn_workgroup_id_x() * kThreads + __builtin_amdgcn_workitem_id_x()) * 8;
+    const int64_t whole = (width + 7) / 8 * 8, left = width - at;
+    if (left <= 0) return;
+    for (int64_t r = group_y(); r < rows; r += kJoinRows) {
+        const uint16_t *const p = a + r * lda + at;
+        u32x4_t w = {0, 0, 0, 0};
+        if (left >= 8) {
+            w = __builtin_nontemporal_load((const u32x4_any *)p);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 7; e++)
+                if (e < left) w[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+        }
+        *(u32x4_t *)(to + r * whole + at) = w;
+    }
+}
+
 using Tile256 = MixedTile<256, 256, 64, 2, 4, 1, 1>;
 using Tile128 = MixedTile<128, 128, 64, 2, 2, 2, 1>;
 using Tile64 = MixedTile<64, 64, 128, 2, 2, 1, 1>;
@@ -625,7 +660,7 @@ using Tile64x2 = MixedTile<64, 64, 128, 2, 2, 1, 2>;
 
 struct MixedArgs {
     const uint16_t *a;
-    int64_t lda;
+    int64_t lda, width;          // elements between its rows, and of a row
     const uint8_t *codes;
     const float *scales;
     int64_t M, N, K;
@@ -650,8 +685,8 @@ hipError_t run_direct(const MixedArgs &p, int slices, int resident) {
     const uint32_t pad = (uint32_t)((p.N + 127) / 128 * 128);
     const unsigned groups = (unsigned)std::min<int64_t>(mt * nt * slices, resident);
     hipLaunchKernelGGL((direct::k_int8_mixed_direct<G, AT, TRANS, CT, SLICED>), dim3(groups), dim3(G::threads), 0, p.st,
-                       p.a, p.lda, p.codes, p.scales, p.M, p.N, p.K, pad, (uint32_t)slices, (uint32_t)mt, (uint32_t)nt,
-                       groups, p.c, p.ldc);
+                       p.a, p.lda, p.codes, p.scales, p.M, p.N, p.K, p.width, pad, (uint32_t)slices, (uint32_t)mt,
+                       (uint32_t)nt, groups, p.c, p.ldc);
     return hipGetLastError();
 }
 
@@ -668,25 +703,36 @@ constexpr int kPlain256 = 3, kDirect128 = 4, kDirect256 = 5;
 
 struct Choice {
     int form, slices;
+    bool copy;                   // of a, to aligned rows
+    int64_t copy_bytes, work;    // of that copy, and all scratch memory
 };
+constexpr int64_t kMostCopied = (int64_t)256 << 20;
 // Slices of K (up to 16, each of at least 256) fill the GPU where there are few tiles: 512 x
-// 4096, K = 14336 96 us with 4, 275 without; 2048 x 4096, K = 14336 239 with 2, 283 without.
-// They cost a second launch, and the sums a trip to memory and back.
-Choice choose(int64_t M, int64_t N, int64_t K, bool aligned, bool slicing) {
-    Choice best = {0, 1};
+// 4096, K = 14336 80 us with 4 (tiles of 128), 140 without; 2048 x 4096, K = 14336 222 with 2, 283
+// without.  They cost a second launch, and the sums a trip to memory and back.  A copy of an a
+// that is not aligned costs the same: 14335 x 4095, K = 2047 272 us with it and 328 without;
+// scratch: scratch memory may be used.
+Choice choose(int64_t M, int64_t N, int64_t K, bool transpose, bool aligned, bool scratch) {
+    Choice best = {0, 1, false, 0, 0};
     int64_t least = INT64_MAX;
+    const int64_t width = (transpose ? M : K), wide = (width + 7) / 8 * 8, copied = 2 * wide * (transpose ? K : M);
+    aligned = aligned && width % 8 == 0 && wide <= direct::kMaxLd;
+    const bool copy = !aligned && scratch && K > 0 && wide <= direct::kMaxLd && copied <= kMostCopied;
     for (int f = 0; f <= kDirect256; f++) {
-        if (aligned ? f == kPlain256 : f >= kDirect128) continue;
+        if (f >= kDirect128 ? !aligned && !copy : aligned && f == kPlain256) continue;
         const Form &m = kForms[f];
         const int64_t tiles = m.tiles(M, N), stages = (K + m.stage - 1) / m.stage;
         if (tiles > kMaxGroups / 2) continue;
-        for (int s = 1; s <= (slicing ? 16 : 1); s *= 2) {
+        const bool with = f >= kDirect128 && copy;
+        for (int s = 1; s <= (scratch ? 16 : 1); s *= 2) {
             if (s > 1 && (K / s < 256 || tiles * s > m.resident + m.resident / 4)) break;
             int64_t price = m.price(tiles * s, (stages + s - 1) / s);
-            if (s > 1) price += 550 + (2 * s + 1) * M * N / 12000;             // 4.8 TB/s
+            if (s > 1) price += 550 + (8 * s - 1) * M * N / 50000;   // fp32 sums out at 4 TB/s, in at 6.2
+            if (with) price += 700 + copied / 22500;                 // out and in at 4.5 TB/s
             if (price < least) {
                 least = price;
-                best = {f, s};
+                const int64_t bytes = with ? (copied + 255) / 256 * 256 : 0;
+                best = {f, s, with, bytes, bytes + (s > 1 ? 4 * s * M * N : 0)};
             }
         }
     }
@@ -705,13 +751,25 @@ hipError_t run_form(const MixedArgs &p, Choice which) {
     }
 }
 
+// is a, with rows lda apart, as the copies to LDS need it (where their width is, too)
+bool is_aligned(const void *a, int64_t lda) { return (uintptr_t)a % 16 == 0 && lda % 8 == 0 && lda <= direct::kMaxLd; }
+
 template <int AT, bool TRANS, int CT>
-hipError_t run_mixed(const MixedArgs &p, float *work) {
-    const bool aligned = (uintptr_t)p.a % 16 == 0 && p.lda % 8 == 0 && (TRANS ? p.M : p.K) % 8 == 0 && p.lda <= direct::kMaxLd;
-    const Choice which = choose(p.M, p.N, p.K, aligned, work != nullptr);
+hipError_t run_mixed(MixedArgs p, uint8_t *work) {
+    const Choice which = choose(p.M, p.N, p.K, TRANS, is_aligned(p.a, p.lda), work != nullptr);
+    if (which.copy) {
+        const int64_t rows = TRANS ? p.K : p.M;
+        const dim3 grid((unsigned)((p.width + 8 * kThreads - 1) / (8 * kThreads)), (unsigned)std::min<int64_t>(rows, kJoinRows));
+        hipLaunchKernelGGL(k_int8_mixed_align, grid, dim3(kThreads), 0, p.st, p.a, p.lda, rows, p.width, (uint16_t *)work);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        p.a = (const uint16_t *)work;
+        p.lda = p.width = (p.width + 7) / 8 * 8;
+    }
     if (which.slices == 1) return run_form<AT, TRANS, CT, false>(p, which);
+    float *const sums = (float *)(work + which.copy_bytes);
     MixedArgs q = p;
-    q.c = work;
+    q.c = sums;
     q.ldc = p.N;
     const hipError_t e = run_form<AT, TRANS, F32, true>(q, which);
     if (e != hipSuccess) return e;
@@ -719,30 +777,31 @@ hipError_t run_mixed(const MixedArgs &p, float *work) {
     const bool flat = p.ldc == p.N && p.N % 4 == 0;
     const int64_t rows = flat ? 1 : p.M, cols = flat ? p.M * p.N : p.N;
     const dim3 grid((unsigned)((cols + 4 * kThreads - 1) / (4 * kThreads)), (unsigned)std::min<int64_t>(rows, kJoinRows));
-    hipLaunchKernelGGL((k_int8_mixed_join<CT>), grid, dim3(kThreads), 0, p.st, work, which.slices, p.M * p.N, rows, cols,
+    hipLaunchKernelGGL((k_int8_mixed_join<CT>), grid, dim3(kThreads), 0, p.st, sums, which.slices, p.M * p.N, rows, cols,
                        p.c, p.ldc);
     return hipGetLastError();
 }
 
 template <int AT, bool TRANS>
-hipError_t by_result(const MixedArgs &p, int ct, float *work) {
+hipError_t by_result(const MixedArgs &p, int ct, uint8_t *work) {
     return ct == F32 ? run_mixed<AT, TRANS, F32>(p, work) : run_mixed<AT, TRANS, AT>(p, work);
 }
 
 }  // namespace
 
-// the more of an aligned and of another a
-int int8_mixed_slices(int64_t M, int64_t N, int64_t K) {
-    if (M < 1 || N < 1 || K < 1) return 1;
-    return std::max(choose(M, N, K, false, true).slices, choose(M, N, K, true, true).slices);
+int64_t int8_mixed_work(int64_t M, int64_t N, int64_t K, int transpose, bool aligned) {
+    if (M < 1 || N < 1 || K < 1) return 0;
+    return choose(M, N, K, transpose, aligned, true).work;
 }
+bool int8_mixed_aligned(const void *a, int64_t lda) { return is_aligned(a, lda); }
 
 hipError_t launch_int8_mixed(const void *a, int at, int64_t lda, int transpose, const uint8_t *codes,
                              const float *scales, int64_t M, int64_t N, int64_t K, void *c, int ct, int64_t ldc,
-                             float *work, hipStream_t st) {
-    const MixedArgs p = {(const uint16_t *)a, lda, codes, scales, M, N, K, c, ldc, st};
-    if (at == BF16) return transpose ? by_result<BF16, true>(p, ct, work) : by_result<BF16, false>(p, ct, work);
-    if (at == F16) return transpose ? by_result<F16, true>(p, ct, work) : by_result<F16, false>(p, ct, work);
+                             void *work, hipStream_t st) {
+    const MixedArgs p = {(const uint16_t *)a, lda, transpose ? M : K, codes, scales, M, N, K, c, ldc, st};
+    uint8_t *const w = (uint8_t *)work;
+    if (at == BF16) return transpose ? by_result<BF16, true>(p, ct, w) : by_result<BF16, false>(p, ct, w);
+    if (at == F16) return transpose ? by_result<F16, true>(p, ct, w) : by_result<F16, false>(p, ct, w);
     return hipErrorInvalidValue;
 }
 

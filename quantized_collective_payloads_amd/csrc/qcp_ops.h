@@ -63,11 +63,13 @@ hipError_t launch_int8_linear_rows(const void *x, int xt, int64_t ldx, int64_t M
                                    const float *bs, int64_t N, int64_t stages, void *y, int64_t ldy, hipStream_t st);
 
 // C[M, N] = A X for a 16-bit A (transpose: given as [K, M]) and the payload of X [K, N];
-// see qcp_int8_mixed.hip.  work: null, or room for slices * M * N floats
-int int8_mixed_slices(int64_t M, int64_t N, int64_t K);
+// see qcp_int8_mixed.hip.  work: null, or as many bytes as said here; aligned: what the other
+// function says of a
+int64_t int8_mixed_work(int64_t M, int64_t N, int64_t K, int transpose, bool aligned);
+bool int8_mixed_aligned(const void *a, int64_t lda);
 hipError_t launch_int8_mixed(const void *a, int at, int64_t lda, int transpose, const uint8_t *codes,
                              const float *scales, int64_t M, int64_t N, int64_t K, void *c, int ct, int64_t ldc,
-                             float *work, hipStream_t st);
+                             void *work, hipStream_t st);
 
 // the counter hash of the stochastic rounding: an invertible scramble of 32 bits
 // (two rounds of xor-shift and an odd multiplier, the fractions of sqrt 2 and sqrt 3)

@@ -415,7 +415,7 @@ int int8_matmul_mixed(const void *a, int at, int64_t lda, int32_t transpose, con
     if (N > kMixedMaxN || lda > kMixedMaxLd || !int8_payload(K, N, &pad)) return QCP_EINVAL;
     if ((M + 255) / 256 > qcp::kMaxGroups / 2 / ((N + 255) / 256)) return QCP_EINVAL;   // tiles of C
     if (!c || (K > 0 && (!a || !codes || !scales))) return QCP_EINVAL;
-    const int64_t need = work ? qcp_int8_mixed_work(M, N, K) : 0;
+    const int64_t need = work ? qcp_int8_mixed_work(M, N, K, transpose, qcp::int8_mixed_aligned(a, lda) ? 1 : 0) : 0;
     if (work_bytes < need) return QCP_EINVAL;
     if (!aligned16(codes) || !aligned16(scales) || !aligned16(work) || (uintptr_t)a % 2 ||
         (uintptr_t)c % dtype_bytes(ct))
@@ -426,13 +426,14 @@ int int8_matmul_mixed(const void *a, int at, int64_t lda, int32_t transpose, con
     for (int i = 0; i < 3; i++)
         if (overlap(c, cb, in[i], bytes[i]) || overlap(work, need, in[i], bytes[i])) return QCP_EINVAL;
     return status_of(qcp::launch_int8_mixed(a, at, lda, transpose, codes, scales, M, N, K, c, ct, ldc,
-                                            need ? (float *)work : nullptr, (hipStream_t)stream));
+                                            need ? work : nullptr, (hipStream_t)stream));
 }
 
-int64_t qcp_int8_mixed_work(int64_t M, int64_t N, int64_t K) {
-    if (M < 0 || N < 0 || K < 0 || M > kMaxElems || N > kMaxElems || K > kMaxElems) return -1;
-    const int slices = qcp::int8_mixed_slices(M, N, K);
-    return slices > 1 ? 4 * slices * M * N : 0;
+int64_t qcp_int8_mixed_work(int64_t M, int64_t N, int64_t K, int32_t transpose, int32_t aligned) {
+    if (M < 0 || N < 0 || K < 0 || M > kMaxElems || N > kMixedMaxN || K > kMaxElems) return -1;
+    if ((transpose != 0 && transpose != 1) || (aligned != 0 && aligned != 1)) return -1;
+    if ((M + 255) / 256 > qcp::kMaxGroups / 2 / ((N + 256) / 256)) return -1;
+    return qcp::int8_mixed_work(M, N, K, transpose, aligned != 0);
 }
 
 }  // extern "C"

@@ -159,9 +159,11 @@ def _mixed(index, a, codes, scales, M, N, K, transpose, c):
     if not a.is_contiguous() and a.stride(0) == 1 and a.stride(1) >= a.shape[0]:
         a, transpose = a.t(), not transpose
     a, lda = _rows_of(a)
-    t, at, size = _scratch("qcp_int8_mixed_work", c, M, N, K)
-    _enqueue("int8_matmul_mixed", index, a.data_ptr(), DTYPES[a.dtype], lda, 1 if transpose else 0, codes, scales,
-             M, N, K, c.data_ptr(), DTYPES[c.dtype], N, at, size)
+    first, transpose = a.data_ptr(), 1 if transpose else 0
+    t, at, size = _scratch("qcp_int8_mixed_work", c, M, N, K, transpose,
+                           1 if first % 16 == 0 and lda % 8 == 0 and lda <= 1 << 22 else 0)
+    _enqueue("int8_matmul_mixed", index, first, DTYPES[a.dtype], lda, transpose, codes, scales, M, N, K, c.data_ptr(),
+             DTYPES[c.dtype], N, at, size)
 
 
 def _quantized(index, x):

@@ -272,6 +272,12 @@ MIXED = [(1, 1, 1), (1, 130, 9), (5, 64, 128), (64, 64, 64), (65, 129, 63), (77,
          (300, 1000, 100), (1500, 2100, 65), (1100, 3100, 200), (3000, 4000, 70), (4097, 3590, 130), (16, 4100, 2000)]
 
 
+# copied to LDS as they lie, in tiles of 128 and 256, over one round and several, with K of whole stages
+# and not, in slices and not, with rows that are first copied to aligned ones
+LARGER = [(260, 4000, 3000), (2050, 2060, 1000), (1024, 1500, 8), (1024, 4096, 64), (2048, 2048, 1088), (4104, 4104, 136), (4096, 4096, 8),
+          (8192, 4104, 520), (5000, 9000, 192), (2048, 4096, 4104), (1027, 4100, 4099), (4099, 1500, 2051), (520, 4099, 8200), (9001, 4111, 1029)]
+
+
 def mixed_case(M, N, K, dt, transpose, seed):
     g = generator(seed)
     a = torch.randn(*((K, M) if transpose else (M, K)), generator=g, device="cuda").to(DT[dt])
@@ -310,7 +316,7 @@ def test_mixed_product(gpu, M, N, K, dt, transpose):
 @GPU
 @pytest.mark.parametrize("transpose", [False, True])
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
-@pytest.mark.parametrize("M,N,K", MIXED + [(260, 4000, 3000), (2050, 2060, 1000)])
+@pytest.mark.parametrize("M,N,K", MIXED + LARGER)
 def test_mixed_product_of_integers_is_exact(gpu, M, N, K, dt, transpose):
     """Small integers times powers of two: all sums are exact, so every value is, whatever the
     order.  K takes each row of a stage, its last one too."""
@@ -420,7 +426,7 @@ def test_streams_and_graph(gpu):
                 qcp.int8_matmul_mixed(tall, *t, 64, transpose=True), qcp.int8_linear(x, w), qcp.int8_linear(x, b)]
     same = lambda p, q: torch.equal(p.view(torch.uint8), q.view(torch.uint8))  # noqa: E731
     lib = qcp.library()
-    assert lib.qcp_int8_matmul_work(64, 64, 9000) > 0 and lib.qcp_int8_mixed_work(64, 64, 6000) > 0
+    assert lib.qcp_int8_matmul_work(64, 64, 9000) > 0 and lib.qcp_int8_mixed_work(64, 64, 6000, 1, 1) > 0
     want = [t.clone() for t in chain()]
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -777,9 +783,13 @@ def test_rows_below_the_bound_have_no_slices(lib):
 
 def test_c_entry_of_the_mixed_product_refuses(lib):
     work = lib.qcp_int8_mixed_work
-    need = work(64, 64, 9000)
-    assert need > 0 and work(4096, 4096, 28672) == 0 and work(64, 64, 200) == 0 and work(0, 64, 9000) == work(64, 64, 0) == 0
-    assert work(-1, 64, 8192) == work(64, 1 << 40, 8192) == -1
+    need = work(64, 64, 9000, 0, 1)
+    assert need > 0 and need % (4 * 64 * 64) == 0
+    assert work(4096, 4096, 28672, 0, 1) == work(64, 64, 200, 0, 1) == work(0, 64, 9000, 0, 1) == work(64, 64, 0, 1, 1) == 0
+    assert work(-1, 64, 8192, 0, 1) == work(64, 1 << 40, 8192, 0, 1) == work(64, 64, 64, 2, 1) == work(64, 64, 64, 0, 2) == -1
+    copied = work(4096, 4096, 4100, 0, 0)                                # a's rows to 16 bytes: 4104 elements each
+    assert copied == 4096 * 4104 * 2 and work(4096, 4096, 4100, 0, 1) == copied and work(4096, 4096, 4096, 0, 1) == 0
+    assert work(50257, 4096, 8192, 1, 0) == 0                            # more than 256 MB is not copied
 
     def mul(a=A, at=2, lda=9000, t=0, x=A + S, s=A + 2 * S, M=64, N=64, K=9000, c=A + 3 * S, ct=2, ldc=64, w=A + 4 * S, n=need):
         return lib.int8_matmul_mixed(a, at, lda, t, x, s, M, N, K, c, ct, ldc, w, n, None)
