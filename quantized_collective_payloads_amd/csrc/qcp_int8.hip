@@ -9,6 +9,10 @@
 // The scale has to be known before the first code, so a team of lanes (16, a wave, or a
 // work-group) keeps a whole row in registers: x is read once.  A piece is 16 bytes of x:
 // 8 values of 16 bits or 4 of 32, whose codes are 8 or 4 consecutive bytes.
+//
+// Bound: HBM, 3 bytes per 16-bit value each way.  8192 x 28672 bf16: quantize 114 to 122 us (6.2
+// to 5.8 TB/s), dequantize 100 (7.0); 28672 x 8192 107 us; a copy runs at 5.1 TB/s.  x is read past
+// the caches (ordinary loads: 126 and 125 us); the codes stay there for the product.
 #include <algorithm>
 
 #include "qcp_int8.h"

@@ -9,6 +9,12 @@
 // reads 4 columns of 8 rows, decodes them (a conversion, a product with the row's scale and
 // half a rounding a code), and has 8 k of each column, 16 bytes to write to LDS; of a 16-bit
 // matrix the same with byte moves.  Both operands then lie in LDS with k along the rows.
+// Where a's rows are aligned (or it is large, and a copy with aligned rows is cheap), larger
+// products take the form below instead, which leaves the transposition to reads of LDS.
+//
+// Bound, of this form: the latency of a stage's load, decode, write and read where there are few
+// tiles (77 x 520, K = 1033 11 us, the smallest 5 to 6), and the decoding beside few products in
+// small tiles.
 #include <algorithm>
 
 #include "qcp_matmul.h"
