@@ -364,7 +364,8 @@ int64_t qcp_int8_matmul_work(int64_t M, int64_t N, int64_t K);
  *   w_codes, w_scales   the payload of W, N rows of K codes
  *   y          M x N of type xt, rows ldy apart
  * Where qcp_int8_linear_rows_fit(M, N, K) is 0 (more than 8 rows, rows too long for a
- * work-group to hold, or a product that is as quick in two launches), QCP_EUNSUPPORTED.
+ * work-group to hold, or a product that is as quick in two launches), QCP_EUNSUPPORTED;
+ * that function is host only.
  */
 int int8_linear_rows(const void *x, int xt, int64_t M, int64_t K, int64_t ldx, const uint8_t *w_codes,
                      const float *w_scales, int64_t N, void *y, int64_t ldy, void *stream);

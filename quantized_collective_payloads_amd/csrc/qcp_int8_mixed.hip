@@ -721,9 +721,10 @@ constexpr int64_t kMostCopied = (int64_t)256 << 20;
 Choice choose(int64_t M, int64_t N, int64_t K, bool transpose, bool aligned, bool scratch) {
     Choice best = {0, 1, false, 0, 0};
     int64_t least = INT64_MAX;
-    const int64_t width = (transpose ? M : K), wide = (width + 7) / 8 * 8, copied = 2 * wide * (transpose ? K : M);
+    const int64_t width = transpose ? M : K, rows = transpose ? K : M, wide = (width + 7) / 8 * 8;
     aligned = aligned && width % 8 == 0 && wide <= direct::kMaxLd;
-    const bool copy = !aligned && scratch && K > 0 && wide <= direct::kMaxLd && copied <= kMostCopied;
+    const bool copy = !aligned && scratch && K > 0 && wide <= direct::kMaxLd && rows <= kMostCopied / (2 * wide);
+    const int64_t copied = copy ? 2 * wide * rows : 0;
     for (int f = 0; f <= kDirect256; f++) {
         if (f >= kDirect128 ? !aligned && !copy : aligned && f == kPlain256) continue;
         const Form &m = kForms[f];

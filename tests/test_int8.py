@@ -789,6 +789,7 @@ def test_c_entry_of_the_mixed_product_refuses(lib):
     assert work(-1, 64, 8192, 0, 1) == work(64, 1 << 40, 8192, 0, 1) == work(64, 64, 64, 2, 1) == work(64, 64, 64, 0, 2) == -1
     copied = work(4096, 4096, 4100, 0, 0)                                # a's rows to 16 bytes: 4104 elements each
     assert copied == 4096 * 4104 * 2 and work(4096, 4096, 4100, 0, 1) == copied and work(4096, 4096, 4096, 0, 1) == 0
+    assert work(1 << 36, 64, 1 << 36, 0, 0) >= -1 and work(1 << 36, 64, 1 << 36, 1, 0) >= -1
     assert work(50257, 4096, 8192, 1, 0) == 0                            # more than 256 MB is not copied
 
     def mul(a=A, at=2, lda=9000, t=0, x=A + S, s=A + 2 * S, M=64, N=64, K=9000, c=A + 3 * S, ct=2, ldc=64, w=A + 4 * S, n=need):
