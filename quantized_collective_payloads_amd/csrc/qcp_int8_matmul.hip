@@ -428,7 +428,8 @@ hipError_t run_rows(const uint8_t *a, const float *as, const uint8_t *b, const f
 // Bound: reading W once; what a launch of its own for Q(x) takes, 2.6 us of the GPU and 6 of the
 // host, is as much as a small product.  Every work-group makes Q(x) for itself, in LDS: a team
 // of its lanes keeps a row in registers, V pieces a lane, as the quantize does and with its
-// results.  Its first loads of W go out before.
+// results.  Its first loads of W go out before (those of two steps: 1 x 4096, K = 4096 9.2 us from HBM and
+// 9.8, 1 x 14336, K = 4096 19.1 and 17.9).
 //
 // LDS holds a row's pieces of 16 bytes in the order piece ^ (row % 8), so that the reads of a
 // piece of 8 rows touch different banks.
@@ -537,7 +538,9 @@ hipError_t few_rows(const void *x, int64_t ldx, int64_t M, int64_t K, const uint
     const int64_t granules = 2 * stages, teams = M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : 8;
     const int64_t each = (granules * 8 + kFewThreads / teams - 1) / (kFewThreads / teams);   // pieces a lane
     if (each <= 1) return run_few<XT, 1>(x, ldx, M, K, b, bs, N, granules, y, ldy, st);
+    if (each <= 2) return run_few<XT, 2>(x, ldx, M, K, b, bs, N, granules, y, ldy, st);
     if (each <= 4) return run_few<XT, 4>(x, ldx, M, K, b, bs, N, granules, y, ldy, st);
+    if (each <= 8) return run_few<XT, 8>(x, ldx, M, K, b, bs, N, granules, y, ldy, st);
     if (each <= 16) return run_few<XT, 16>(x, ldx, M, K, b, bs, N, granules, y, ldy, st);
     return hipErrorInvalidValue;
 }
