@@ -59,9 +59,9 @@ template <int TM_, int TN_, int KS_, int WM_, int WN_, int AHEAD_, int TEAMS_> s
     }
 };
 
-// The stages of one slice of k of one tile.  TRANS: a is given as [K, M].
-constexpr int64_t kJoinRows = 32768;                         // of work-groups of the join
+constexpr int64_t kJoinRows = 32768;                         // rows of work-groups, of the kernels that have one for each row
 
+// The stages of one slice of k of one tile.  TRANS: a is given as [K, M].
 template <class G, int AT, bool TRANS, int CT, bool SLICED>
 __global__ __launch_bounds__(G::threads * G::TEAMS, 2) void k_int8_mixed(
     const uint16_t *__restrict__ a, int64_t lda, const uint8_t *__restrict__ codes, const float *__restrict__ scales,
