@@ -320,9 +320,9 @@ __global__ __launch_bounds__(G::threads * G::TEAMS, 2) void k_int8_mixed(
 // tiles of 256 that is 1% the slower).
 //
 // Bound: the power that the matrix cores draw on normal values: 8192 x 8192, K = 4096 takes 460 us
-// (1.2 PFLOP/s, the clock at 1.8 GHz) and on zeros 320 (1.7 PFLOP/s, 2.4 GHz); in cycles the cores are
-// busy 63% of the time, LDS 35%.  4096 x 4096, K = 4096 119 us; 14336 x 4096, K = 2048 to fp32 245;
-// 2048 x 2048, K = 2048 in tiles of 128 26.
+// (1.2 PFLOP/s, the clock at 1.9 GHz; the cores are busy in 60% of the cycles, LDS in 33%) and on
+// zeros 320 to 334 (1.7 PFLOP/s, 2.4 GHz).  4096 x 4096, K = 4096 119 to 124 us; 14336 x 4096,
+// K = 2048 to fp32 245; 2048 x 2048, K = 2048 in tiles of 128 28.
 //
 // Pieces of 16 bytes lie in LDS in an order that spreads what a read touches in a cycle over all
 // banks: of a row by row, piece ^ (row / 2 % 8); of a transposed, piece ^ 4 (row % 4); of the
