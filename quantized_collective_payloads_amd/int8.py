@@ -206,6 +206,43 @@ def _backward(index, dy, payload, rows, cols, transpose, dtype):
     return c if c.dtype is dtype else c.to(dtype)
 
 
+# Autograd accumulates a leaf's gradients on the stream on which a graph first reached the leaf,
+# for as long as a graph that reaches it lives.  Where that is the default stream, a backward pass
+# in a capture makes the default stream wait for the capture, which no capture allows and the
+# process may not survive.  So the layer notes the stream at the leaves that it sees, directly or
+# behind up to two casts and views (1.5 us a call of 67 and more), and its backward pass refuses such a capture.
+_FIRST_STREAM = "int8_linear: stream of the first graph"
+_Leaf = torch._C._functions.AccumulateGrad
+
+
+def _leaves(node):
+    """What autograd keeps of each leaf next to a node while a graph that reaches the leaf lives."""
+    found = []
+    for n, _ in node.next_functions:
+        for _ in range(3):
+            if type(n) is _Leaf:
+                found.append(n)
+            up = () if n is None else n.next_functions
+            if len(up) != 1:
+                break
+            n = up[0][0]
+    return found
+
+
+def _raw_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index) if index >= 0 else -1
+
+
+def _captured(index):
+    return index >= 0 and torch.cuda.is_current_stream_capturing()
+
+
+def _refuse_leaves_of_the_default_stream(node, index):
+    if _captured(index) and any(n.metadata.get(_FIRST_STREAM) == 0 for n in _leaves(node)):
+        raise RuntimeError("int8_linear: a backward pass is captured while a graph of the same leaves, recorded on the "
+                           "default stream, lives: free its outputs first, or record it on another stream")
+
+
 class _Linear(torch.autograd.Function):
     """y = Q(x) Q(w)^T.  The payload of x, which the forward product needs, is also all that
     is kept of x: 8 bits a value.  The backward products read it and that of w as they
@@ -228,6 +265,7 @@ class _Linear(torch.autograd.Function):
         qx, qw = ctx.saved_tensors
         T, I, O = ctx.sizes
         index, dx, dw = dy.get_device(), None, None
+        _refuse_leaves_of_the_default_stream(ctx, index)
         if qw is not None:
             dx = _backward(index, dy, _at(qw, O, I), O, I, False, ctx.kinds[0])
         if qx is not None:
@@ -250,6 +288,7 @@ class _FrozenLinear(torch.autograd.Function):
     def backward(ctx, dy):
         codes, scales = ctx.saved_tensors
         I, O = ctx.sizes
+        _refuse_leaves_of_the_default_stream(ctx, dy.get_device())
         dx = _backward(dy.get_device(), dy, (codes.data_ptr(), scales.data_ptr()), O, I, False, dy.dtype)
         return dx, None, None
 
@@ -264,7 +303,8 @@ def int8_linear(x: torch.Tensor, weight) -> torch.Tensor:
     Differentiable in x and in a weight tensor, backwards, with the rounding passed
     straight through: of x only the 8-bit payload is kept, and the backward products read it
     (and the weight's) in the gradient's type.  A forward-mode tangent raises
-    NotImplementedError."""
+    NotImplementedError; a backward pass that is captured into a graph while autograd still
+    holds a graph of the same leaves from the default stream raises RuntimeError."""
     frozen = isinstance(weight, (tuple, list))
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x: expected a torch.Tensor with at least one dimension")
@@ -293,6 +333,10 @@ def int8_linear(x: torch.Tensor, weight) -> torch.Tensor:
     # autograd to refuse in either mode
     if torch.is_grad_enabled() or any(unpack_dual(t).tangent is not None for t in (x2, *parts)):
         y = (_FrozenLinear if frozen else _Linear).apply(x2, *parts)
+        if y.requires_grad:
+            stream = _raw_stream(y.get_device())
+            for n in _leaves(y.grad_fn):
+                n.metadata.setdefault(_FIRST_STREAM, stream)
     else:
         index = x2.get_device()
         if frozen:

@@ -699,6 +699,30 @@ def test_linear_captured_in_a_graph(gpu):
         assert all(torch.equal(a, b) for a, b in zip(got, step())), k
 
 
+@GPU
+def test_linear_refuses_a_captured_backward_beside_a_living_graph_on_the_gpu(gpu):
+    """The refusal leaves the capture and the leaves usable: without the living graph the same
+    capture replays the eager step's gradients."""
+    x, w = values(90, 300, "bf16", 1).requires_grad_(), values(140, 300, "bf16", 2).requires_grad_()
+    dy = values(90, 140, "bf16", 3)
+    alive = qcp.int8_linear(x, w)
+    want = torch.autograd.grad(alive, (x, w), dy)
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="default stream, lives"):
+        with torch.cuda.graph(graph):
+            torch.autograd.grad(qcp.int8_linear(x, w), (x, w), dy)
+    del alive, graph
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = torch.autograd.grad(qcp.int8_linear(x, w), (x, w), dy)
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 # ------------------------------------------------------------------ refusals (CPU)
 
 OK, EINVAL, EALIGN, EUNSUP = 0, -1, -2, -3
@@ -883,6 +907,33 @@ def test_linear_refuses_forward_mode_tangents(layer_on_cpu, grad, which):
                     qcp.int8_linear(v, payload)
         assert qcp.int8_linear(x, w).shape == (3, 4)
     assert qcp.int8_linear(x, payload).shape == (3, 4)
+
+
+@pytest.mark.parametrize("kind", ["tensor", "cast", "frozen"])
+@pytest.mark.parametrize("stream,refused", [(0, True), (7, False)])
+def test_linear_refuses_a_captured_backward_beside_a_living_graph(layer_on_cpu, monkeypatch, kind, stream, refused):
+    from quantized_collective_payloads_amd import int8
+    streams = {"now": stream}
+    monkeypatch.setattr(int8, "_raw_stream", lambda index: streams["now"])
+    monkeypatch.setattr(int8, "_captured", lambda index: streams["now"] == 9)
+    w = torch.ones(4, 32, requires_grad=True)
+    payload = torch.zeros(4, 128, dtype=torch.uint8), torch.ones(4)
+
+    def layer(x, on):
+        streams["now"] = on
+        return qcp.int8_linear(x, payload if kind == "frozen" else w.to(torch.bfloat16) if kind == "cast" else w)
+    for shape in ((6, 32), (2, 3, 32)):
+        for grad in (True, False) if kind != "frozen" else (True,):
+            x = torch.ones(shape, dtype=torch.bfloat16, requires_grad=grad)
+            alive = layer(x, stream)
+            y = layer(x, 9)
+            if refused:
+                with pytest.raises(RuntimeError, match="default stream, lives"):
+                    y.sum().backward()
+            else:
+                y.sum().backward()
+            del alive, y
+            layer(x, 9).sum().backward()
 
 
 EMPTY = [(2, 3, 0), (0,), (3, 0), (0, 3, 0), (0, 0), (2, 0, 64), (0, 64), (64,), (2, 1, 3, 64)]
