@@ -432,7 +432,7 @@ __global__ __launch_bounds__(G::threads, 2) void k_int8_mixed_direct(
             const uint32_t row = min(32 * wave + 8 * i + (lane >> 3), m_rows - 1);
             const uint32_t piece = (lane & 7) ^ (lane >> 4) ^ (4 * (i & 1));
             copy_to_lds(to + wave * 4096 + i * 1024, row * (uint32_t)lda * 2 + piece * 16,
-                        buffer_of(a + m0 * lda, (uint64_t)((m_rows - 1) * lda + width) * 2), (uint32_t)k_next * 2);
+                        buffer_of(a + m0 * lda + k_next, (uint64_t)((m_rows - 1) * lda + width - k_next) * 2), 0);
         }
     };
     auto copied = [&]() __attribute__((always_inline)) {

@@ -111,7 +111,9 @@ __device__ __forceinline__ void store_fragment(const f32x16_t &v, void *c, int64
 // compiler knows what it holds.  The compiler does not count wait states into an asm
 // statement: the s_nop holds the five that a scalar register needs between a vector
 // instruction that writes it (v_readlane, which restores a spilled one) and a memory
-// instruction that reads it, and the one that m0 needs.
+// instruction that reads it, and the one that m0 needs.  The range check, which reads zeros
+// past the end of the buffer, is relied on for voff alone: with a soff other than 0 their sum
+// has to end within the buffer by itself.
 __device__ __forceinline__ void copy_to_lds(uint32_t lds, uint32_t voff, i32x4_t rsrc, uint32_t soff) {
     asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                  :
