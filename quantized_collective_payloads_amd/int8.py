@@ -19,6 +19,7 @@ from .mxfp4 import _matrix, _pad, _result, _same_gpu
 _u8, _f32 = torch.uint8, torch.float32
 _HALF = (torch.float16, torch.bfloat16)
 _UNSLICED = 63 * 128              # slices of K begin at 64 stages of 128
+_FARTHEST = 1 << 23               # elements between the rows that the mixed product takes
 
 
 def _payload(codes, scales, what: str):
@@ -134,8 +135,9 @@ def int8_matmul_mixed(a: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
                       transpose: bool = False, dtype=None, out=None):
     """A X for a 2-D fp16 or bf16 tensor A [M, K] (with `transpose`, `a` is [K, M] and A its
     transpose) and the payload of X [K, cols], read in a's type: [M, cols] in `dtype`,
-    which is a's (the default) or float32, accumulated in fp32.  Rows of `a` may lie any
-    distance apart, and a transposed view is read where it is; other strides are copied."""
+    which is a's (the default) or float32, accumulated in fp32.  Rows of `a` up to 2^23 elements
+    apart, and those of a transposed view, are read where they are; other strides, and rows
+    that are farther apart or longer, are copied.  cols <= 2^24."""
     if type(a) is not torch.Tensor or a.dim() != 2 or a.dtype not in _HALF:
         _matrix(a, "a")
         if a.dtype not in _HALF:
@@ -156,9 +158,14 @@ def int8_matmul_mixed(a: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
 
 
 def _mixed(index, a, codes, scales, M, N, K, transpose, c):
-    if not a.is_contiguous() and a.stride(0) == 1 and a.stride(1) >= a.shape[0]:
+    if not a.is_contiguous() and a.stride(0) == 1 and a.shape[0] <= a.stride(1) <= _FARTHEST:
         a, transpose = a.t(), not transpose
     a, lda = _rows_of(a)
+    if lda > _FARTHEST:
+        # packed, along the dimension that is short enough (both are longer in no tensor)
+        if a.shape[1] > _FARTHEST:
+            a, transpose = a.t(), not transpose
+        a, lda = a.contiguous(), a.shape[1]
     first, transpose = a.data_ptr(), 1 if transpose else 0
     t, at, size = _scratch("qcp_int8_mixed_work", c, M, N, K, transpose,
                            1 if first % 16 == 0 and lda % 8 == 0 and lda <= 1 << 22 else 0)
