@@ -215,25 +215,48 @@ def _backward(index, dy, payload, rows, cols, transpose, dtype):
 
 # Autograd accumulates a leaf's gradients on the stream on which a graph first reached the leaf,
 # for as long as a graph that reaches it lives.  Where that is the default stream, a backward pass
-# in a capture makes the default stream wait for the capture, which no capture allows and the
-# process may not survive.  So the layer notes the stream at the leaves that it sees, directly or
-# behind up to two casts and views (1.5 us a call of 67 and more), and its backward pass refuses such a capture.
+# in a capture that gives the leaf a gradient makes the default stream wait for the capture, which
+# no capture allows and the process may not survive.  Torch does not tell a leaf's stream.  So the
+# layer notes its own stream at the leaves next to it and at those behind up to _BEHIND operators
+# with one input (0.7 us of a forward call of 25), and its backward pass refuses such a capture for
+# every noted leaf before it.  A leaf that only other operators have reached is not noted.
 _FIRST_STREAM = "int8_linear: stream of the first graph"
+_BEHIND = 8
 _Leaf = torch._C._functions.AccumulateGrad
 
 
-def _leaves(node):
-    """What autograd keeps of each leaf next to a node while a graph that reaches the leaf lives."""
+def _near_leaves(node):
+    """What autograd keeps of each leaf near a node while a graph that reaches the leaf lives."""
     found = []
     for n, _ in node.next_functions:
-        for _ in range(3):
+        for _ in range(1 + _BEHIND):
+            if n is None:
+                break
             if type(n) is _Leaf:
                 found.append(n)
-            up = () if n is None else n.next_functions
-            if len(up) != 1:
                 break
-            n = up[0][0]
+            up = [m for m, _ in n.next_functions if m is not None]
+            n = up[0] if len(up) == 1 else None
     return found
+
+
+def _leaves(node):
+    """The same of all leaves before a node."""
+    found, seen, todo = [], set(), [node]
+    while todo:
+        for n, _ in todo.pop().next_functions:
+            if n is not None and n not in seen:
+                seen.add(n)
+                (found if type(n) is _Leaf else todo).append(n)
+    return found
+
+
+def _receives(leaf):
+    """Whether the backward pass that runs gives a leaf a gradient."""
+    try:
+        return torch._C._will_engine_execute_node(leaf)
+    except RuntimeError:                           # what autograd.grad says of the leaves that it was asked for
+        return True
 
 
 def _raw_stream(index):
@@ -245,7 +268,7 @@ def _captured(index):
 
 
 def _refuse_leaves_of_the_default_stream(node, index):
-    if _captured(index) and any(n.metadata.get(_FIRST_STREAM) == 0 for n in _leaves(node)):
+    if _captured(index) and any(n.metadata.get(_FIRST_STREAM) == 0 and _receives(n) for n in _leaves(node)):
         raise RuntimeError("int8_linear: a backward pass is captured while a graph of the same leaves, recorded on the "
                            "default stream, lives: free its outputs first, or record it on another stream")
 
@@ -310,8 +333,11 @@ def int8_linear(x: torch.Tensor, weight) -> torch.Tensor:
     Differentiable in x and in a weight tensor, backwards, with the rounding passed
     straight through: of x only the 8-bit payload is kept, and the backward products read it
     (and the weight's) in the gradient's type.  A forward-mode tangent raises
-    NotImplementedError; a backward pass that is captured into a graph while autograd still
-    holds a graph of the same leaves from the default stream raises RuntimeError."""
+    NotImplementedError.  A captured backward pass that gives a gradient to a leaf of which
+    autograd still holds a graph that the layer recorded on the default stream raises
+    RuntimeError, where the layer saw the leaf directly or behind up to 8 operators with one
+    input; torch would end the process there, as it does for its own operators, and for leaves
+    that the layer has not seen."""
     frozen = isinstance(weight, (tuple, list))
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x: expected a torch.Tensor with at least one dimension")
@@ -342,7 +368,7 @@ def int8_linear(x: torch.Tensor, weight) -> torch.Tensor:
         y = (_FrozenLinear if frozen else _Linear).apply(x2, *parts)
         if y.requires_grad:
             stream = _raw_stream(y.get_device())
-            for n in _leaves(y.grad_fn):
+            for n in _near_leaves(y.grad_fn):
                 n.metadata.setdefault(_FIRST_STREAM, stream)
     else:
         index = x2.get_device()
