@@ -45,9 +45,9 @@ def _payload(codes, scales, what: str):
     raise ValueError(f"{what}codes: not a payload")
 
 
-def _columns(P: int, cols: int):
+def _columns(P: int, cols: int, what: str = ""):
     if cols < 0 or _pad(cols) != P:
-        raise ValueError(f"codes: rows of {P} values for {cols} columns")
+        raise ValueError(f"{what}codes: rows of {P} values for {cols} columns")
 
 
 def _rows_of(x):
@@ -328,7 +328,9 @@ def int8_linear(x: torch.Tensor, weight) -> torch.Tensor:
     rounded to INT8 by tokens and the weight by output channels.
 
     weight   a 2-D fp16/bf16/fp32 tensor, quantized at every call; or a payload (codes,
-             scales) of int8_quantize, made once (serving, frozen weights)
+             scales) of int8_quantize, made once (serving, frozen weights), or (codes,
+             scales, in): a payload's rows are whole 128s, and only where it is told does
+             the layer know an x of another length within the same 128
 
     Differentiable in x and in a weight tensor, backwards, with the rounding passed
     straight through: of x only the 8-bit payload is kept, and the backward products read it
@@ -342,12 +344,16 @@ def int8_linear(x: torch.Tensor, weight) -> torch.Tensor:
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x: expected a torch.Tensor with at least one dimension")
     if frozen:
-        if len(weight) != 2:
-            raise ValueError("weight: expected a tensor or a payload (codes, scales)")
-        O, P, _ = _payload(*weight, "weight ")
+        if len(weight) not in (2, 3) or (len(weight) == 3 and not isinstance(weight[2], int)):
+            raise ValueError("weight: expected a tensor or a payload (codes, scales) or (codes, scales, in)")
+        parts = tuple(weight[:2])
+        O, P, _ = _payload(*parts, "weight ")
+        if len(weight) == 3:
+            _columns(P, weight[2], "weight ")
+            if x.shape[-1] != weight[2]:
+                raise ValueError(f"x: last dimension {x.shape[-1]}, weight's {weight[2]}")
         if P != _pad(x.shape[-1]):
             raise ValueError(f"x: last dimension {x.shape[-1]}, weight rows of {P} values")
-        parts = tuple(weight)
     else:
         _matrix(weight, "weight")
         O = weight.shape[0]
