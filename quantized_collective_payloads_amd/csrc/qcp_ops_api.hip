@@ -80,6 +80,10 @@ bool int8_payload(int64_t lines, int64_t n, int64_t *pad) { return mx_payload(li
 constexpr int64_t kInt8MaxK = 130944;
 // the mixed product: 128 rows of the payload and 256 of a, in bytes, are 32-bit offsets
 constexpr int64_t kMixedMaxN = (int64_t)1 << 24, kMixedMaxLd = (int64_t)1 << 23;
+// and its tiles of C, 256 x 256, a launch's work-groups
+bool mixed_tiles(int64_t M, int64_t N) {
+    return N <= 0 || (M + 255) / 256 <= qcp::kMaxGroups / 2 / ((N + 255) / 256);
+}
 
 // The arguments that adamw_step checks, by their names there
 struct AdamwArgs {
@@ -413,7 +417,7 @@ int int8_matmul_mixed(const void *a, int at, int64_t lda, int32_t transpose, con
     if (rc != QCP_OK) return rc;
     if (M == 0 || N == 0) return QCP_OK;
     if (N > kMixedMaxN || lda > kMixedMaxLd || !int8_payload(K, N, &pad)) return QCP_EINVAL;
-    if ((M + 255) / 256 > qcp::kMaxGroups / 2 / ((N + 255) / 256)) return QCP_EINVAL;   // tiles of C
+    if (!mixed_tiles(M, N)) return QCP_EINVAL;
     if (!c || (K > 0 && (!a || !codes || !scales))) return QCP_EINVAL;
     const int64_t need = work ? qcp_int8_mixed_work(M, N, K, transpose, qcp::int8_mixed_aligned(a, lda) ? 1 : 0) : 0;
     if (work_bytes < need) return QCP_EINVAL;
@@ -432,7 +436,7 @@ int int8_matmul_mixed(const void *a, int at, int64_t lda, int32_t transpose, con
 int64_t qcp_int8_mixed_work(int64_t M, int64_t N, int64_t K, int32_t transpose, int32_t aligned) {
     if (M < 0 || N < 0 || K < 0 || M > kMaxElems || N > kMixedMaxN || K > kMaxElems) return -1;
     if ((transpose != 0 && transpose != 1) || (aligned != 0 && aligned != 1)) return -1;
-    if ((M + 255) / 256 > qcp::kMaxGroups / 2 / ((N + 256) / 256)) return -1;
+    if (!mixed_tiles(M, N)) return -1;
     return qcp::int8_mixed_work(M, N, K, transpose, aligned != 0);
 }
 

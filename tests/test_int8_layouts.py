@@ -85,3 +85,13 @@ def test_backward_through_outputs_that_were_stacked(gpu):  # noqa: F811
     one = torch.autograd.grad(qcp.int8_linear(x[5], w), w, dy[:, 5])[0]
     assert torch.equal(one, qcp.int8_matmul_mixed(dy[:, 5].contiguous(), *qcp.int8_quantize(x[5].detach()), I, transpose=True))
     assert torch.isfinite(dw).all()
+
+
+def test_scratch_memory_is_told_for_every_size_that_the_product_takes():
+    """Its own bound on the tiles of C was the smaller one where N is a multiple of 256."""
+    work = qcp.library().qcp_int8_mixed_work
+    most = (2 ** 24 - 1) // 2                      # tiles of 256
+    for N, rows in ((256, most), (255, most), (1, most), (512, most // 2), (1024, most // 4), (1 << 24, most // 65536)):
+        assert work(256 * rows, N, 64, 0, 1) >= 0, N
+        assert work(256 * rows + 1, N, 64, 0, 1) == -1, N
+    assert work(0, 0, 64, 0, 1) == work(1 << 31, 0, 64, 1, 0) == 0
