@@ -384,10 +384,11 @@ int qcp_int8_linear_rows_fit(int64_t M, int64_t N, int64_t K);
  *   work       null, or scratch memory on the device of at least qcp_int8_mixed_work(...)
  *              bytes, 16-byte aligned: for slices of a long K side by side, added up in a
  *              fixed order in a second launch, and for a copy of a large a whose rows are
- *              not aligned to 16 bytes (at most 84 and 256 MB).  The order of the sums,
+ *              not aligned to 16 bytes (at most 80 and 256 MiB).  The order of the sums,
  *              and with it their last bits, differs from the product without.
  * dx = dy W: a = dy, the payload of W [out, in].  dW = dy^T x: a = dy with transpose, the
- * payload of x [tokens, in], which is all that a layer keeps of its input.
+ * payload of x [tokens, in], which is all that a layer keeps of its input.  In fp16 a value
+ * of the payload above 65504 is an infinity, and small ones are subnormal.
  */
 int int8_matmul_mixed(const void *a, int at, int64_t lda, int32_t transpose, const uint8_t *codes,
                       const float *scales, int64_t M, int64_t N, int64_t K, void *c, int ct, int64_t ldc,

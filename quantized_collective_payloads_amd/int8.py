@@ -3,7 +3,8 @@ on the matrix cores, and a linear layer that keeps its input in 8 bits for the
 backward pass (int8_* of include/qcp.h).
 
 A payload of `rows` rows of n values is a pair (codes, scales): uint8 [rows, P] in
-two's complement, with P = n rounded up to whole 128s, and float32 [rows].
+two's complement, with P = n rounded up to whole 128s, and float32 [rows].  Both begin at
+16 bytes: rows of a larger payload at multiples of 4 are payloads themselves.
 
 As in mxfp4.py, each function first asks what every valid call answers with yes and
 goes through the checks that name the fault only where the answer is no.
@@ -275,9 +276,9 @@ def _refuse_leaves_of_the_default_stream(node, index):
 
 class _Linear(torch.autograd.Function):
     """y = Q(x) Q(w)^T.  The payload of x, which the forward product needs, is also all that
-    is kept of x: 8 bits a value.  The backward products read it and that of w as they
-    are: dx = dy Q(w), dw = dy^T Q(x), the gradients of the product with the rounding
-    passed straight through."""
+    is kept of x: 8 bits a value; that of w is kept for dx.  The backward products read
+    them in dy's type: dx = dy Q(w), dw = dy^T Q(x), the gradients of the product with the
+    rounding to INT8 passed straight through, up to a rounding of each value to 16 bits."""
 
     @staticmethod
     def forward(ctx, x, w):
@@ -332,14 +333,21 @@ def int8_linear(x: torch.Tensor, weight) -> torch.Tensor:
              scales, in): a payload's rows are whole 128s, and only where it is told does
              the layer know an x of another length within the same 128
 
-    Differentiable in x and in a weight tensor, backwards, with the rounding passed
-    straight through: of x only the 8-bit payload is kept, and the backward products read it
-    (and the weight's) in the gradient's type.  A forward-mode tangent raises
-    NotImplementedError.  A captured backward pass that gives a gradient to a leaf of which
-    autograd still holds a graph that the layer recorded on the default stream raises
-    RuntimeError, where the layer saw the leaf directly or behind up to 8 operators with one
-    input; torch would end the process there, as it does for its own operators, and for leaves
-    that the layer has not seen."""
+    in <= 130944.  Differentiable in x and in a weight tensor, backwards, with the rounding to
+    INT8 passed straight through.  The backward products read the payloads in the gradient's
+    type, code * scale rounded to it, where the forward product takes it as it is; under fp16,
+    weights above 65504 are infinite there.
+
+    What waits for the backward pass: of x its payload, in (whole 128s) + 4 bytes a token, if
+    the weight needs a gradient; of a weight tensor its payload, as much an output channel, if
+    x does.  A layer in 16 bits holds 2 in bytes a token and refers to its weight: with fewer
+    tokens than output channels this one holds more.
+
+    A forward-mode tangent raises NotImplementedError.  A captured backward pass raises
+    RuntimeError if it gives a gradient to a leaf of which autograd still holds a graph that
+    the layer recorded on the default stream, and if the layer saw the leaf directly or behind
+    up to 8 operators with one input.  Torch ends the process there, as it does under its own
+    operators, and for leaves that the layer has not seen."""
     frozen = isinstance(weight, (tuple, list))
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x: expected a torch.Tensor with at least one dimension")
