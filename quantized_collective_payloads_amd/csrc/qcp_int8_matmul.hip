@@ -594,10 +594,22 @@ int int8_matmul_slices(int64_t M, int64_t N, int64_t stages) {
     return (int)std::min<int64_t>(8, 256 / (rows * cols));
 }
 
-// Up to 8 rows that fit LDS, where the work that every work-group repeats takes no more than the
-// launch that it saves (us of the GPU in one launch and in two, warm: 1 x 14336, K = 4096 15.5
-// and 16.2; 1 x 4096, K = 4096 6.6 and 7.6; 8 x 4096, K = 4096 9.1 and 8.5, but 6 us less of the
-// host; 8 x 14336, K = 4096 24.7 and 18.3).
+// Up to 8 rows that fit LDS, while what every work-group repeats (M P codes, N / 16 times) takes
+// about what the launch does that it saves.  us in one launch and in two, in a graph with W in
+// the last cache, there from HBM, and called eagerly, where two are bound by the host:
+//   1 x 4096, K = 4096    6.6 and 7.6
+//   1 x 14336, K = 4096   15.5 and 16.2
+//   2 x 4096, K = 4096    6.3 and 7.2    8.6 and 9.5     6.1 and 12.2
+//   4 x 8192, K = 4096    9.4 and 10.7   12.2 and 12.6   9.0 and 11.6
+//   8 x 1024, K = 4096    7.1 and 7.8    8.6 and 8.6     7.2 and 11.5
+//   8 x 4096, K = 4096    8.5 and 8.4    10.9 and 9.9    8.3 and 11.6
+//   8 x 2048, K = 6144    9.8 and 9.5    13.4 and 11.1   9.7 and 12.2
+// beyond the bound on N:
+//   8 x 6144, K = 4096    12.1 and 11.9  13.3 and 12.7   11.9 and 12.3
+//   8 x 14336, K = 4096   22.9 and 18.3  25.1 and 19.0   22.4 and 17.8
+//   4 x 14336, K = 4096   17.6 and 17.2  19.0 and 17.9   17.2 and 16.9
+// So 8 rows at the bound give up a tenth (a fifth where K is longest) in a graph with W from HBM
+// for a quarter of an eager call.
 bool int8_linear_few(int64_t M, int64_t N, int64_t stages) {
     const int64_t teams = M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : 8, P = stages * 128;
     if (M < 1 || M > 8 || stages < 1 || teams * P > kFewBytes || (N + 15) / 16 > kMaxGroups / 2) return false;

@@ -319,10 +319,13 @@ __global__ __launch_bounds__(G::threads * G::TEAMS, 2) void k_int8_mixed(
 // just read, and the waves wait for those reads as well (1024 x 4096, K = 4096 46 us and 52; in
 // tiles of 256 that is 1% the slower).
 //
-// Bound: the power that the matrix cores draw on normal values: 8192 x 8192, K = 4096 takes 460 us
-// (1.2 PFLOP/s, the clock at 1.9 GHz; the cores are busy in 60% of the cycles, LDS in 33%) and on
-// zeros 320 to 334 (1.7 PFLOP/s, 2.4 GHz).  4096 x 4096, K = 4096 119 to 124 us; 14336 x 4096,
-// K = 2048 to fp32 245; 2048 x 2048, K = 2048 in tiles of 128 28.
+// Bound: the cycles in which the matrix cores wait, two fifths of them, and on normal values the
+// power that they draw, which takes the clock from 2.4 GHz to 1.9.  8192 x 8192, K = 4096 takes 460
+// us (1.2 PFLOP/s; the cores are busy in 60% of the cycles and LDS in 33%, the waves wait in 31% of
+// their time for a barrier or a count, and 80 of 142 vector instructions a wave and stage are the
+// decoding) and on zeros 320 to 334 (1.7 PFLOP/s).  4096 x 4096, K = 4096 119 to 124 us; 2048 x 4096,
+// K = 14336 in two slices 207 and 13 for the join; 14336 x 4096, K = 2048 to fp32 240 to 253, whose
+// 3.5 rounds of tiles take 4; 2048 x 2048, K = 2048 in tiles of 128 28 to 29.
 //
 // Pieces of 16 bytes lie in LDS in an order that spreads what a read touches in a cycle over all
 // banks: of a row by row, piece ^ (row / 2 % 8); of a transposed, piece ^ 4 (row % 4); of the
@@ -475,8 +478,9 @@ __global__ __launch_bounds__(G::threads, 2) void k_int8_mixed_direct(
     };
     using std::integral_constant;
     using zero = integral_constant<int, 0>;
-    // what lies past the end of K in the slot at `at`, `left` of whose rows exist, becomes zeros:
-    // a's values (of a row by row, `left` is a multiple of 8) and the scales
+    // what lies past the end of K in the slot at `at`, `left` of whose k exist, becomes zeros: a's
+    // values and the scales.  Of a row by row these are whole pieces of 8 k; where K ends inside
+    // one, the rows are the aligned copy's, which holds zeros from K to the end of that piece
     auto clear = [&](uint32_t at, uint32_t left) __attribute__((always_inline)) {
         typedef __attribute__((address_space(3))) u32x4_t lds_piece;
 #pragma unroll
