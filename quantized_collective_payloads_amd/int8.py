@@ -346,7 +346,7 @@ def int8_linear(x: torch.Tensor, weight) -> torch.Tensor:
     A forward-mode tangent raises NotImplementedError.  A captured backward pass raises
     RuntimeError if it gives a gradient to a leaf of which autograd still holds a graph that
     the layer recorded on the default stream, and if the layer saw the leaf directly or behind
-    up to 8 operators with one input.  Torch ends the process there, as it does under its own
+    up to 8 operators with one input.  Torch may end the process there, as under its own
     operators, and for leaves that the layer has not seen."""
     frozen = isinstance(weight, (tuple, list))
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
